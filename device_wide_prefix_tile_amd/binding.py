@@ -24,7 +24,11 @@ _DTYPES = {torch.int32: SCAN_I32, torch.uint32: SCAN_U32, torch.float32: SCAN_F3
 EXPORTS = ("scan_inclusive", "scan_exclusive", "segmented_scan", "compact", "scan_status_string",
            "scan_get_device_error", "scan_release_workspace", "scan_set_small_n_max",
            "scan_set_spin_limit", "scan_set_multi_tile_mode", "scan_copy_probe", "csr_row_offsets",
-           "radix_split", "scan_noalloc")
+           "radix_split", "scan_noalloc",
+           # dwpt_seq.h, bound in sequence.py
+           "embedding_lookup", "embedding_grad", "embedding_grad_workspace", "causal_conv1d", "causal_conv1d_grad",
+           "causal_conv1d_grad_workspace", "causal_conv1d_step", "selective_scan", "selective_scan_workspace",
+           "selective_scan_saved", "selective_scan_grad", "selective_scan_grad_workspace", "selective_scan_step")
 
 _lib = None
 

@@ -1,0 +1,1321 @@
+// Selective state-space scan: for every channel d and state n
+//   dt = softplus(delta + bias);  a = exp(dt A);  h = a h' + dt x B;
+//   y = (sum_n C h + D x) silu(z)
+// its gradient, and its form for single tokens.
+//
+// The recurrence is a scan of real affine maps h -> a h + b, as many as
+// rows x channels x states, that are made from far fewer inputs and never
+// leave the registers.  Per map: one exponential (a quarter-rate
+// instruction) and four multiplies or fused multiply-adds, against 1/16 of
+// the bytes of a row: the kernels are bound by the vector units, not by
+// memory.
+//
+// Layout.  A wavefront owns 16 channels; lane = 4 * channel + quarter, and a
+// lane holds S = ceil(states / 4) rounded up to 4, 8 or 16 neighbouring states
+// of its channel.  The sum over a channel's states is then S - 1 adds in the
+// lane and two DPP adds in its quad.  Rows are taken in tiles: the lanes load
+// 16-byte pieces of the tile's rows (the next tile's while this one is worked
+// on), turn them into (dt, dt x) pairs in LDS, B and C into 32-bit rows, and
+// walk the rows; results go back through LDS to the lanes that loaded the
+// inputs, which finish and store them as 16-byte pieces.  No wavefront waits
+// for another.
+//
+// Spans.  Where sequences and channels are too few to fill the chip, the rows
+// are cut into spans that are scanned at the same time: a first launch takes
+// every span from a zero state to its end (no C, no output) and keeps that
+// state E and the sum of dt, whose exponential is the product of the span's
+// factors; the second takes the states of the spans before it in the same
+// sequence, h = exp(A sum dt) h + E one after another, and scans its rows from
+// there.  This is the library's reduce-then-scan with its middle step folded
+// into the last one.
+//
+// Packed sequences are segments: a wavefront walks them one after another,
+// starting each from its initial state.
+#include "seq_common.hpp"
+
+namespace dwpt_seq {
+namespace {
+
+constexpr int kWaves = 4;             // wavefronts per workgroup
+constexpr int kWaveChannels = 16;     // channels per wavefront
+constexpr int kWgChannels = kWaves * kWaveChannels;
+constexpr uint32_t kMaxChannels = 1u << 20;
+constexpr uint32_t kEmptyStep = 32;   // workgroups per channel block that look for empty sequences
+
+// S states per lane: TT rows per tile, SUB rows whose factors the gradient keeps in registers
+// (SUB * S factors and as many products: 2 * 32 registers).
+template <int S>
+struct Cfg {
+    static constexpr int NP = 4 * S;  // states, padded
+    static constexpr int TT = S == 16 ? 16 : 32;
+    static constexpr int SUB = 32 / S;
+};
+
+int states_per_lane(uint32_t states) { return states <= 16 ? 4 : states <= 32 ? 8 : 16; }
+uint32_t tile_rows(int s) { return s == 16 ? 16 : 32; }
+
+// Rows cut into spans.  Sequences of one length: `per_seq` spans of `span_rows` rows for each (the
+// last one shorter); packed sequences: every span_rows rows, wherever sequences begin.
+struct Plan {
+    Sequences seqs;
+    uint32_t channels, states, groups, group_channels;
+    uint32_t blocks_per_group, blocks;  // workgroups along a group's channels, along all
+    uint32_t span_rows, per_seq, spans, tiles_per_span;
+
+    __device__ __forceinline__ void rows_of(uint32_t span, uint32_t& r0, uint32_t& r1) const
+    {
+        if (seqs.offsets) {
+            r0 = span * span_rows;
+            r1 = min(r0 + span_rows, seqs.rows);
+        } else {
+            const uint32_t s = span / per_seq, first = (span % per_seq) * span_rows;
+            r0 = s * seqs.len + first;
+            r1 = s * seqs.len + min(first + span_rows, seqs.len);
+        }
+    }
+    // The span that row r of the sequence that `span` meets lies in (r in a sequence of `span`).
+    __device__ __forceinline__ uint32_t span_of(uint32_t span, uint32_t r) const
+    {
+        if (seqs.offsets) return r / span_rows;
+        const uint32_t s = span / per_seq;
+        return s * per_seq + (r - s * seqs.len) / span_rows;
+    }
+};
+
+struct Inputs {
+    const void *x, *delta, *B, *C, *z;
+    int64_t x_stride, delta_stride, b_stride, c_stride, z_stride;
+    const float *A, *D, *delta_bias, *initial;
+    int softplus, vec, vec_bc;  // vec: 16-byte pieces of x, delta, z (and y ...); vec_bc: of B and C
+};
+
+// ------------------------------------------------------------ tiles
+// How the lanes share a tile of TT rows by 16 channels: `pieces` 16-byte pieces each.
+template <typename T, int TT>
+struct Tile {
+    static constexpr int V = 16 / sizeof(T);
+    static constexpr int LPR = kWaveChannels / V;  // lanes per row
+    static constexpr int RPL = 64 / LPR;           // rows per piece
+    static constexpr int PIECES = TT > RPL ? TT / RPL : 1;
+    using P = Pack<T, V>;
+
+    __device__ static __forceinline__ int row(int i, int lane) { return i * RPL + lane / LPR; }
+    __device__ static __forceinline__ int col(int lane) { return (lane % LPR) * V; }
+
+    // Rows [r0, r0 + len), channels [c0, c0 + nch) of p; zeros elsewhere.
+    __device__ static __forceinline__ void load(P (&out)[PIECES], const void* base, int64_t stride, uint32_t r0, int len,
+                                                uint32_t c0, int nch, int vec, int lane)
+    {
+        const T* p = static_cast<const T*>(base);
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+            const int r = row(i, lane), c = col(lane);
+            out[i] = zero_pack<T, V>();
+            if (r < len && c < nch) {
+                const T* q = p + (int64_t)(r0 + r) * stride + c0 + c;
+                if (vec) {
+                    out[i] = load_pack<T, V>(q);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < V; ++j)
+                        if (c + j < nch) out[i].v[j] = q[j];
+                }
+            }
+        }
+    }
+    __device__ static __forceinline__ void store(void* base, int64_t stride, uint32_t r0, int len, uint32_t c0, int nch,
+                                                 int vec, int lane, int i, const float (&f)[V])
+    {
+        const int r = row(i, lane), c = col(lane);
+        if (r >= len || c >= nch) return;
+        T* q = static_cast<T*>(base) + (int64_t)(r0 + r) * stride + c0 + c;
+        const P p = pack<T, V>(f);
+        if (vec) {
+            *reinterpret_cast<P*>(q) = p;
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (c + j < nch) q[j] = p.v[j];
+        }
+    }
+};
+
+// A tile of TT rows by NP states of B or C, shared by LANES lanes.
+template <typename T, int TT, int NP, int LANES>
+struct StateTile {
+    static constexpr int V = 16 / sizeof(T);
+    static constexpr int LPR = NP / V;
+    static constexpr int TOTAL = TT * LPR;  // pieces of the tile
+    static constexpr int PIECES = (TOTAL + LANES - 1) / LANES;
+    using P = Pack<T, V>;
+
+    __device__ static __forceinline__ void load(P (&out)[PIECES], const void* base, int64_t stride, uint32_t r0, int len,
+                                                uint32_t at, int states, int vec, int lane)
+    {
+        const T* p = static_cast<const T*>(base);
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+            const int k = i * LANES + lane, r = k / LPR, n = (k % LPR) * V;
+            out[i] = zero_pack<T, V>();
+            if (k < TOTAL && r < len && n < states) {
+                const T* q = p + (int64_t)(r0 + r) * stride + at + n;
+                if (vec) {
+                    out[i] = load_pack<T, V>(q);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < V; ++j)
+                        if (n + j < states) out[i].v[j] = q[j];
+                }
+            }
+        }
+    }
+    __device__ static __forceinline__ void put(float* lds, const P (&in)[PIECES], int lane)
+    {
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+            const int k = i * LANES + lane;
+            if (TOTAL % LANES && k >= TOTAL) continue;
+            float f[V];
+            unpack(in[i], f);
+#pragma unroll
+            for (int j = 0; j < V; j += 4) *reinterpret_cast<f32x4*>(lds + k * V + j) = f32x4{f[j], f[j + 1], f[j + 2], f[j + 3]};
+        }
+    }
+};
+
+template <int S>
+__device__ __forceinline__ void lds_states(const float* p, float (&f)[S])
+{
+#pragma unroll
+    for (int s = 0; s < S; s += 4) {
+        const f32x4 v = *reinterpret_cast<const f32x4*>(p + s);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[s + j] = v[j];
+    }
+}
+
+// The four lanes of a quad hold four values each; lane q receives the sum over the quad of value q.
+__device__ __forceinline__ float quad_transpose_sum(const float (&v)[4], int q)
+{
+    const bool odd = q & 1, high = q & 2;
+    float a = odd ? v[1] : v[0], b = odd ? v[3] : v[2];
+    a += dpp<kQuadXor1>(odd ? v[0] : v[1]);
+    b += dpp<kQuadXor1>(odd ? v[2] : v[3]);
+    const float keep = high ? b : a, give = high ? a : b;
+    return keep + dpp<kQuadXor2>(give);
+}
+
+// Where a wavefront stands: its channels and its lane's part of them.
+struct Place {
+    int lane, w, d, q;       // channel and quarter of the lane
+    uint32_t group, c0;      // first channel of the wavefront
+    int nch;                 // channels of the wavefront (0: none)
+    __device__ __forceinline__ Place(const Plan& p, uint32_t block)
+    {
+        lane = threadIdx.x & 63;
+        w = uniform(threadIdx.x >> 6);
+        d = lane >> 2;
+        q = lane & 3;
+        group = block / p.blocks_per_group;
+        const uint32_t first = (block % p.blocks_per_group) * kWgChannels + w * kWaveChannels;
+        c0 = group * p.group_channels + first;
+        nch = first < p.group_channels ? (int)min(p.group_channels - first, (uint32_t)kWaveChannels) : 0;
+    }
+};
+
+// The lane's S states of the (channels x states) array p at channel c0 + d; zeros where padded.
+template <int S>
+__device__ __forceinline__ void load_states(const float* __restrict__ p, const Plan& pl, const Place& me, float (&f)[S],
+                                            float scale = 1.0f)
+{
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        const uint32_t n = me.q * S + s;
+        f[s] = me.d < me.nch && n < pl.states ? p[(size_t)(me.c0 + me.d) * pl.states + n] * scale : 0.0f;
+    }
+}
+template <int S>
+__device__ __forceinline__ void store_states(float* __restrict__ p, const Plan& pl, const Place& me, const float (&f)[S])
+{
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        const uint32_t n = me.q * S + s;
+        if (me.d < me.nch && n < pl.states) p[(size_t)(me.c0 + me.d) * pl.states + n] = f[s];
+    }
+}
+// The same in the workspace, padded to NP states per channel: [index][channels][NP].
+template <int S>
+__device__ __forceinline__ void load_padded(const float* __restrict__ p, const Plan& pl, const Place& me, size_t index,
+                                            float (&f)[S])
+{
+    if (me.d < me.nch) {
+        lds_states<S>(p + (index * pl.channels + me.c0 + me.d) * (4 * S) + me.q * S, f);
+    } else {
+#pragma unroll
+        for (int s = 0; s < S; ++s) f[s] = 0.0f;
+    }
+}
+template <int S>
+__device__ __forceinline__ void store_padded(float* __restrict__ p, const Plan& pl, const Place& me, size_t index,
+                                             const float (&f)[S])
+{
+    if (me.d >= me.nch) return;
+    float* o = p + (index * pl.channels + me.c0 + me.d) * (4 * S) + me.q * S;
+#pragma unroll
+    for (int s = 0; s < S; s += 4) *reinterpret_cast<f32x4*>(o + s) = f32x4{f[s], f[s + 1], f[s + 2], f[s + 3]};
+}
+template <int S>
+__device__ __forceinline__ void start_state(const float* __restrict__ initial, const Plan& pl, const Place& me, uint32_t s,
+                                            float (&h)[S])
+{
+    if (initial) {
+        load_states<S>(initial + (size_t)s * pl.channels * pl.states, pl, me, h);
+    } else {
+#pragma unroll
+        for (int i = 0; i < S; ++i) h[i] = 0.0f;
+    }
+}
+
+// What later spans need of a span: its state from a zero start (or its gradient, backwards) and
+// the sum of dt over the rows.
+struct SpanTotals {
+    float* states;  // [span][channels][NP]
+    float* dt_sum;  // [span][channels]
+};
+// h = the state behind spans [first, last], joined in order (`step` 1) or in reverse (-1).
+template <int S>
+__device__ __forceinline__ void join_spans(const SpanTotals& t, const Plan& pl, const Place& me, uint32_t first,
+                                           uint32_t last, int step, const float (&A2)[S], float (&h)[S])
+{
+    load_padded<S>(t.states, pl, me, first, h);
+    while (first != last) {
+        first += step;
+        const float sum = me.d < me.nch ? t.dt_sum[(size_t)first * pl.channels + me.c0 + me.d] : 0.0f;
+        float e[S];
+        load_padded<S>(t.states, pl, me, first, e);
+#pragma unroll
+        for (int s = 0; s < S; ++s) h[s] = fmaf(exp2_fast(A2[s] * sum), h[s], e[s]);
+    }
+}
+
+// dt of one element: raw = delta + bias
+__device__ __forceinline__ float step_size(float raw, int sp) { return sp ? softplus(raw) : raw; }
+
+// ------------------------------------------------------------ forward
+// TOTALS: the span's totals only.
+template <typename T, int S, bool TOTALS>
+__global__ __launch_bounds__(kWaves * 64) void scan_kernel(Plan pl, Inputs in, SpanTotals totals, void* y,
+                                                           int64_t y_stride, float* final_state, float* saved)
+{
+    using C = Cfg<S>;
+    constexpr int TT = C::TT, NP = C::NP;
+    using X = Tile<T, TT>;
+    using BC = StateTile<T, TT, NP, 64>;
+    constexpr int V = X::V;
+    __shared__ __align__(16) f32x2 s_dt[kWaves][TT * kWaveChannels];
+    __shared__ __align__(16) float s_b[kWaves][TT * NP];
+    __shared__ __align__(16) float s_c[TOTALS ? 1 : kWaves][TOTALS ? 4 : TT * NP];
+    __shared__ __align__(16) float s_y[TOTALS ? 1 : kWaves][TOTALS ? 4 : TT * kWaveChannels];
+
+    const uint32_t block = blockIdx.x % pl.blocks, span = blockIdx.x / pl.blocks;
+    const Place me(pl, block);
+    if (me.nch == 0) return;
+    if (span >= pl.spans) {
+        // behind the spans: the final states of empty sequences
+        for (uint32_t s = span - pl.spans; s < pl.seqs.count; s += kEmptyStep) {
+            if (pl.seqs.end(s) > pl.seqs.start(s)) continue;
+            float h[S];
+            start_state<S>(in.initial, pl, me, s, h);
+            store_states<S>(final_state + (size_t)s * pl.channels * pl.states, pl, me, h);
+        }
+        return;
+    }
+    uint32_t r0, r1;
+    pl.rows_of(span, r0, r1);
+    f32x2* const dt = s_dt[me.w];
+    float* const lb = s_b[me.w];
+    float* const lc = s_c[TOTALS ? 0 : me.w];
+    float* const ly = s_y[TOTALS ? 0 : me.w];
+
+    float A2[S], h[S];
+    load_states<S>(in.A, pl, me, A2, kLog2e);
+    float bias[V], skip[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int c = X::col(me.lane) + j;
+        bias[j] = in.delta_bias && c < me.nch ? in.delta_bias[me.c0 + c] : 0.0f;
+        skip[j] = in.D && c < me.nch ? in.D[me.c0 + c] : 0.0f;
+    }
+    const uint32_t bc_at = me.group * pl.states;
+
+    uint32_t pos = r0, st, en;
+    int s = pl.seqs.find(pos);
+    while (pl.seqs.seek(s, pos, r1, st, en)) {
+        pos = (uint32_t)uniform((int)pos);
+        const uint32_t e = min(en, r1);
+        if (TOTALS && en <= r1) {  // ends here: no later span continues it
+            pos = e;
+            continue;
+        }
+        if (pos == st) {
+            start_state<S>(in.initial, pl, me, (uint32_t)s, h);
+        } else if (TOTALS) {
+#pragma unroll
+            for (int i = 0; i < S; ++i) h[i] = 0.0f;
+        } else {
+            join_spans<S>(totals, pl, me, pl.span_of(span, st), span - 1, 1, A2, h);
+        }
+        float sum = 0.0f;
+        typename X::P px[X::PIECES], pd[X::PIECES], pz[X::PIECES];
+        typename BC::P pb[BC::PIECES], pc[BC::PIECES];
+        const auto fetch = [&](uint32_t at, int len) {
+            X::load(px, in.x, in.x_stride, at, len, me.c0, me.nch, in.vec, me.lane);
+            X::load(pd, in.delta, in.delta_stride, at, len, me.c0, me.nch, in.vec, me.lane);
+            BC::load(pb, in.B, in.b_stride, at, len, bc_at, pl.states, in.vec_bc, me.lane);
+            if (!TOTALS) {
+                BC::load(pc, in.C, in.c_stride, at, len, bc_at, pl.states, in.vec_bc, me.lane);
+                if (in.z) X::load(pz, in.z, in.z_stride, at, len, me.c0, me.nch, in.vec, me.lane);
+            }
+        };
+        const auto tile_len = [&](uint32_t at) { return (int)(min(r0 + ((at - r0) / TT + 1) * TT, e) - at); };
+        int len = tile_len(pos);
+        fetch(pos, len);
+        while (true) {
+            if (!TOTALS && saved && (pos - r0) % TT == 0)
+                store_padded<S>(saved, pl, me, (size_t)span * pl.tiles_per_span + (pos - r0) / TT, h);
+            // (dt, dt x) of the tile; rows behind len keep the state: dt = 0
+            float xf[X::PIECES][V], zf[X::PIECES][V];
+#pragma unroll
+            for (int i = 0; i < X::PIECES; ++i) {
+                float df[V];
+                unpack(px[i], xf[i]);
+                unpack(pd[i], df);
+                if (!TOTALS && in.z) unpack(pz[i], zf[i]);
+                const int r = X::row(i, me.lane);
+                if (TT % X::RPL && r >= TT) continue;
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float v = r < len ? step_size(df[j] + bias[j], in.softplus) : 0.0f;
+                    dt[r * kWaveChannels + X::col(me.lane) + j] = f32x2{v, v * xf[i][j]};
+                }
+            }
+            BC::put(lb, pb, me.lane);
+            if (!TOTALS) BC::put(lc, pc, me.lane);
+            wave_sync();
+            const uint32_t next = pos + len;
+            int next_len = 0;
+            if (next < e) {
+                next_len = tile_len(next);
+                fetch(next, next_len);
+            }
+            for (int t = 0; t < len; t += 4) {
+                float part[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const f32x2 v = dt[(t + u) * kWaveChannels + me.d];
+                    float b[S], c[S];
+                    lds_states<S>(lb + (t + u) * NP + me.q * S, b);
+                    if (!TOTALS) lds_states<S>(lc + (t + u) * NP + me.q * S, c);
+                    if (TOTALS) sum += v[0];
+                    part[u] = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < S; ++i) {
+                        h[i] = fmaf(exp2_fast(v[0] * A2[i]), h[i], v[1] * b[i]);
+                        if (!TOTALS) part[u] = fmaf(c[i], h[i], part[u]);
+                    }
+                }
+                if (!TOTALS) ly[(t + me.q) * kWaveChannels + me.d] = quad_transpose_sum(part, me.q);
+            }
+            if (!TOTALS && y) {
+                wave_sync();
+#pragma unroll
+                for (int i = 0; i < X::PIECES; ++i) {
+                    const int r = X::row(i, me.lane);
+                    if (r >= len) continue;
+                    float f[V];
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        f[j] = fmaf(skip[j], xf[i][j], ly[r * kWaveChannels + X::col(me.lane) + j]);
+                        if (in.z) f[j] *= silu(zf[i][j]);
+                    }
+                    X::store(y, y_stride, pos, len, me.c0, me.nch, in.vec, me.lane, i, f);
+                }
+            }
+            wave_sync();
+            pos = next;
+            if (pos >= e) break;
+            len = next_len;
+        }
+        if (TOTALS) {
+            store_padded<S>(totals.states, pl, me, span, h);
+            if (me.q == 0 && me.d < me.nch) totals.dt_sum[(size_t)span * pl.channels + me.c0 + me.d] = sum;
+        } else if (final_state && en <= r1) {
+            store_states<S>(final_state + (size_t)s * pl.channels * pl.states, pl, me, h);
+        }
+    }
+}
+
+// ------------------------------------------------------------ single tokens
+// A wavefront takes 16 channels of one row, lanes as above.
+template <typename T, int S>
+__global__ __launch_bounds__(kWaves * 64) void scan_step_kernel(Plan pl, Inputs in, const int32_t* __restrict__ slots,
+                                                                uint32_t n_slots, float* __restrict__ state,
+                                                                T* __restrict__ y, int64_t y_stride)
+{
+    const uint32_t block = blockIdx.x % pl.blocks, r = blockIdx.x / pl.blocks;
+    const Place me(pl, block);
+    if (me.d >= me.nch) return;
+    const int32_t slot = slots ? slots[r] : (int32_t)r;
+    if (slot < 0 || (uint32_t)slot >= n_slots) return;
+    const uint32_t c = me.c0 + me.d;
+    float* sp = state + ((size_t)slot * pl.channels + c) * pl.states + me.q * S;
+    const float* ap = in.A + (size_t)c * pl.states + me.q * S;
+    const T* bp = static_cast<const T*>(in.B) + (int64_t)r * in.b_stride + me.group * pl.states + me.q * S;
+    const T* cp = static_cast<const T*>(in.C) + (int64_t)r * in.c_stride + me.group * pl.states + me.q * S;
+    float h[S], a[S], b[S], cc[S];
+    const bool whole = in.vec_bc;  // states = 4 S, state and A 16-byte aligned
+#pragma unroll
+    for (int i = 0; i < S; i += 4) {
+        if (whole) {
+            const f32x4 hv = *reinterpret_cast<const f32x4*>(sp + i), av = *reinterpret_cast<const f32x4*>(ap + i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                h[i + j] = hv[j];
+                a[i + j] = av[j];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bool ok = me.q * S + i + j < pl.states;
+                h[i + j] = ok ? sp[i + j] : 0.0f;
+                a[i + j] = ok ? ap[i + j] : 0.0f;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const bool ok = me.q * S + i + j < pl.states;
+            b[i + j] = ok ? (float)bp[i + j] : 0.0f;
+            cc[i + j] = ok ? (float)cp[i + j] : 0.0f;
+        }
+    }
+    const float x = (float)static_cast<const T*>(in.x)[(int64_t)r * in.x_stride + c];
+    const float raw = (float)static_cast<const T*>(in.delta)[(int64_t)r * in.delta_stride + c] +
+                      (in.delta_bias ? in.delta_bias[c] : 0.0f);
+    const float dt = step_size(raw, in.softplus);
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+        h[i] = fmaf(exp2_fast(dt * a[i] * kLog2e), h[i], dt * x * b[i]);
+        sum = fmaf(cc[i], h[i], sum);
+    }
+#pragma unroll
+    for (int i = 0; i < S; i += 4) {
+        if (whole) {
+            *reinterpret_cast<f32x4*>(sp + i) = f32x4{h[i], h[i + 1], h[i + 2], h[i + 3]};
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (me.q * S + i + j < pl.states) sp[i + j] = h[i + j];
+        }
+    }
+    sum = quad_sum(sum);
+    if (me.q == 0) {
+        if (in.D) sum = fmaf(in.D[c], x, sum);
+        if (in.z) sum *= silu((float)static_cast<const T*>(in.z)[(int64_t)r * in.z_stride + c]);
+        y[(int64_t)r * y_stride + c] = (T)sum;
+    }
+}
+
+// ------------------------------------------------------------ gradient
+struct Grads {
+    const void* dy;
+    int64_t dy_stride;
+    const float* dfinal;
+    void *dx, *ddelta, *dz;
+    int64_t dx_stride, ddelta_stride, dz_stride;
+    float* dinitial;
+    const float* saved;
+    float* bc;    // [channel block][rows][2 NP]: the block's sums for dB and dC
+    float* dA;    // [span][channels][NP]
+    float* dch;   // [span][2][channels]: dD, ddelta_bias
+};
+
+// Backwards, g = a[t+1] dh[t+1] is what the later rows pass on to row t's state:
+//   dh = dv C + g;  g' = a dh         (dv = dy silu(z))
+// Totals of a span for the spans before it: g at its first row from g = 0 behind its last (or from
+// dfinal where the sequence ends in it), and the sum of dt.
+template <typename T, int S>
+__global__ __launch_bounds__(kWaves * 64) void grad_totals_kernel(Plan pl, Inputs in, Grads gr, SpanTotals totals)
+{
+    using C = Cfg<S>;
+    constexpr int TT = C::TT, NP = C::NP;
+    using X = Tile<T, TT>;
+    using BC = StateTile<T, TT, NP, 64>;
+    constexpr int V = X::V;
+    __shared__ __align__(16) f32x2 s_dt[kWaves][TT * kWaveChannels];
+    __shared__ __align__(16) float s_c[kWaves][TT * NP];
+
+    const uint32_t block = blockIdx.x % pl.blocks, span = blockIdx.x / pl.blocks;
+    const Place me(pl, block);
+    if (me.nch == 0) return;
+    uint32_t r0, r1, st, en;
+    pl.rows_of(span, r0, r1);
+    uint32_t pos = r0;
+    int s = pl.seqs.find(pos);
+    // only a sequence that began in an earlier span needs this span's totals
+    if (!pl.seqs.seek(s, pos, r1, st, en) || pos != r0 || st == r0) return;
+    f32x2* const dt = s_dt[me.w];
+    float* const lc = s_c[me.w];
+    float A2[S], g[S];
+    load_states<S>(in.A, pl, me, A2, kLog2e);
+    float bias[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int c = X::col(me.lane) + j;
+        bias[j] = in.delta_bias && c < me.nch ? in.delta_bias[me.c0 + c] : 0.0f;
+    }
+    if (en <= r1)
+        start_state<S>(gr.dfinal, pl, me, (uint32_t)s, g);
+    else
+#pragma unroll
+        for (int i = 0; i < S; ++i) g[i] = 0.0f;
+    uint32_t hi = (uint32_t)uniform((int)min(en, r1));
+    float sum = 0.0f;
+    typename X::P pd[X::PIECES], pz[X::PIECES], py[X::PIECES];
+    typename BC::P pc[BC::PIECES];
+    const auto fetch = [&](uint32_t at, int len) {
+        X::load(pd, in.delta, in.delta_stride, at, len, me.c0, me.nch, in.vec, me.lane);
+        X::load(py, gr.dy, gr.dy_stride, at, len, me.c0, me.nch, in.vec, me.lane);
+        if (in.z) X::load(pz, in.z, in.z_stride, at, len, me.c0, me.nch, in.vec, me.lane);
+        BC::load(pc, in.C, in.c_stride, at, len, me.group * pl.states, pl.states, in.vec_bc, me.lane);
+    };
+    uint32_t lo = r0 + (hi - 1 - r0) / TT * TT;
+    fetch(lo, (int)(hi - lo));
+    while (true) {
+        const int len = (int)(hi - lo);
+#pragma unroll
+        for (int i = 0; i < X::PIECES; ++i) {
+            float df[V], yf[V], zf[V];
+            unpack(pd[i], df);
+            unpack(py[i], yf);
+            if (in.z) unpack(pz[i], zf);
+            const int r = X::row(i, me.lane);
+            if (TT % X::RPL && r >= TT) continue;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float v = r < len ? step_size(df[j] + bias[j], in.softplus) : 0.0f;
+                dt[r * kWaveChannels + X::col(me.lane) + j] = f32x2{v, in.z ? yf[j] * silu(zf[j]) : yf[j]};
+            }
+        }
+        BC::put(lc, pc, me.lane);
+        wave_sync();
+        const bool more = lo > r0;
+        if (more) fetch(lo - TT, TT);
+        for (int t = (len - 1) | 3; t >= 0; t -= 4) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const f32x2 v = dt[(t - u) * kWaveChannels + me.d];
+                float c[S];
+                lds_states<S>(lc + (t - u) * NP + me.q * S, c);
+                sum += v[0];
+#pragma unroll
+                for (int i = 0; i < S; ++i) g[i] = exp2_fast(v[0] * A2[i]) * fmaf(v[1], c[i], g[i]);
+            }
+        }
+        wave_sync();
+        if (!more) break;
+        hi = lo;
+        lo -= TT;
+    }
+    store_padded<S>(totals.states, pl, me, span, g);
+    if (me.q == 0 && me.d < me.nch) totals.dt_sum[(size_t)span * pl.channels + me.c0 + me.d] = sum;
+}
+
+// Every gradient of a span's rows.  Tiles are taken from the last to the first.  A tile's states
+// are recomputed from its saved one: once forwards, keeping the state in front of every SUB rows,
+// then SUB rows at a time with their factors a and products a h' in registers, which the walk
+// back over those rows uses.
+//
+// dB and dC are sums over channels, which lie across the lanes: the matrix unit adds them up.
+// v_mfma_f32_16x16x4_f32 multiplies a 16 x 4 matrix by a 4 x 16 one whose element (k, j) is in
+// lane 16 k + j; with a first matrix that is 1 in row t mod 16 and 0 elsewhere it adds, into row
+// t mod 16 of the accumulator, the four 16-lane rows of any register.  So 16 rows of the tile
+// collect in one accumulator per state, at one instruction per row and state and none on the
+// vector units; what is left is a sum over the 4 channels of a lane row, every 16 rows.  The
+// wavefronts of a workgroup add theirs in LDS, the workgroups theirs in a second launch, always in
+// the same order.
+template <typename T, int S>
+__global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(S == 4 ? 2 : 1))) void grad_kernel(Plan pl, Inputs in, Grads gr, SpanTotals totals)
+{
+    using C = Cfg<S>;
+    constexpr int TT = C::TT, NP = C::NP, SUB = C::SUB, BLOCKS = TT / SUB;
+    using X = Tile<T, TT>;
+    using BC = StateTile<T, TT, NP, kWaves * 64>;
+    constexpr int V = X::V;
+    __shared__ __align__(16) f32x2 s_dt[kWaves][TT * kWaveChannels];  // (dt, dt x), then the row's sums (dt part, x part)
+    __shared__ __align__(16) float s_dv[kWaves][TT * kWaveChannels];  // dv, then sum_n C h
+    __shared__ __align__(16) float s_h[kWaves][BLOCKS * 64 * S];      // state in front of every SUB rows
+    __shared__ __align__(16) float s_b[TT * NP], s_c[TT * NP];
+    // the wavefront's sums for dB and dC, 16 rows at a time, take the place of states that are used up
+    constexpr int SUMS = BLOCKS * 64 * S - TT * 2 * NP;
+    static_assert(SUMS >= 0 && SUMS % 4 == 0, "the sums fit behind the states still needed");
+
+    const uint32_t block = blockIdx.x % pl.blocks, span = blockIdx.x / pl.blocks;
+    const Place me(pl, block);
+    uint32_t r0, r1;
+    pl.rows_of(span, r0, r1);
+    f32x2* const dt = s_dt[me.w];
+    float* const ldv = s_dv[me.w];
+    float* const lh = s_h[me.w];
+    float* const lsum = lh + SUMS;
+    float A2[S], g[S], dA[S] = {};
+    load_states<S>(in.A, pl, me, A2, kLog2e);
+    float bias[V], skip[V], dskip[V] = {}, dbias[V] = {};
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int c = X::col(me.lane) + j;
+        bias[j] = in.delta_bias && c < me.nch ? in.delta_bias[me.c0 + c] : 0.0f;
+        skip[j] = in.D && c < me.nch ? in.D[me.c0 + c] : 0.0f;
+    }
+    const uint32_t bc_at = me.group * pl.states;
+    float* const bc_out = gr.bc + (size_t)block * pl.seqs.rows * (2 * NP);
+
+    uint32_t hi = r1;
+    while (hi > r0) {
+        // the sequence that row hi - 1 lies in
+        int s = pl.seqs.find(hi - 1);
+        if (s < 0) break;
+        if (s >= (int)pl.seqs.count) {  // behind the last one
+            hi = (uint32_t)uniform((int)min(hi - 1, pl.seqs.start(pl.seqs.count)));
+            continue;
+        }
+        s = uniform(s);
+        const uint32_t st = pl.seqs.start((uint32_t)s), en = max(pl.seqs.end((uint32_t)s), hi);
+        const uint32_t first = (uint32_t)uniform((int)max(st, r0));
+        if (hi == en) {
+            start_state<S>(gr.dfinal, pl, me, (uint32_t)s, g);
+        } else {
+            join_spans<S>(totals, pl, me, pl.span_of(span, en - 1), span + 1, -1, A2, g);
+        }
+        typename X::P px[X::PIECES], pd[X::PIECES], pz[X::PIECES], py[X::PIECES];
+        typename BC::P pb[BC::PIECES], pc[BC::PIECES];
+        const auto fetch = [&](uint32_t at, int len) {
+            X::load(px, in.x, in.x_stride, at, len, me.c0, me.nch, in.vec, me.lane);
+            X::load(pd, in.delta, in.delta_stride, at, len, me.c0, me.nch, in.vec, me.lane);
+            X::load(py, gr.dy, gr.dy_stride, at, len, me.c0, me.nch, in.vec, me.lane);
+            if (in.z) X::load(pz, in.z, in.z_stride, at, len, me.c0, me.nch, in.vec, me.lane);
+            BC::load(pb, in.B, in.b_stride, at, len, bc_at, pl.states, in.vec_bc, threadIdx.x);
+            BC::load(pc, in.C, in.c_stride, at, len, bc_at, pl.states, in.vec_bc, threadIdx.x);
+        };
+        uint32_t lo = max(r0 + (hi - 1 - r0) / TT * TT, first);
+        constexpr bool AHEAD = S < 16;  // the next tile's pieces in registers (64 states leave none for them)
+        if (AHEAD) fetch(lo, (int)(hi - lo));
+        while (true) {
+            const int len = (int)(hi - lo);
+            if (!AHEAD) fetch(lo, len);
+            // the state in front of the tile
+            float h[S];
+            if (lo == st)
+                start_state<S>(in.initial, pl, me, (uint32_t)s, h);
+            else
+                load_padded<S>(gr.saved, pl, me, (size_t)span * pl.tiles_per_span + (lo - r0) / TT, h);
+            float xf[X::PIECES][V], df[X::PIECES][V], zf[X::PIECES][V], yf[X::PIECES][V];
+#pragma unroll
+            for (int i = 0; i < X::PIECES; ++i) {
+                unpack(px[i], xf[i]);
+                unpack(pd[i], df[i]);
+                unpack(py[i], yf[i]);
+                if (in.z) unpack(pz[i], zf[i]);
+                const int r = X::row(i, me.lane);
+                if (TT % X::RPL && r >= TT) continue;
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    df[i][j] += bias[j];
+                    const float v = r < len ? step_size(df[i][j], in.softplus) : 0.0f;
+                    const int at = r * kWaveChannels + X::col(me.lane) + j;
+                    dt[at] = f32x2{v, v * xf[i][j]};
+                    ldv[at] = in.z ? yf[i][j] * silu(zf[i][j]) : yf[i][j];
+                }
+            }
+            BC::put(s_b, pb, threadIdx.x);
+            BC::put(s_c, pc, threadIdx.x);
+            __syncthreads();
+            const bool more = lo > first;
+            const uint32_t next = more ? max(r0 + (lo - 1 - r0) / TT * TT, first) : lo;
+            if (AHEAD && more) fetch(next, (int)(lo - next));
+
+            // forwards: the states in front of every SUB rows
+            const int blocks = (len + SUB - 1) / SUB;
+            for (int k = 0;; ++k) {
+#pragma unroll
+                for (int i = 0; i < S; i += 4)
+                    *reinterpret_cast<f32x4*>(lh + (k * 64 + me.lane) * S + i) = f32x4{h[i], h[i + 1], h[i + 2], h[i + 3]};
+                if (k + 1 >= blocks) break;
+#pragma unroll
+                for (int u = 0; u < SUB; ++u) {
+                    const int t = k * SUB + u;
+                    const f32x2 v = dt[t * kWaveChannels + me.d];
+                    float b[S];
+                    lds_states<S>(s_b + t * NP + me.q * S, b);
+#pragma unroll
+                    for (int i = 0; i < S; ++i) h[i] = fmaf(exp2_fast(v[0] * A2[i]), h[i], v[1] * b[i]);
+                }
+            }
+            // backwards, SUB rows at a time
+            f32x4 accB[S], accC[S];
+#pragma unroll
+            for (int i = 0; i < S; ++i) accB[i] = accC[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int k = blocks - 1; k >= 0; --k) {
+                lds_states<S>(lh + (k * 64 + me.lane) * S, h);
+                float a[SUB][S], p[SUB][S];  // the factor and a h'
+#pragma unroll
+                for (int u = 0; u < SUB; ++u) {
+                    const int t = k * SUB + u;
+                    const f32x2 v = dt[t * kWaveChannels + me.d];
+                    float b[S];
+                    lds_states<S>(s_b + t * NP + me.q * S, b);
+#pragma unroll
+                    for (int i = 0; i < S; ++i) {
+                        a[u][i] = exp2_fast(v[0] * A2[i]);
+                        p[u][i] = a[u][i] * h[i];
+                        h[i] = fmaf(v[1], b[i], p[u][i]);
+                    }
+                }
+#pragma unroll
+                for (int u = SUB - 1; u >= 0; --u) {
+                    const int t = k * SUB + u;
+                    const f32x2 v = dt[t * kWaveChannels + me.d];
+                    const float dv = ldv[t * kWaveChannels + me.d];
+                    float b[S], c[S];
+                    lds_states<S>(s_b + t * NP + me.q * S, b);
+                    lds_states<S>(s_c + t * NP + me.q * S, c);
+                    const float select = (me.lane & 15) == (t & 15) ? 1.0f : 0.0f;
+                    float ch = 0.0f, sd = 0.0f, sx = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < S; ++i) {
+                        const float ht = fmaf(v[1], b[i], p[u][i]);
+                        ch = fmaf(c[i], ht, ch);
+                        accC[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(select, dv * ht, accC[i], 0, 0, 0);
+                        const float dh = fmaf(dv, c[i], g[i]);
+                        accB[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(select, dh * v[1], accB[i], 0, 0, 0);
+                        sx = fmaf(dh, b[i], sx);
+                        const float through = dh * p[u][i];
+                        dA[i] = fmaf(v[0], through, dA[i]);
+                        sd = fmaf(A2[i], through, sd);
+                        g[i] = a[u][i] * dh;
+                    }
+                    ch = quad_sum(ch);
+                    sd = quad_sum(sd);
+                    sx = quad_sum(sx);
+                    if (me.q == (t & 3)) {  // every lane of the quad has read the row's values
+                        dt[t * kWaveChannels + me.d] = f32x2{sd * kLn2, sx};
+                        ldv[t * kWaveChannels + me.d] = ch;
+                    }
+                }
+                if ((k * SUB) % 16 == 0) {
+                    // the accumulators hold 16 rows: lane 16 k + j has rows 4 k .. 4 k + 3, column j =
+                    // 4 (channel mod 4) + quarter; each of the four lanes of a quarter keeps one row
+                    const int row = k * SUB + 4 * (me.lane >> 4) + ((me.lane >> 2) & 3);
+                    const int pick = (me.lane >> 2) & 3;
+                    float fb[S], fc[S];
+#pragma unroll
+                    for (int i = 0; i < S; ++i) {
+                        float vb[4], vc[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            vb[j] = accB[i][j];
+                            vc[j] = accC[i][j];
+                            vb[j] += dpp<kRowRor4>(vb[j]);
+                            vc[j] += dpp<kRowRor4>(vc[j]);
+                            vb[j] += dpp<kRowRor8>(vb[j]);
+                            vc[j] += dpp<kRowRor8>(vc[j]);
+                        }
+                        fb[i] = pick == 0 ? vb[0] : pick == 1 ? vb[1] : pick == 2 ? vb[2] : vb[3];
+                        fc[i] = pick == 0 ? vc[0] : pick == 1 ? vc[1] : pick == 2 ? vc[2] : vc[3];
+                        accB[i] = accC[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                    }
+#pragma unroll
+                    for (int i = 0; i < S; i += 4) {
+                        *reinterpret_cast<f32x4*>(lsum + row * 2 * NP + me.q * S + i) = f32x4{fb[i], fb[i + 1], fb[i + 2], fb[i + 3]};
+                        *reinterpret_cast<f32x4*>(lsum + row * 2 * NP + NP + me.q * S + i) =
+                            f32x4{fc[i], fc[i + 1], fc[i + 2], fc[i + 3]};
+                    }
+                }
+            }
+            __syncthreads();
+            // the workgroup's sums for dB and dC
+            for (int i = threadIdx.x; i < len * 2 * NP / 4; i += kWaves * 64) {
+                f32x4 v = *reinterpret_cast<const f32x4*>(&s_h[0][SUMS + i * 4]);
+#pragma unroll
+                for (int w = 1; w < kWaves; ++w) v += *reinterpret_cast<const f32x4*>(&s_h[w][SUMS + i * 4]);
+                *reinterpret_cast<f32x4*>(bc_out + (size_t)lo * (2 * NP) + (size_t)i * 4) = v;
+            }
+            // the rows' own gradients
+#pragma unroll
+            for (int i = 0; i < X::PIECES; ++i) {
+                const int r = X::row(i, me.lane);
+                if (r >= len) continue;
+                float ox[V], od[V], oz[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const int at = r * kWaveChannels + X::col(me.lane) + j;
+                    const f32x2 q = dt[at];
+                    const float raw = df[i][j], v = step_size(raw, in.softplus), x = xf[i][j], dy = yf[i][j];
+                    float dv = dy;
+                    if (in.z) {
+                        const float z = zf[i][j], sg = sigmoid(z), full = fmaf(skip[j], x, ldv[at]);
+                        dv = dy * z * sg;
+                        oz[j] = dy * full * sg * (1.0f + z * (1.0f - sg));
+                    }
+                    ox[j] = fmaf(dv, skip[j], v * q[1]);
+                    od[j] = fmaf(x, q[1], q[0]);
+                    if (in.softplus && !(raw > 20.0f)) od[j] *= sigmoid(raw);
+                    dskip[j] = fmaf(dv, x, dskip[j]);
+                    dbias[j] += od[j];
+                }
+                X::store(gr.dx, gr.dx_stride, lo, len, me.c0, me.nch, in.vec, me.lane, i, ox);
+                X::store(gr.ddelta, gr.ddelta_stride, lo, len, me.c0, me.nch, in.vec, me.lane, i, od);
+                if (in.z) X::store(gr.dz, gr.dz_stride, lo, len, me.c0, me.nch, in.vec, me.lane, i, oz);
+            }
+            __syncthreads();
+            hi = lo;
+            if (!more) break;
+            lo = next;
+        }
+        if (first == st && gr.dinitial)
+            store_states<S>(gr.dinitial + (size_t)s * pl.channels * pl.states, pl, me, g);
+    }
+    store_padded<S>(gr.dA, pl, me, span, dA);
+    // lanes that loaded the same channels
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+#pragma unroll
+        for (int o = X::LPR; o < 64; o <<= 1) {
+            dskip[j] += __shfl_xor(dskip[j], o, 64);
+            dbias[j] += __shfl_xor(dbias[j], o, 64);
+        }
+        const int c = X::col(me.lane) + j;
+        if (me.lane < X::LPR && c < me.nch) {
+            float* out = gr.dch + (size_t)span * 2 * pl.channels + me.c0 + c;
+            out[0] = dskip[j];
+            out[pl.channels] = dbias[j];
+        }
+    }
+}
+
+// dB and dC: the workgroups' sums of a group's channels.  A lane takes 4 columns of a row.
+template <typename T>
+__global__ __launch_bounds__(256) void join_bc_kernel(Plan pl, const float* __restrict__ bc, uint32_t np, T* __restrict__ dB,
+                                                      int64_t db_stride, T* __restrict__ dC, int64_t dc_stride)
+{
+    const uint32_t quads = np / 2;  // 2 np columns
+    const uint64_t i = blockIdx.x * (uint64_t)256 + threadIdx.x;
+    const uint32_t col = (uint32_t)(i % quads) * 4;
+    const uint64_t rg = i / quads;
+    const uint32_t group = (uint32_t)(rg % pl.groups);
+    const uint64_t row = rg / pl.groups;
+    if (row >= pl.seqs.rows || row < pl.seqs.start(0) || row >= pl.seqs.start(pl.seqs.count)) return;
+    const size_t step = (size_t)pl.seqs.rows * 2 * np;
+    const float* p = bc + (size_t)group * pl.blocks_per_group * step + row * 2 * np + col;
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+    for (uint32_t b = 0; b < pl.blocks_per_group; ++b) v += *reinterpret_cast<const f32x4*>(p + b * step);
+    const uint32_t n = col % np;
+    T* out = (col < np ? dB + (int64_t)row * db_stride : dC + (int64_t)row * dc_stride) + group * pl.states + n;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (n + j < pl.states) out[j] = (T)v[j];
+}
+
+// dA, dD and ddelta_bias: the spans' sums.
+__global__ __launch_bounds__(256) void join_spans_kernel(Plan pl, const float* __restrict__ dA_part,
+                                                         const float* __restrict__ dch, uint32_t np, float* __restrict__ dA,
+                                                         float* __restrict__ dD, float* __restrict__ dbias)
+{
+    const uint64_t i = blockIdx.x * (uint64_t)256 + threadIdx.x, na = (uint64_t)pl.channels * np;
+    float sum = 0.0f;
+    if (i < na) {
+#pragma unroll 8
+        for (uint32_t s = 0; s < pl.spans; ++s) sum += dA_part[s * na + i];
+        const uint32_t n = (uint32_t)(i % np);
+        if (n < pl.states) dA[i / np * pl.states + n] = sum;
+    } else if (i < na + 2 * (uint64_t)pl.channels) {
+        const uint64_t c = i - na;
+#pragma unroll 8
+        for (uint32_t s = 0; s < pl.spans; ++s) sum += dch[s * 2 * (uint64_t)pl.channels + c];
+        if (c < pl.channels) {
+            if (dD) dD[c] = sum;
+        } else if (dbias) {
+            dbias[c - pl.channels] = sum;
+        }
+    }
+}
+
+// dinitial of empty sequences is dfinal.
+template <int S>
+__global__ __launch_bounds__(kWaves * 64) void grad_empty_kernel(Plan pl, const float* __restrict__ dfinal,
+                                                                 float* __restrict__ dinitial)
+{
+    const uint32_t block = blockIdx.x % pl.blocks;
+    const Place me(pl, block);
+    for (uint32_t s = blockIdx.x / pl.blocks; s < pl.seqs.count; s += kEmptyStep) {
+        if (pl.seqs.end(s) > pl.seqs.start(s)) continue;
+        float g[S];
+        start_state<S>(dfinal, pl, me, s, g);
+        store_states<S>(dinitial + (size_t)s * pl.channels * pl.states, pl, me, g);
+    }
+}
+
+// ------------------------------------------------------------ host side
+constexpr uint32_t kTargetWorkgroups = 512;  // two per compute unit
+constexpr uint32_t kMinSpanRows = 128;
+
+Plan make_plan(uint32_t channels, uint32_t states, uint32_t groups, uint64_t rows, uint64_t seqs, const int32_t* offsets)
+{
+    Plan p{};
+    p.seqs = Sequences{offsets, (uint32_t)rows, (uint32_t)seqs, seqs ? (uint32_t)(rows / seqs) : 0u};
+    p.channels = channels;
+    p.states = states;
+    p.groups = groups;
+    p.group_channels = channels / groups;
+    p.blocks_per_group = (p.group_channels + kWgChannels - 1) / kWgChannels;
+    p.blocks = groups * p.blocks_per_group;
+    const uint32_t tt = tile_rows(states_per_lane(states));
+    // rows of one sequence, or of all packed ones; and how many spans they may be cut into
+    const uint64_t run = offsets ? rows : p.seqs.len, runs = offsets ? 1 : seqs;
+    uint64_t cuts = 1;
+    if (run) {
+        cuts = (kTargetWorkgroups + runs * p.blocks - 1) / (runs * p.blocks);
+        cuts = std::max<uint64_t>(1, std::min<uint64_t>(cuts, run / kMinSpanRows));
+    }
+    p.span_rows = (uint32_t)std::max<uint64_t>(tt, round_up((run + cuts - 1) / cuts, tt));
+    p.per_seq = (uint32_t)((run + p.span_rows - 1) / p.span_rows);
+    p.spans = offsets ? p.per_seq : (uint32_t)(p.per_seq * seqs);
+    p.tiles_per_span = p.span_rows / tt;
+    return p;
+}
+Plan make_plan(const selective_scan_args_t& a)
+{
+    return make_plan(a.channels, a.states, a.groups, a.rows, a.seqs, a.seq_offsets);
+}
+
+size_t padded_states(uint32_t states) { return 4 * (size_t)states_per_lane(states); }
+
+struct Space {
+    SpanTotals totals;
+    float *bc, *dA, *dch;
+    size_t bytes;
+};
+Space lay_out(const Plan& p, bool grad, void* base)
+{
+    Space s{};
+    size_t at = 0;
+    const auto take = [&](size_t floats) {
+        float* q = reinterpret_cast<float*>(static_cast<char*>(base) + at);
+        at += round_up(floats * 4, 256);
+        return q;
+    };
+    const size_t np = padded_states(p.states);
+    if (p.per_seq > 1) {
+        s.totals.states = take((size_t)p.spans * p.channels * np);
+        s.totals.dt_sum = take((size_t)p.spans * p.channels);
+    }
+    if (grad) {
+        s.bc = take((size_t)p.blocks * p.seqs.rows * 2 * np);
+        s.dA = take((size_t)p.spans * p.channels * np);
+        s.dch = take((size_t)p.spans * 2 * p.channels);
+    }
+    s.bytes = std::max<size_t>(at, 256);
+    return s;
+}
+
+scan_status_t check_sizes(int dtype, uint64_t rows, uint32_t channels, uint32_t states, uint32_t groups)
+{
+    if (!valid_dtype(dtype)) return SCAN_ERR_UNSUPPORTED;
+    if (states < 1 || states > 64) return SCAN_ERR_UNSUPPORTED;
+    if (channels < 1 || channels > kMaxChannels || groups < 1 || channels % groups) return SCAN_ERR_INVALID;
+    if (rows >= ((uint64_t)1 << 31)) return SCAN_ERR_INVALID;
+    return SCAN_OK;
+}
+
+struct Rows {
+    int dtype;
+    uint64_t rows;
+    bool ok(const void* p, int64_t stride, uint32_t width) const
+    {
+        return rows == 0 ||
+               (p && aligned(p, dtype_size(dtype)) && stride >= (int64_t)width && stride <= ((int64_t)1 << 31));
+    }
+    bool vec(const void* p, int64_t stride) const
+    {
+        return aligned(p, 16) && stride % (16 / (int64_t)dtype_size(dtype)) == 0;
+    }
+};
+
+scan_status_t check_scan(const selective_scan_args_t& a)
+{
+    const scan_status_t st = check_sizes(a.dtype, a.rows, a.channels, a.states, a.groups);
+    if (st != SCAN_OK) return st;
+    if (a.seqs >= ((uint64_t)1 << 31)) return SCAN_ERR_INVALID;
+    if (a.seqs == 0 ? a.rows != 0 : (!a.seq_offsets && a.rows % a.seqs != 0)) return SCAN_ERR_INVALID;
+    if (!aligned(a.seq_offsets, 4)) return SCAN_ERR_INVALID;
+    const Rows r{a.dtype, a.rows};
+    const uint32_t gn = a.groups * a.states;
+    if (!r.ok(a.x, a.x_stride, a.channels) || !r.ok(a.delta, a.delta_stride, a.channels) || !r.ok(a.B, a.b_stride, gn) ||
+        !r.ok(a.C, a.c_stride, gn) || (a.z && !r.ok(a.z, a.z_stride, a.channels)))
+        return SCAN_ERR_INVALID;
+    if (!a.A) return SCAN_ERR_INVALID;
+    for (const void* p : {(const void*)a.A, (const void*)a.D, (const void*)a.delta_bias, (const void*)a.initial_state,
+                          (const void*)a.final_state})
+        if (!aligned(p, 4)) return SCAN_ERR_INVALID;
+    return aligned(a.saved, 16) ? SCAN_OK : SCAN_ERR_INVALID;
+}
+
+template <class A>
+Inputs make_inputs(const A& a, const Rows& r)
+{
+    Inputs in{};
+    in.x = a.x;
+    in.delta = a.delta;
+    in.B = a.B;
+    in.C = a.C;
+    in.z = a.z;
+    in.x_stride = a.x_stride;
+    in.delta_stride = a.delta_stride;
+    in.b_stride = a.b_stride;
+    in.c_stride = a.c_stride;
+    in.z_stride = a.z_stride;
+    in.A = a.A;
+    in.D = a.D;
+    in.delta_bias = a.delta_bias;
+    in.softplus = a.delta_softplus != 0;
+    const uint32_t v = 16 / (uint32_t)dtype_size(a.dtype);
+    in.vec = a.channels / a.groups % v == 0 && r.vec(a.x, a.x_stride) && r.vec(a.delta, a.delta_stride) &&
+             (!a.z || r.vec(a.z, a.z_stride));
+    in.vec_bc = a.states == padded_states(a.states) && r.vec(a.B, a.b_stride) && r.vec(a.C, a.c_stride);
+    return in;
+}
+
+// Calls f(T, S).
+template <class F>
+scan_status_t dispatch(int dtype, uint32_t states, F f)
+{
+    return with_dtype(dtype, [&](auto e) -> scan_status_t {
+        using T = decltype(e);
+        switch (states_per_lane(states)) {
+            case 4: return f(T(), std::integral_constant<int, 4>());
+            case 8: return f(T(), std::integral_constant<int, 8>());
+            default: return f(T(), std::integral_constant<int, 16>());
+        }
+    });
+}
+
+scan_status_t forward(const selective_scan_args_t& a, hipStream_t stream)
+{
+    const Plan p = make_plan(a);
+    const Space w = lay_out(p, false, a.workspace);
+    const Rows r{a.dtype, a.rows};
+    Inputs in = make_inputs(a, r);
+    in.initial = a.initial_state;
+    if (a.y) in.vec = in.vec && r.vec(a.y, a.y_stride);
+    return dispatch(a.dtype, a.states, [&](auto te, auto se) -> scan_status_t {
+        using T = decltype(te);
+        constexpr int S = decltype(se)::value;
+        const uint64_t wgs = (uint64_t)p.spans * p.blocks;
+        const uint64_t extra = a.final_state ? (uint64_t)std::min<uint64_t>(p.seqs.count, kEmptyStep) * p.blocks : 0;
+        if (wgs + extra > 0x7FFFFFFFu) return SCAN_ERR_INVALID;
+        if (p.per_seq > 1)
+            hipLaunchKernelGGL((scan_kernel<T, S, true>), dim3((unsigned)wgs), dim3(kWaves * 64), 0, stream, p, in, w.totals,
+                               (void*)nullptr, (int64_t)0, (float*)nullptr, (float*)nullptr);
+        if (wgs + extra)
+            hipLaunchKernelGGL((scan_kernel<T, S, false>), dim3((unsigned)(wgs + extra)), dim3(kWaves * 64), 0, stream, p, in,
+                               w.totals, a.y, a.y_stride, a.final_state, a.saved);
+        return launched();
+    });
+}
+
+scan_status_t gradient(const selective_scan_grad_args_t& g, hipStream_t stream)
+{
+    const selective_scan_args_t& a = g.args;
+    const Plan p = make_plan(a);
+    const Space w = lay_out(p, true, a.workspace);
+    const Rows r{a.dtype, a.rows};
+    Inputs in = make_inputs(a, r);
+    in.initial = a.initial_state;
+    in.vec = in.vec && r.vec(g.dy, g.dy_stride) && r.vec(g.dx, g.dx_stride) && r.vec(g.ddelta, g.ddelta_stride) &&
+             (!a.z || r.vec(g.dz, g.dz_stride));
+    const Grads gr{g.dy, g.dy_stride, g.dfinal_state, g.dx,        g.ddelta, g.dz, g.dx_stride, g.ddelta_stride,
+                   g.dz_stride, g.dinitial_state, a.saved, w.bc, w.dA, w.dch};
+    return dispatch(a.dtype, a.states, [&](auto te, auto se) -> scan_status_t {
+        using T = decltype(te);
+        constexpr int S = decltype(se)::value;
+        const uint32_t np = 4 * S;
+        const uint64_t wgs = (uint64_t)p.spans * p.blocks;
+        const uint64_t bc = ((uint64_t)a.rows * a.groups * (np / 2) + 255) / 256;
+        if (wgs > 0x7FFFFFFFu || bc > 0x7FFFFFFFu) return SCAN_ERR_INVALID;
+        const dim3 block(kWaves * 64);
+        if (p.per_seq > 1)
+            hipLaunchKernelGGL((grad_totals_kernel<T, S>), dim3((unsigned)wgs), block, 0, stream, p, in, gr, w.totals);
+        if (wgs) {
+            hipLaunchKernelGGL((grad_kernel<T, S>), dim3((unsigned)wgs), block, 0, stream, p, in, gr, w.totals);
+            hipLaunchKernelGGL((join_bc_kernel<T>), dim3((unsigned)bc), dim3(256), 0, stream, p, (const float*)w.bc, np,
+                               static_cast<T*>(g.dB), g.db_stride, static_cast<T*>(g.dC), g.dc_stride);
+        }
+        const uint64_t sums = (uint64_t)a.channels * (np + 2);
+        hipLaunchKernelGGL(join_spans_kernel, dim3((unsigned)((sums + 255) / 256)), dim3(256), 0, stream, p,
+                           (const float*)w.dA, (const float*)w.dch, np, g.dA, g.dD, g.ddelta_bias);
+        if (g.dinitial_state && p.seqs.count && (a.seq_offsets || a.rows == 0))
+            hipLaunchKernelGGL((grad_empty_kernel<S>), dim3((unsigned)(std::min(p.seqs.count, kEmptyStep) * p.blocks)), block,
+                               0, stream, p, g.dfinal_state, g.dinitial_state);
+        return launched();
+    });
+}
+
+}  // namespace
+}  // namespace dwpt_seq
+
+using namespace dwpt_seq;
+
+extern "C" {
+
+size_t selective_scan_workspace(const selective_scan_args_t* args)
+{
+    if (!args || check_scan(*args) != SCAN_OK) return 0;
+    return lay_out(make_plan(*args), false, nullptr).bytes;
+}
+
+size_t selective_scan_saved(const selective_scan_args_t* args)
+{
+    if (!args || check_scan(*args) != SCAN_OK) return 0;
+    const Plan p = make_plan(*args);
+    return (size_t)p.spans * p.tiles_per_span * p.channels * padded_states(p.states);
+}
+
+scan_status_t selective_scan(const selective_scan_args_t* args, void* stream)
+{
+    if (!args) return SCAN_ERR_INVALID;
+    const selective_scan_args_t& a = *args;
+    const scan_status_t st = check_scan(a);
+    if (st != SCAN_OK) return st;
+    const size_t es = dtype_size(a.dtype), need = selective_scan_workspace(&a);
+    if (a.y && !Rows{a.dtype, a.rows}.ok(a.y, a.y_stride, a.channels)) return SCAN_ERR_INVALID;
+    if (!a.workspace || !aligned(a.workspace, 256) || a.workspace_bytes < need) return SCAN_ERR_INVALID;
+    const uint64_t state = (uint64_t)a.seqs * a.channels * a.states * 4;
+    const uint32_t gn = a.groups * a.states;
+    const Range outs[] = {range(a.y, a.rows, a.y_stride, a.channels, es), range(a.final_state, state),
+                          range(a.saved, selective_scan_saved(&a) * 4), range(a.workspace, need)};
+    const Range ins[] = {range(a.x, a.rows, a.x_stride, a.channels, es),
+                         range(a.delta, a.rows, a.delta_stride, a.channels, es),
+                         range(a.z, a.rows, a.z_stride, a.channels, es),
+                         range(a.B, a.rows, a.b_stride, gn, es),
+                         range(a.C, a.rows, a.c_stride, gn, es),
+                         range(a.A, (uint64_t)a.channels * a.states * 4),
+                         range(a.D, (uint64_t)a.channels * 4),
+                         range(a.delta_bias, (uint64_t)a.channels * 4),
+                         range(a.initial_state, state),
+                         range(a.seq_offsets, (a.seqs + 1) * 4)};
+    if (any_overlap(outs, ins)) return SCAN_ERR_INVALID;
+    return forward(a, static_cast<hipStream_t>(stream));
+}
+
+size_t selective_scan_grad_workspace(const selective_scan_grad_args_t* args)
+{
+    if (!args || check_scan(args->args) != SCAN_OK) return 0;
+    return lay_out(make_plan(args->args), true, nullptr).bytes;
+}
+
+scan_status_t selective_scan_grad(const selective_scan_grad_args_t* grad, void* stream)
+{
+    if (!grad) return SCAN_ERR_INVALID;
+    const selective_scan_grad_args_t& g = *grad;
+    const selective_scan_args_t& a = g.args;
+    const scan_status_t st = check_scan(a);
+    if (st != SCAN_OK) return st;
+    const size_t es = dtype_size(a.dtype), need = selective_scan_grad_workspace(&g);
+    const Rows r{a.dtype, a.rows};
+    const uint32_t gn = a.groups * a.states;
+    if (!r.ok(g.dy, g.dy_stride, a.channels) || !r.ok(g.dx, g.dx_stride, a.channels) ||
+        !r.ok(g.ddelta, g.ddelta_stride, a.channels) || !r.ok(g.dB, g.db_stride, gn) || !r.ok(g.dC, g.dc_stride, gn) ||
+        (a.z && !r.ok(g.dz, g.dz_stride, a.channels)))
+        return SCAN_ERR_INVALID;
+    if (!g.dA || (a.D != nullptr) != (g.dD != nullptr) || (a.delta_bias != nullptr) != (g.ddelta_bias != nullptr) ||
+        (!a.z && g.dz) || (a.rows && !a.saved))
+        return SCAN_ERR_INVALID;
+    for (const void* p : {(const void*)g.dfinal_state, (const void*)g.dA, (const void*)g.dD, (const void*)g.ddelta_bias,
+                          (const void*)g.dinitial_state})
+        if (!aligned(p, 4)) return SCAN_ERR_INVALID;
+    if (!a.workspace || !aligned(a.workspace, 256) || a.workspace_bytes < need) return SCAN_ERR_INVALID;
+    const uint64_t state = (uint64_t)a.seqs * a.channels * a.states * 4;
+    const Range outs[] = {range(g.dx, a.rows, g.dx_stride, a.channels, es),
+                          range(g.ddelta, a.rows, g.ddelta_stride, a.channels, es),
+                          range(g.dz, a.rows, g.dz_stride, a.channels, es),
+                          range(g.dB, a.rows, g.db_stride, gn, es),
+                          range(g.dC, a.rows, g.dc_stride, gn, es),
+                          range(g.dA, (uint64_t)a.channels * a.states * 4),
+                          range(g.dD, (uint64_t)a.channels * 4),
+                          range(g.ddelta_bias, (uint64_t)a.channels * 4),
+                          range(g.dinitial_state, state),
+                          range(a.workspace, need)};
+    const Range ins[] = {range(a.x, a.rows, a.x_stride, a.channels, es),
+                         range(a.delta, a.rows, a.delta_stride, a.channels, es),
+                         range(a.z, a.rows, a.z_stride, a.channels, es),
+                         range(a.B, a.rows, a.b_stride, gn, es),
+                         range(a.C, a.rows, a.c_stride, gn, es),
+                         range(g.dy, a.rows, g.dy_stride, a.channels, es),
+                         range(a.A, (uint64_t)a.channels * a.states * 4),
+                         range(a.D, (uint64_t)a.channels * 4),
+                         range(a.delta_bias, (uint64_t)a.channels * 4),
+                         range(a.initial_state, state),
+                         range(g.dfinal_state, state),
+                         range(a.saved, selective_scan_saved(&a) * 4),
+                         range(a.seq_offsets, (a.seqs + 1) * 4)};
+    if (any_overlap(outs, ins)) return SCAN_ERR_INVALID;
+    return gradient(g, static_cast<hipStream_t>(stream));
+}
+
+scan_status_t selective_scan_step(const selective_scan_step_args_t* args, void* stream)
+{
+    if (!args) return SCAN_ERR_INVALID;
+    const selective_scan_step_args_t& a = *args;
+    const scan_status_t st = check_sizes(a.dtype, a.rows, a.channels, a.states, a.groups);
+    if (st != SCAN_OK) return st;
+    if (a.n_slots >= ((uint64_t)1 << 31)) return SCAN_ERR_INVALID;
+    if (a.rows == 0) return SCAN_OK;
+    const Rows r{a.dtype, a.rows};
+    const uint32_t gn = a.groups * a.states;
+    const size_t es = dtype_size(a.dtype);
+    if (!r.ok(a.x, a.x_stride, a.channels) || !r.ok(a.delta, a.delta_stride, a.channels) || !r.ok(a.B, a.b_stride, gn) ||
+        !r.ok(a.C, a.c_stride, gn) || (a.z && !r.ok(a.z, a.z_stride, a.channels)) || !r.ok(a.y, a.y_stride, a.channels))
+        return SCAN_ERR_INVALID;
+    if (!a.A || !a.state) return SCAN_ERR_INVALID;
+    for (const void* p : {(const void*)a.A, (const void*)a.D, (const void*)a.delta_bias, (const void*)a.state,
+                          (const void*)a.slots})
+        if (!aligned(p, 4)) return SCAN_ERR_INVALID;
+    const Range outs[] = {range(a.y, a.rows, a.y_stride, a.channels, es),
+                          range(a.state, a.n_slots * (uint64_t)a.channels * a.states * 4)};
+    const Range ins[] = {range(a.x, a.rows, a.x_stride, a.channels, es),
+                         range(a.delta, a.rows, a.delta_stride, a.channels, es),
+                         range(a.z, a.rows, a.z_stride, a.channels, es),
+                         range(a.B, a.rows, a.b_stride, gn, es),
+                         range(a.C, a.rows, a.c_stride, gn, es),
+                         range(a.A, (uint64_t)a.channels * a.states * 4),
+                         range(a.D, (uint64_t)a.channels * 4),
+                         range(a.delta_bias, (uint64_t)a.channels * 4),
+                         range(a.slots, a.rows * 4)};
+    if (any_overlap(outs, ins)) return SCAN_ERR_INVALID;
+    const Plan p = make_plan(a.channels, a.states, a.groups, a.rows, 1, nullptr);
+    const uint64_t wgs = a.rows * (uint64_t)p.blocks;
+    if (wgs > 0x7FFFFFFFu) return SCAN_ERR_INVALID;
+    Inputs in = make_inputs(a, r);
+    in.vec_bc = a.states == padded_states(a.states) && aligned(a.state, 16) && aligned(a.A, 16);
+    return dispatch(a.dtype, a.states, [&](auto te, auto se) -> scan_status_t {
+        using T = decltype(te);
+        constexpr int S = decltype(se)::value;
+        hipLaunchKernelGGL((scan_step_kernel<T, S>), dim3((unsigned)wgs), dim3(kWaves * 64), 0,
+                           static_cast<hipStream_t>(stream), p, in, a.slots, (uint32_t)a.n_slots, a.state,
+                           static_cast<T*>(a.y), a.y_stride);
+        return launched();
+    });
+}
+
+}  // extern "C"

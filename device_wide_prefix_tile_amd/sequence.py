@@ -1,0 +1,580 @@
+"""Sequence-model operators over torch tensors: embedding lookup and its gradient by sorted
+tokens, the short causal convolution and the selective state-space scan, with their gradients
+and their single-token forms (C ABI in include/dwpt_seq.h).
+
+Argument marshalling only, as in ``binding``: every step runs in the library's HIP kernels, calls
+enqueue on the current stream of the tensors' device (or on ``stream``) and return without
+synchronising, and there is no CPU fallback.  Outputs and workspaces come from torch's allocator
+on the stream that the call runs on, so a call can be captured into a graph.
+
+Layout: channels last.  Rows are (B, L, D) for B sequences of one length, or (rows, D) with
+``seq_offsets`` (int32, S + 1 ascending) for sequences packed one behind the other.  A tensor of
+rows may be a slice of a wider one (any row stride); its last dimension is contiguous.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple, Optional
+
+import torch
+
+from .binding import ScanError, _raw_stream, lib
+
+_DTYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+_ACT = {None: 0, "silu": 1}
+_P, _I, _I64, _U32, _U64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_uint64
+
+
+class _ConvArgs(ctypes.Structure):
+    _fields_ = [("dtype", _I), ("weight_dtype", _I), ("activation", _I), ("width", _I), ("rows", _U64), ("seqs", _U64),
+                ("seq_offsets", _P), ("channels", _U32), ("reserved", _U32), ("x", _P), ("x_stride", _I64), ("weight", _P),
+                ("bias", _P), ("initial_state", _P), ("y", _P), ("y_stride", _I64), ("final_state", _P)]
+
+
+class _ConvGradArgs(ctypes.Structure):
+    _fields_ = [("args", _ConvArgs), ("dy", _P), ("dy_stride", _I64), ("dfinal_state", _P), ("dx", _P), ("dx_stride", _I64),
+                ("dweight", _P), ("dbias", _P), ("dinitial_state", _P), ("workspace", _P), ("workspace_bytes", _U64)]
+
+
+class _ConvStepArgs(ctypes.Structure):
+    _fields_ = [("dtype", _I), ("weight_dtype", _I), ("activation", _I), ("width", _I), ("rows", _U64), ("n_slots", _U64),
+                ("slots", _P), ("channels", _U32), ("reserved", _U32), ("x", _P), ("x_stride", _I64), ("weight", _P),
+                ("bias", _P), ("state", _P), ("y", _P), ("y_stride", _I64)]
+
+
+_SCAN_INPUTS = [("channels", _U32), ("states", _U32), ("groups", _U32), ("reserved", _U32), ("x", _P), ("x_stride", _I64),
+                ("delta", _P), ("delta_stride", _I64), ("A", _P), ("B", _P), ("b_stride", _I64), ("C", _P),
+                ("c_stride", _I64), ("D", _P), ("z", _P), ("z_stride", _I64), ("delta_bias", _P)]
+
+
+class _ScanArgs(ctypes.Structure):
+    _fields_ = ([("dtype", _I), ("delta_softplus", _I), ("rows", _U64), ("seqs", _U64), ("seq_offsets", _P)] + _SCAN_INPUTS
+                + [("initial_state", _P), ("y", _P), ("y_stride", _I64), ("final_state", _P), ("saved", _P),
+                   ("workspace", _P), ("workspace_bytes", _U64)])
+
+
+class _ScanGradArgs(ctypes.Structure):
+    _fields_ = [("args", _ScanArgs), ("dy", _P), ("dy_stride", _I64), ("dfinal_state", _P), ("dx", _P), ("dx_stride", _I64),
+                ("ddelta", _P), ("ddelta_stride", _I64), ("dz", _P), ("dz_stride", _I64), ("dB", _P), ("db_stride", _I64),
+                ("dC", _P), ("dc_stride", _I64), ("dA", _P), ("dD", _P), ("ddelta_bias", _P), ("dinitial_state", _P)]
+
+
+class _ScanStepArgs(ctypes.Structure):
+    _fields_ = ([("dtype", _I), ("delta_softplus", _I), ("rows", _U64), ("n_slots", _U64), ("slots", _P)] + _SCAN_INPUTS
+                + [("state", _P), ("y", _P), ("y_stride", _I64)])
+
+
+SIGNATURES = {
+    "embedding_lookup": ([_I, _P, _I, _U64, _P, _I64, _U64, _U32, ctypes.c_float, _P, _P], _I),
+    "embedding_grad": ([_I, _I, _P, _I, _U64, _P, _I64, _U64, _U32, ctypes.c_float, _I, _P, _P, _U64, _P], _I),
+    "embedding_grad_workspace": ([_U64, _U64, _U32], _U64),
+    "causal_conv1d": ([ctypes.POINTER(_ConvArgs), _P], _I),
+    "causal_conv1d_grad": ([ctypes.POINTER(_ConvGradArgs), _P], _I),
+    "causal_conv1d_grad_workspace": ([ctypes.POINTER(_ConvArgs)], _U64),
+    "causal_conv1d_step": ([ctypes.POINTER(_ConvStepArgs), _P], _I),
+    "selective_scan": ([ctypes.POINTER(_ScanArgs), _P], _I),
+    "selective_scan_workspace": ([ctypes.POINTER(_ScanArgs)], _U64),
+    "selective_scan_saved": ([ctypes.POINTER(_ScanArgs)], _U64),
+    "selective_scan_grad": ([ctypes.POINTER(_ScanGradArgs), _P], _I),
+    "selective_scan_grad_workspace": ([ctypes.POINTER(_ScanGradArgs)], _U64),
+    "selective_scan_step": ([ctypes.POINTER(_ScanStepArgs), _P], _I),
+}
+
+_seq_lib = None
+
+
+def _lib():
+    global _seq_lib
+    if _seq_lib is None:
+        L = lib()
+        for name, (argtypes, restype) in SIGNATURES.items():
+            fn = getattr(L, name)
+            fn.argtypes = argtypes
+            fn.restype = restype
+        _seq_lib = L
+    return _seq_lib
+
+
+# ---------------------------------------------------------------------- calls
+def _enqueue(x: torch.Tensor, stream, call):
+    """call(handle) with x's device current, on the stream asked for: torch allocates on that
+    stream inside, so memory that is let go is reused in its order."""
+    index = x.device.index
+    if stream is None and torch.cuda.current_device() == index:  # the usual case, without context managers
+        return call(_raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream)
+    with torch.cuda.device(index):
+        if stream is None:
+            return call(torch.cuda.current_stream().cuda_stream)
+        if not hasattr(stream, "cuda_stream"):
+            handle = int(stream)
+            if handle == 0:
+                stream = torch.cuda.default_stream()
+            else:
+                stream = torch.cuda.ExternalStream(handle)
+        elif stream.device.index != index:
+            raise ValueError("stream belongs to another device than the tensors")
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
+
+
+def _check(status: int, what: str):
+    if status != 0:
+        raise ScanError(status, what)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _on(x: torch.Tensor, name: str, t: torch.Tensor):
+    if t.device != x.device:
+        raise ValueError("%s must be on the device of the other tensors" % name)
+
+
+def _rows(t: torch.Tensor, name: str, shape=None, like: Optional[torch.Tensor] = None, inner: int = 1):
+    """Row stride of t, whose last `inner` dimensions are contiguous and whose leading ones are one flat run of rows."""
+    if shape is not None and t.shape != shape:
+        raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
+    if like is not None:
+        if t.dtype != like.dtype:
+            raise TypeError("%s must be %s" % (name, like.dtype))
+        if t.device != like.device:
+            raise ValueError("%s must be on the device of the other tensors" % name)
+    size, st = t.shape, t.stride()
+    n = len(size)
+    width = 1
+    for k in range(n - 1, n - 1 - inner, -1):
+        if size[k] != 1 and st[k] != width:
+            raise ValueError("the last dimension%s of %s must be contiguous" % ("s" if inner > 1 else "", name))
+        width *= size[k]
+    lead = n - inner
+    if lead == 0:
+        return width
+    row = st[lead - 1]
+    if size[lead - 1] <= 1:  # one row per sequence (or none): the sequences' stride is the rows'
+        if lead == 1 or size[0] <= 1:
+            return width if row < width else row
+        row = st[0]
+    elif lead == 2 and size[0] > 1 and st[0] != size[1] * row:
+        raise ValueError("the rows of %s must follow one another at one stride" % name)
+    if row < width and t.numel():
+        raise ValueError("the rows of %s overlap" % name)
+    return max(row, width)
+
+
+def _plain(t: torch.Tensor, name: str, shape, dtype, device):
+    if t.shape != tuple(shape):
+        raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s" % (name, dtype))
+    if t.device != device:
+        raise ValueError("%s must be on the device of the other tensors" % name)
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _x(x: torch.Tensor, name: str = "x"):
+    if x.dtype not in _DTYPE:
+        raise TypeError("%s must be float32, float16 or bfloat16" % name)
+    if not x.is_cuda:
+        raise ValueError("%s must be a device tensor" % name)
+
+
+def _lengths(x: torch.Tensor, seq_offsets):
+    """(rows, sequences, offsets pointer)"""
+    if seq_offsets is None:
+        if x.dim() != 3:
+            raise ValueError("x must be (B, L, D), or (rows, D) with seq_offsets")
+        return x.shape[0] * x.shape[1], x.shape[0], None
+    if x.dim() != 2:
+        raise ValueError("with seq_offsets x must be (rows, D)")
+    if seq_offsets.dtype != torch.int32 or seq_offsets.dim() != 1 or not seq_offsets.is_contiguous() or seq_offsets.shape[0] < 1:
+        raise TypeError("seq_offsets must be a contiguous 1-D int32 tensor of S + 1 values")
+    _on(x, "seq_offsets", seq_offsets)
+    return x.shape[0], seq_offsets.shape[0] - 1, seq_offsets.data_ptr()
+
+
+def _out(out, x: torch.Tensor, name: str, shape=None):
+    shape = x.shape if shape is None else shape
+    if out is None:
+        return torch.empty(shape, dtype=x.dtype, device=x.device)
+    if out.shape != shape:
+        raise ValueError("%s must have shape %s" % (name, tuple(shape)))
+    return out
+
+
+def _optional_state(state, shape, dtype, device):
+    """`state` may be a tensor to write into, or True for a new one."""
+    if state is None or state is False:
+        return None
+    return torch.empty(shape, dtype=dtype, device=device) if state is True else state
+
+
+# ---------------------------------------------------------------------- embedding
+def _tokens(tokens: torch.Tensor):
+    if tokens.dtype not in (torch.int32, torch.int64):
+        raise TypeError("tokens must be int32 or int64")
+    if not tokens.is_cuda or not tokens.is_contiguous():
+        raise ValueError("tokens must be a contiguous device tensor")
+    return tokens.element_size()
+
+
+def embedding_lookup(tokens: torch.Tensor, table: torch.Tensor, scale: float = 1.0, out: Optional[torch.Tensor] = None,
+                     stream=None):
+    """out[..., :] = scale * table[tokens[...]]; a token outside the table gives a row of zeros.
+
+    tokens: int32 or int64 of any shape; table: (V, D) float32, float16 or bfloat16."""
+    size = _tokens(tokens)
+    _x(table, "table")
+    if table.dim() != 2 or table.shape[0] < 1 or table.shape[1] < 1:
+        raise ValueError("table must be (V, D)")
+    _on(tokens, "table", table)
+    stride = _rows(table, "table")
+    shape = tokens.shape + table.shape[1:]
+
+    def call(handle):
+        y = _out(out, table, "out", shape)
+        if y.dtype != table.dtype or y.device != table.device or not y.is_contiguous():
+            raise ValueError("out must be a contiguous tensor of the table's type and device")
+        _check(_lib().embedding_lookup(_DTYPE[table.dtype], tokens.data_ptr(), size, tokens.numel(), table.data_ptr(), stride,
+                                       table.shape[0], table.shape[1], scale, y.data_ptr(), handle), "embedding_lookup")
+        return y
+
+    return _enqueue(tokens, stream, call)
+
+
+def embedding_grad(tokens: torch.Tensor, dout: torch.Tensor, n_rows: int, scale: float = 1.0,
+                   out: Optional[torch.Tensor] = None, accumulate: bool = False, stream=None):
+    """Gradient of ``embedding_lookup`` by the table: (n_rows, D), row v the scaled sum of dout over
+    the positions that hold token v, added up in 32 bits in a fixed order.
+
+    dout: tokens.shape + (D,).  out (n_rows, D): dout's type or float32; with ``accumulate`` the
+    gradient is added to it (rows without a position keep what they hold)."""
+    size = _tokens(tokens)
+    _x(dout, "dout")
+    if dout.dim() != tokens.dim() + 1 or dout.shape[:-1] != tokens.shape or dout.shape[-1] < 1:
+        raise ValueError("dout must have shape tokens.shape + (D,)")
+    _on(tokens, "dout", dout)
+    if dout.dim() > 3:
+        dout = dout.view(-1, dout.shape[-2], dout.shape[-1])
+    stride = _rows(dout, "dout")
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    n, d = tokens.numel(), dout.shape[-1]
+    if not 1 <= n_rows <= 1 << 24:
+        raise ValueError("n_rows must be in 1 .. 2^24")
+
+    def call(handle):
+        L = _lib()
+        g = _out(out, dout, "out", (n_rows, d))
+        if g.dtype not in (dout.dtype, torch.float32) or g.device != dout.device or not g.is_contiguous():
+            raise ValueError("out must be a contiguous tensor of dout's type or float32, on its device")
+        need = L.embedding_grad_workspace(n, n_rows, d)
+        ws = torch.empty(need, dtype=torch.uint8, device=dout.device)
+        _check(L.embedding_grad(_DTYPE[dout.dtype], _DTYPE[g.dtype], tokens.data_ptr(), size, n, dout.data_ptr(), stride,
+                                n_rows, d, scale, 1 if accumulate else 0, g.data_ptr(), ws.data_ptr(), need, handle),
+               "embedding_grad")
+        return g
+
+    return _enqueue(tokens, stream, call)
+
+
+# ---------------------------------------------------------------------- convolution
+class ConvGrads(NamedTuple):
+    """Gradients of causal_conv1d; dweight and dbias are float32, dbias and dinitial_state None where the input was."""
+    dx: torch.Tensor
+    dweight: torch.Tensor
+    dbias: Optional[torch.Tensor]
+    dinitial_state: Optional[torch.Tensor]
+
+
+def _conv_args(x, weight, bias, activation, seq_offsets, initial_state):
+    _x(x)
+    rows, seqs, offsets = _lengths(x, seq_offsets)
+    d = x.shape[-1]
+    if weight.dim() != 2 or weight.shape[0] != d or not 2 <= weight.shape[1] <= 4:
+        raise ValueError("weight must be (D, K) with K in 2 .. 4")
+    if activation not in _ACT:
+        raise ValueError("activation must be None or 'silu'")
+    k, wt = weight.shape[1], weight.dtype
+    if wt != x.dtype and wt != torch.float32:
+        raise TypeError("weight must be of x's type or float32")
+    a = _ConvArgs(dtype=_DTYPE[x.dtype], weight_dtype=_DTYPE[wt], activation=_ACT[activation], width=k, rows=rows, seqs=seqs,
+                  seq_offsets=offsets, channels=d, x=x.data_ptr(), x_stride=_rows(x, "x"),
+                  weight=_plain(weight, "weight", (d, k), wt, x.device))
+    if bias is not None:
+        a.bias = _plain(bias, "bias", (d,), wt, x.device)
+    if initial_state is not None:
+        a.initial_state = _plain(initial_state, "initial_state", (seqs, k - 1, d), x.dtype, x.device)
+    return a, seqs, k, d
+
+
+def causal_conv1d(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                  activation: Optional[str] = None, seq_offsets: Optional[torch.Tensor] = None,
+                  initial_state: Optional[torch.Tensor] = None, final_state=None, out: Optional[torch.Tensor] = None,
+                  stream=None):
+    """y[t] = act(bias + sum_k weight[:, k] * x[t - K + 1 + k]) along every sequence, per channel.
+
+    x: (B, L, D), or (rows, D) with seq_offsets; weight (D, K), K = 2 .. 4, and bias (D,) of x's
+    type or float32.  Inputs before a sequence come from initial_state (S, K - 1, D), oldest
+    first, else they are zero.  final_state: a tensor (S, K - 1, D) for the last K - 1 inputs of
+    every sequence, or True for a new one: (y, final_state) is returned then, else y.  Rows of y
+    that belong to no sequence are not written."""
+    a, seqs, k, d = _conv_args(x, weight, bias, activation, seq_offsets, initial_state)
+
+    def call(handle):
+        y = _out(out, x, "out")
+        a.y, a.y_stride = y.data_ptr(), _rows(y, "out", x.shape, x)
+        fin = _optional_state(final_state, (seqs, k - 1, d), x.dtype, x.device)
+        if fin is not None:
+            a.final_state = _plain(fin, "final_state", (seqs, k - 1, d), x.dtype, x.device)
+        _check(_lib().causal_conv1d(ctypes.byref(a), handle), "causal_conv1d")
+        return y if fin is None else (y, fin)
+
+    return _enqueue(x, stream, call)
+
+
+def causal_conv1d_grad(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                       activation: Optional[str] = None, seq_offsets: Optional[torch.Tensor] = None,
+                       initial_state: Optional[torch.Tensor] = None, dfinal_state: Optional[torch.Tensor] = None,
+                       dx: Optional[torch.Tensor] = None, stream=None) -> ConvGrads:
+    """Gradients of ``causal_conv1d`` (its arguments) for dy, and for dfinal_state if given.
+
+    dx may be given to write into (a slice of a wider tensor, say)."""
+    a, seqs, k, d = _conv_args(x, weight, bias, activation, seq_offsets, initial_state)
+    g = _ConvGradArgs(args=a, dy=dy.data_ptr(), dy_stride=_rows(dy, "dy", x.shape, x))
+    if dfinal_state is not None:
+        g.dfinal_state = _plain(dfinal_state, "dfinal_state", (seqs, k - 1, d), x.dtype, x.device)
+
+    def call(handle):
+        L = _lib()
+        ox = _out(dx, x, "dx")
+        g.dx, g.dx_stride = ox.data_ptr(), _rows(ox, "dx", x.shape, x)
+        dw = torch.empty(d, k, dtype=torch.float32, device=x.device)
+        db = None if bias is None else torch.empty(d, dtype=torch.float32, device=x.device)
+        di = None if initial_state is None else torch.empty_like(initial_state)
+        need = L.causal_conv1d_grad_workspace(ctypes.byref(a))
+        ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+        g.dweight, g.dbias, g.dinitial_state = dw.data_ptr(), _ptr(db), _ptr(di)
+        g.workspace, g.workspace_bytes = ws.data_ptr(), need
+        _check(L.causal_conv1d_grad(ctypes.byref(g), handle), "causal_conv1d_grad")
+        return ConvGrads(ox, dw, db, di)
+
+    return _enqueue(x, stream, call)
+
+
+def _slots(x, slots, n_slots):
+    if slots is None:
+        if n_slots < x.shape[0]:
+            raise ValueError("state has fewer slots than x has rows")
+        return None
+    return _plain(slots, "slots", (x.shape[0],), torch.int32, x.device)
+
+
+def causal_conv1d_step(x: torch.Tensor, state: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                       activation: Optional[str] = None, slots: Optional[torch.Tensor] = None,
+                       out: Optional[torch.Tensor] = None, stream=None):
+    """One token per row of x (rows, D): y from state[slots[i]] (its last K - 1 inputs) and x[i]; the
+    state (n_slots, K - 1, D) is shifted in place.
+
+    slots: int32 (rows,), distinct within a call; None: row i has slot i.  A row whose slot lies
+    outside the state is skipped: its row of y is not written."""
+    _x(x)
+    if x.dim() != 2 or state.dim() != 3 or weight.dim() != 2:
+        raise ValueError("x must be (rows, D), state (n_slots, K - 1, D), weight (D, K)")
+    if activation not in _ACT:
+        raise ValueError("activation must be None or 'silu'")
+    d, k, wt = x.shape[1], weight.shape[1], weight.dtype
+    if weight.shape[0] != d or not 2 <= k <= 4:
+        raise ValueError("weight must be (D, K) with K in 2 .. 4")
+    if wt != x.dtype and wt != torch.float32:
+        raise TypeError("weight must be of x's type or float32")
+    n = state.shape[0]
+    a = _ConvStepArgs(dtype=_DTYPE[x.dtype], weight_dtype=_DTYPE[wt], activation=_ACT[activation], width=k, rows=x.shape[0],
+                      n_slots=n, slots=_slots(x, slots, n), channels=d, x=x.data_ptr(), x_stride=_rows(x, "x"),
+                      weight=_plain(weight, "weight", (d, k), wt, x.device),
+                      bias=None if bias is None else _plain(bias, "bias", (d,), wt, x.device),
+                      state=_plain(state, "state", (n, k - 1, d), x.dtype, x.device))
+
+    def call(handle):
+        y = _out(out, x, "out")
+        a.y, a.y_stride = y.data_ptr(), _rows(y, "out", x.shape, x)
+        _check(_lib().causal_conv1d_step(ctypes.byref(a), handle), "causal_conv1d_step")
+        return y
+
+    return _enqueue(x, stream, call)
+
+
+# ---------------------------------------------------------------------- scan
+class ScanGrads(NamedTuple):
+    """Gradients of selective_scan; dA, dD, ddelta_bias and dinitial_state are float32, and None where the input was."""
+    dx: torch.Tensor
+    ddelta: torch.Tensor
+    dA: torch.Tensor
+    dB: torch.Tensor
+    dC: torch.Tensor
+    dD: Optional[torch.Tensor]
+    dz: Optional[torch.Tensor]
+    ddelta_bias: Optional[torch.Tensor]
+    dinitial_state: Optional[torch.Tensor]
+
+
+def _scan_inputs(a, x, delta, A, B, C, D, z, delta_bias, delta_softplus):
+    """Fills the fields that every form of the scan has; returns (channels, states)."""
+    if A.dim() != 2 or B.dim() < 2:
+        raise ValueError("A must be (D, N), B and C x.shape[:-1] + (groups, N)")
+    d, n = A.shape
+    groups = B.shape[-2]
+    if x.shape[-1] != d or not 1 <= n <= 64:
+        raise ValueError("A must be (D, N) with N in 1 .. 64")
+    if groups < 1 or d % groups:
+        raise ValueError("the groups of B and C must divide the channels")
+    bc = x.shape[:-1] + (groups, n)
+    a.dtype, a.delta_softplus = _DTYPE[x.dtype], 1 if delta_softplus else 0
+    a.channels, a.states, a.groups = d, n, groups
+    a.x, a.x_stride = x.data_ptr(), _rows(x, "x")
+    a.delta, a.delta_stride = delta.data_ptr(), _rows(delta, "delta", x.shape, x)
+    a.A = _plain(A, "A", (d, n), torch.float32, x.device)
+    a.B, a.b_stride = B.data_ptr(), _rows(B, "B", bc, x, 2)
+    a.C, a.c_stride = C.data_ptr(), _rows(C, "C", bc, x, 2)
+    if D is not None:
+        a.D = _plain(D, "D", (d,), torch.float32, x.device)
+    if z is not None:
+        a.z, a.z_stride = z.data_ptr(), _rows(z, "z", x.shape, x)
+    if delta_bias is not None:
+        a.delta_bias = _plain(delta_bias, "delta_bias", (d,), torch.float32, x.device)
+    return d, n
+
+
+def _scan_args(x, delta, A, B, C, D, z, delta_bias, delta_softplus, seq_offsets, initial_state):
+    _x(x)
+    a = _ScanArgs()
+    a.rows, a.seqs, a.seq_offsets = _lengths(x, seq_offsets)
+    d, n = _scan_inputs(a, x, delta, A, B, C, D, z, delta_bias, delta_softplus)
+    if initial_state is not None:
+        a.initial_state = _plain(initial_state, "initial_state", (a.seqs, d, n), torch.float32, x.device)
+    return a, (a.seqs, d, n)
+
+
+def selective_scan(x: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
+                   D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                   delta_bias: Optional[torch.Tensor] = None, delta_softplus: bool = False,
+                   seq_offsets: Optional[torch.Tensor] = None, initial_state: Optional[torch.Tensor] = None,
+                   final_state=None, save_for_grad: bool = False, out: Optional[torch.Tensor] = None, stream=None):
+    """Selective state-space scan along every sequence, per channel d (of group g) and state n:
+
+        dt = delta + delta_bias, through softplus if delta_softplus
+        h[t] = exp(dt A[d, n]) h[t-1] + dt x[t, d] B[t, g, n]
+        y[t, d] = (sum_n C[t, g, n] h[t] + D[d] x[t, d]) * silu(z[t, d])
+
+    x, delta, z: (B, L, D), or (rows, D) with seq_offsets; B, C: x.shape[:-1] + (G, N), all of x's
+    type; G divides D, N <= 64.  A (D, N), D (D,), delta_bias (D,) and the states (S, D, N) are
+    float32.  initial_state: h before every sequence (default zero).  final_state: a tensor for h
+    after every sequence, or True for a new one.  save_for_grad: also return the states that
+    ``selective_scan_grad`` starts from.  Returns y, followed by what was asked for."""
+    a, state = _scan_args(x, delta, A, B, C, D, z, delta_bias, delta_softplus, seq_offsets, initial_state)
+
+    def call(handle):
+        L = _lib()
+        y = _out(out, x, "out")
+        a.y, a.y_stride = y.data_ptr(), _rows(y, "out", x.shape, x)
+        got = [y]
+        fin = _optional_state(final_state, state, torch.float32, x.device)
+        if fin is not None:
+            a.final_state = _plain(fin, "final_state", state, torch.float32, x.device)
+            got.append(fin)
+        if save_for_grad:
+            saved = torch.empty(L.selective_scan_saved(ctypes.byref(a)), dtype=torch.float32, device=x.device)
+            a.saved = saved.data_ptr()
+            got.append(saved)
+        need = L.selective_scan_workspace(ctypes.byref(a))
+        ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+        a.workspace, a.workspace_bytes = ws.data_ptr(), need
+        _check(L.selective_scan(ctypes.byref(a), handle), "selective_scan")
+        return y if len(got) == 1 else tuple(got)
+
+    return _enqueue(x, stream, call)
+
+
+def selective_scan_grad(dy: torch.Tensor, x: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                        C: torch.Tensor, D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                        delta_bias: Optional[torch.Tensor] = None, delta_softplus: bool = False,
+                        seq_offsets: Optional[torch.Tensor] = None, initial_state: Optional[torch.Tensor] = None,
+                        dfinal_state: Optional[torch.Tensor] = None, saved: Optional[torch.Tensor] = None,
+                        dx: Optional[torch.Tensor] = None, dz: Optional[torch.Tensor] = None, stream=None) -> ScanGrads:
+    """Gradients of ``selective_scan`` (its arguments) for dy, and for dfinal_state if given.
+
+    saved: what ``selective_scan(..., save_for_grad=True)`` returned for the same inputs; without
+    it the states are scanned again.  dx and dz may be given to write into (two slices of one
+    tensor, say)."""
+    a, state = _scan_args(x, delta, A, B, C, D, z, delta_bias, delta_softplus, seq_offsets, initial_state)
+    g = _ScanGradArgs(dy=dy.data_ptr(), dy_stride=_rows(dy, "dy", x.shape, x))
+    if dfinal_state is not None:
+        g.dfinal_state = _plain(dfinal_state, "dfinal_state", state, torch.float32, x.device)
+    if dz is not None and z is None:
+        raise ValueError("dz given without z")
+
+    def call(handle):
+        L = _lib()
+        f32 = dict(dtype=torch.float32, device=x.device)
+        need_saved = L.selective_scan_saved(ctypes.byref(a))
+        states = saved
+        if states is None:
+            states = torch.empty(need_saved, **f32)
+            need = L.selective_scan_workspace(ctypes.byref(a))
+            ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+            a.saved, a.workspace, a.workspace_bytes = states.data_ptr(), ws.data_ptr(), need
+            _check(L.selective_scan(ctypes.byref(a), handle), "selective_scan")
+        a.saved = _plain(states, "saved", (need_saved,), torch.float32, x.device)
+        ox = _out(dx, x, "dx")
+        od = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        oz = None if z is None else _out(dz, x, "dz")
+        oB = torch.empty(B.shape, dtype=x.dtype, device=x.device)
+        oC = torch.empty(C.shape, dtype=x.dtype, device=x.device)
+        oA = torch.empty(A.shape, **f32)
+        oD = None if D is None else torch.empty(D.shape, **f32)
+        ob = None if delta_bias is None else torch.empty(delta_bias.shape, **f32)
+        oi = None if initial_state is None else torch.empty(state, **f32)
+        g.args = a
+        g.dx, g.dx_stride = ox.data_ptr(), _rows(ox, "dx", x.shape, x)
+        g.ddelta, g.ddelta_stride = od.data_ptr(), _rows(od, "ddelta")
+        if oz is not None:
+            g.dz, g.dz_stride = oz.data_ptr(), _rows(oz, "dz", x.shape, x)
+        g.dB, g.db_stride = oB.data_ptr(), _rows(oB, "dB", inner=2)
+        g.dC, g.dc_stride = oC.data_ptr(), _rows(oC, "dC", inner=2)
+        g.dA, g.dD, g.ddelta_bias, g.dinitial_state = oA.data_ptr(), _ptr(oD), _ptr(ob), _ptr(oi)
+        need = L.selective_scan_grad_workspace(ctypes.byref(g))
+        ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+        g.args.workspace, g.args.workspace_bytes = ws.data_ptr(), need
+        _check(L.selective_scan_grad(ctypes.byref(g), handle), "selective_scan_grad")
+        return ScanGrads(ox, od, oA, oB, oC, oD, oz, ob, oi)
+
+    return _enqueue(x, stream, call)
+
+
+def selective_scan_step(x: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
+                        state: torch.Tensor, D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                        delta_bias: Optional[torch.Tensor] = None, delta_softplus: bool = False,
+                        slots: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, stream=None):
+    """One token per row: one step of ``selective_scan``'s recurrence from state[slots[i]], which is
+    updated in place.
+
+    x, delta, z: (rows, D); B, C: (rows, G, N); state: (n_slots, D, N) float32.  slots as in
+    ``causal_conv1d_step``."""
+    _x(x)
+    if x.dim() != 2 or state.dim() != 3:
+        raise ValueError("x must be (rows, D), state (n_slots, D, N)")
+    a = _ScanStepArgs()
+    d, n = _scan_inputs(a, x, delta, A, B, C, D, z, delta_bias, delta_softplus)
+    a.rows, a.n_slots = x.shape[0], state.shape[0]
+    a.slots = _slots(x, slots, state.shape[0])
+    a.state = _plain(state, "state", (state.shape[0], d, n), torch.float32, x.device)
+
+    def call(handle):
+        y = _out(out, x, "out")
+        a.y, a.y_stride = y.data_ptr(), _rows(y, "out", x.shape, x)
+        _check(_lib().selective_scan_step(ctypes.byref(a), handle), "selective_scan_step")
+        return y
+
+    return _enqueue(x, stream, call)
