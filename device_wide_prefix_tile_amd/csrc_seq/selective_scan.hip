@@ -36,9 +36,7 @@
 namespace dwpt_seq {
 namespace {
 
-constexpr int kWaves = 4;             // wavefronts per workgroup
-constexpr int kWaveChannels = 16;     // channels per wavefront
-constexpr int kWgChannels = kWaves * kWaveChannels;
+constexpr int kWgChannels = 64;       // channels per workgroup
 constexpr uint32_t kMaxChannels = 1u << 20;
 constexpr uint32_t kEmptyStep = 32;   // workgroups per channel block that look for empty sequences
 
@@ -86,16 +84,16 @@ struct Inputs {
     const void *x, *delta, *B, *C, *z;
     int64_t x_stride, delta_stride, b_stride, c_stride, z_stride;
     const float *A, *D, *delta_bias, *initial;
-    int softplus, vec, vec_bc;  // vec: 16-byte pieces of x, delta, z (and y ...); vec_bc: of B and C
+    int softplus, vec;  // vec: every row of the inputs and outputs consists of whole 16-byte pieces
 };
 
 // ------------------------------------------------------------ tiles
-// How the lanes share a tile of TT rows by 16 channels: `pieces` 16-byte pieces each.
-template <typename T, int TT>
+// How the lanes share a tile of TT rows by CW channels: PIECES 16-byte pieces each.
+template <typename T, int TT, int CW, bool VEC>
 struct Tile {
     static constexpr int V = 16 / sizeof(T);
-    static constexpr int LPR = kWaveChannels / V;  // lanes per row
-    static constexpr int RPL = 64 / LPR;           // rows per piece
+    static constexpr int LPR = CW / V;    // lanes per row
+    static constexpr int RPL = 64 / LPR;  // rows per piece
     static constexpr int PIECES = TT > RPL ? TT / RPL : 1;
     using P = Pack<T, V>;
 
@@ -104,7 +102,7 @@ struct Tile {
 
     // Rows [r0, r0 + len), channels [c0, c0 + nch) of p; zeros elsewhere.
     __device__ static __forceinline__ void load(P (&out)[PIECES], const void* base, int64_t stride, uint32_t r0, int len,
-                                                uint32_t c0, int nch, int vec, int lane)
+                                                uint32_t c0, int nch, int lane)
     {
         const T* p = static_cast<const T*>(base);
 #pragma unroll
@@ -113,7 +111,7 @@ struct Tile {
             out[i] = zero_pack<T, V>();
             if (r < len && c < nch) {
                 const T* q = p + (int64_t)(r0 + r) * stride + c0 + c;
-                if (vec) {
+                if (VEC) {
                     out[i] = load_pack<T, V>(q);
                 } else {
 #pragma unroll
@@ -124,13 +122,13 @@ struct Tile {
         }
     }
     __device__ static __forceinline__ void store(void* base, int64_t stride, uint32_t r0, int len, uint32_t c0, int nch,
-                                                 int vec, int lane, int i, const float (&f)[V])
+                                                 int lane, int i, const float (&f)[V])
     {
         const int r = row(i, lane), c = col(lane);
         if (r >= len || c >= nch) return;
         T* q = static_cast<T*>(base) + (int64_t)(r0 + r) * stride + c0 + c;
         const P p = pack<T, V>(f);
-        if (vec) {
+        if (VEC) {
             *reinterpret_cast<P*>(q) = p;
         } else {
 #pragma unroll
@@ -141,7 +139,7 @@ struct Tile {
 };
 
 // A tile of TT rows by NP states of B or C, shared by LANES lanes.
-template <typename T, int TT, int NP, int LANES>
+template <typename T, int TT, int NP, int LANES, bool VEC>
 struct StateTile {
     static constexpr int V = 16 / sizeof(T);
     static constexpr int LPR = NP / V;
@@ -150,7 +148,7 @@ struct StateTile {
     using P = Pack<T, V>;
 
     __device__ static __forceinline__ void load(P (&out)[PIECES], const void* base, int64_t stride, uint32_t r0, int len,
-                                                uint32_t at, int states, int vec, int lane)
+                                                uint32_t at, int states, int lane)
     {
         const T* p = static_cast<const T*>(base);
 #pragma unroll
@@ -159,7 +157,7 @@ struct StateTile {
             out[i] = zero_pack<T, V>();
             if (k < TOTAL && r < len && n < states) {
                 const T* q = p + (int64_t)(r0 + r) * stride + at + n;
-                if (vec) {
+                if (VEC) {
                     out[i] = load_pack<T, V>(q);
                 } else {
 #pragma unroll
@@ -205,11 +203,13 @@ __device__ __forceinline__ float quad_transpose_sum(const float (&v)[4], int q)
     return keep + dpp<kQuadXor2>(give);
 }
 
-// Where a wavefront stands: its channels and its lane's part of them.
+// Where a wavefront stands: its CW channels, and its lane's part of them (channel d, and d + 16 ...).
+template <int CW>
 struct Place {
-    int lane, w, d, q;       // channel and quarter of the lane
-    uint32_t group, c0;      // first channel of the wavefront
-    int nch;                 // channels of the wavefront (0: none)
+    static constexpr int CH = CW / 16;  // channels per lane
+    int lane, w, d, q;                  // channel and quarter of the lane
+    uint32_t group, c0;                 // first channel of the wavefront
+    int nch;                            // channels of the wavefront (0: none)
     __device__ __forceinline__ Place(const Plan& p, uint32_t block)
     {
         lane = threadIdx.x & 63;
@@ -217,64 +217,85 @@ struct Place {
         d = lane >> 2;
         q = lane & 3;
         group = block / p.blocks_per_group;
-        const uint32_t first = (block % p.blocks_per_group) * kWgChannels + w * kWaveChannels;
+        const uint32_t first = (block % p.blocks_per_group) * kWgChannels + w * CW;
         c0 = group * p.group_channels + first;
-        nch = first < p.group_channels ? (int)min(p.group_channels - first, (uint32_t)kWaveChannels) : 0;
+        nch = first < p.group_channels ? (int)min(p.group_channels - first, (uint32_t)CW) : 0;
     }
 };
 
-// The lane's S states of the (channels x states) array p at channel c0 + d; zeros where padded.
-template <int S>
-__device__ __forceinline__ void load_states(const float* __restrict__ p, const Plan& pl, const Place& me, float (&f)[S],
-                                            float scale = 1.0f)
-{
+// The lane's S states of each of its channels.
+template <int S, int CH>
+struct LaneStates {
+    float v[CH][S];
+
+    __device__ __forceinline__ void zero()
+    {
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-        const uint32_t n = me.q * S + s;
-        f[s] = me.d < me.nch && n < pl.states ? p[(size_t)(me.c0 + me.d) * pl.states + n] * scale : 0.0f;
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int i = 0; i < S; ++i) v[c][i] = 0.0f;
     }
-}
-template <int S>
-__device__ __forceinline__ void store_states(float* __restrict__ p, const Plan& pl, const Place& me, const float (&f)[S])
-{
+    // from and to an array (channels x states); zeros where padded
+    __device__ __forceinline__ void load(const float* __restrict__ p, const Plan& pl, const Place<16 * CH>& me,
+                                         float scale = 1.0f)
+    {
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-        const uint32_t n = me.q * S + s;
-        if (me.d < me.nch && n < pl.states) p[(size_t)(me.c0 + me.d) * pl.states + n] = f[s];
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int i = 0; i < S; ++i) {
+                const uint32_t n = me.q * S + i;
+                const int ch = me.d + 16 * c;
+                v[c][i] = ch < me.nch && n < pl.states ? p[(size_t)(me.c0 + ch) * pl.states + n] * scale : 0.0f;
+            }
     }
-}
-// The same in the workspace, padded to NP states per channel: [index][channels][NP].
-template <int S>
-__device__ __forceinline__ void load_padded(const float* __restrict__ p, const Plan& pl, const Place& me, size_t index,
-                                            float (&f)[S])
-{
-    if (me.d < me.nch) {
-        lds_states<S>(p + (index * pl.channels + me.c0 + me.d) * (4 * S) + me.q * S, f);
-    } else {
+    __device__ __forceinline__ void store(float* __restrict__ p, const Plan& pl, const Place<16 * CH>& me) const
+    {
 #pragma unroll
-        for (int s = 0; s < S; ++s) f[s] = 0.0f;
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int i = 0; i < S; ++i) {
+                const uint32_t n = me.q * S + i;
+                const int ch = me.d + 16 * c;
+                if (ch < me.nch && n < pl.states) p[(size_t)(me.c0 + ch) * pl.states + n] = v[c][i];
+            }
     }
-}
-template <int S>
-__device__ __forceinline__ void store_padded(float* __restrict__ p, const Plan& pl, const Place& me, size_t index,
-                                             const float (&f)[S])
-{
-    if (me.d >= me.nch) return;
-    float* o = p + (index * pl.channels + me.c0 + me.d) * (4 * S) + me.q * S;
-#pragma unroll
-    for (int s = 0; s < S; s += 4) *reinterpret_cast<f32x4*>(o + s) = f32x4{f[s], f[s + 1], f[s + 2], f[s + 3]};
-}
-template <int S>
-__device__ __forceinline__ void start_state(const float* __restrict__ initial, const Plan& pl, const Place& me, uint32_t s,
-                                            float (&h)[S])
-{
-    if (initial) {
-        load_states<S>(initial + (size_t)s * pl.channels * pl.states, pl, me, h);
-    } else {
-#pragma unroll
-        for (int i = 0; i < S; ++i) h[i] = 0.0f;
+    // the state of sequence s in an array of them, or zero without one
+    __device__ __forceinline__ void start(const float* __restrict__ p, const Plan& pl, const Place<16 * CH>& me, uint32_t s)
+    {
+        if (p)
+            load(p + (size_t)s * pl.channels * pl.states, pl, me);
+        else
+            zero();
     }
-}
+    // from and to the workspace, padded to 4 S states per channel: [index][channels][4 S]
+    __device__ __forceinline__ void load_padded(const float* __restrict__ p, const Plan& pl, const Place<16 * CH>& me,
+                                                size_t index)
+    {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int ch = me.d + 16 * c;
+            if (ch < me.nch) {
+                lds_states<S>(p + (index * pl.channels + me.c0 + ch) * (4 * S) + me.q * S, v[c]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < S; ++i) v[c][i] = 0.0f;
+            }
+        }
+    }
+    __device__ __forceinline__ void store_padded(float* __restrict__ p, const Plan& pl, const Place<16 * CH>& me,
+                                                 size_t index) const
+    {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int ch = me.d + 16 * c;
+            if (ch >= me.nch) continue;
+            float* o = p + (index * pl.channels + me.c0 + ch) * (4 * S) + me.q * S;
+#pragma unroll
+            for (int i = 0; i < S; i += 4)
+                *reinterpret_cast<f32x4*>(o + i) = f32x4{v[c][i], v[c][i + 1], v[c][i + 2], v[c][i + 3]};
+        }
+    }
+};
 
 // What later spans need of a span: its state from a zero start (or its gradient, backwards) and
 // the sum of dt over the rows.
@@ -283,50 +304,76 @@ struct SpanTotals {
     float* dt_sum;  // [span][channels]
 };
 // h = the state behind spans [first, last], joined in order (`step` 1) or in reverse (-1).
-template <int S>
-__device__ __forceinline__ void join_spans(const SpanTotals& t, const Plan& pl, const Place& me, uint32_t first,
-                                           uint32_t last, int step, const float (&A2)[S], float (&h)[S])
+template <int S, int CH>
+__device__ __forceinline__ void join_spans(const SpanTotals& t, const Plan& pl, const Place<16 * CH>& me, uint32_t first,
+                                           uint32_t last, int step, const LaneStates<S, CH>& A2, LaneStates<S, CH>& h)
 {
-    load_padded<S>(t.states, pl, me, first, h);
+    h.load_padded(t.states, pl, me, first);
+#pragma unroll 4
     while (first != last) {
         first += step;
-        const float sum = me.d < me.nch ? t.dt_sum[(size_t)first * pl.channels + me.c0 + me.d] : 0.0f;
-        float e[S];
-        load_padded<S>(t.states, pl, me, first, e);
+        LaneStates<S, CH> e;
+        e.load_padded(t.states, pl, me, first);
 #pragma unroll
-        for (int s = 0; s < S; ++s) h[s] = fmaf(exp2_fast(A2[s] * sum), h[s], e[s]);
+        for (int c = 0; c < CH; ++c) {
+            const int ch = me.d + 16 * c;
+            const float sum = ch < me.nch ? t.dt_sum[(size_t)first * pl.channels + me.c0 + ch] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < S; ++i) h.v[c][i] = fmaf(exp2_fast(A2.v[c][i] * sum), h.v[c][i], e.v[c][i]);
+        }
     }
 }
 
 // dt of one element: raw = delta + bias
 __device__ __forceinline__ float step_size(float raw, int sp) { return sp ? softplus(raw) : raw; }
 
+// dt of V elements of a row; of a row behind the tile, dt = 0 (softplus(-inf)).
+template <int V>
+__device__ __forceinline__ void step_sizes(const float (&delta)[V], const float (&bias)[V], int sp, bool in_tile,
+                                           float (&dt)[V])
+{
+    const float none = sp ? -INFINITY : 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) dt[j] = in_tile ? delta[j] + bias[j] : none;
+    if (sp) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) dt[j] = softplus(dt[j]);
+    }
+}
+
 // ------------------------------------------------------------ forward
+// A lane has two channels: the B and C that it reads from LDS serve both (with one, those reads
+// keep the LDS busy for three quarters of the time that the vector units need).
+constexpr int kFwdChannels = 32;
+constexpr int kFwdWaves = kWgChannels / kFwdChannels;
+
 // TOTALS: the span's totals only.
-template <typename T, int S, bool TOTALS>
-__global__ __launch_bounds__(kWaves * 64) void scan_kernel(Plan pl, Inputs in, SpanTotals totals, void* y,
-                                                           int64_t y_stride, float* final_state, float* saved)
+template <typename T, int S, bool VEC, bool TOTALS>
+__global__ __launch_bounds__(kFwdWaves * 64) void scan_kernel(Plan pl, Inputs in, SpanTotals totals, void* y,
+                                                              int64_t y_stride, float* final_state, float* saved)
 {
     using C = Cfg<S>;
-    constexpr int TT = C::TT, NP = C::NP;
-    using X = Tile<T, TT>;
-    using BC = StateTile<T, TT, NP, 64>;
+    constexpr int TT = C::TT, NP = C::NP, CW = kFwdChannels, CH = CW / 16;
+    using X = Tile<T, TT, CW, VEC>;
+    using BC = StateTile<T, TT, NP, 64, VEC>;
     constexpr int V = X::V;
-    __shared__ __align__(16) f32x2 s_dt[kWaves][TT * kWaveChannels];
-    __shared__ __align__(16) float s_b[kWaves][TT * NP];
-    __shared__ __align__(16) float s_c[TOTALS ? 1 : kWaves][TOTALS ? 4 : TT * NP];
-    __shared__ __align__(16) float s_y[TOTALS ? 1 : kWaves][TOTALS ? 4 : TT * kWaveChannels];
+    // two rows more than a tile: the walk over the rows reads two ahead
+    __shared__ __align__(16) f32x2 s_dt[kFwdWaves][(TT + 2) * CW];
+    __shared__ __align__(16) float s_b[kFwdWaves][(TT + 2) * NP];
+    __shared__ __align__(16) float s_c[TOTALS ? 1 : kFwdWaves][TOTALS ? 4 : (TT + 2) * NP];
+    __shared__ __align__(16) float s_y[TOTALS ? 1 : kFwdWaves][TOTALS ? 4 : TT * CW];
+    __shared__ __align__(16) float s_par[kFwdWaves][2 * CW];  // delta_bias and D of the wavefront's channels
 
     const uint32_t block = blockIdx.x % pl.blocks, span = blockIdx.x / pl.blocks;
-    const Place me(pl, block);
+    const Place<CW> me(pl, block);
     if (me.nch == 0) return;
     if (span >= pl.spans) {
         // behind the spans: the final states of empty sequences
         for (uint32_t s = span - pl.spans; s < pl.seqs.count; s += kEmptyStep) {
             if (pl.seqs.end(s) > pl.seqs.start(s)) continue;
-            float h[S];
-            start_state<S>(in.initial, pl, me, s, h);
-            store_states<S>(final_state + (size_t)s * pl.channels * pl.states, pl, me, h);
+            LaneStates<S, CH> h;
+            h.start(in.initial, pl, me, s);
+            h.store(final_state + (size_t)s * pl.channels * pl.states, pl, me);
         }
         return;
     }
@@ -336,16 +383,15 @@ __global__ __launch_bounds__(kWaves * 64) void scan_kernel(Plan pl, Inputs in, S
     float* const lb = s_b[me.w];
     float* const lc = s_c[TOTALS ? 0 : me.w];
     float* const ly = s_y[TOTALS ? 0 : me.w];
-
-    float A2[S], h[S];
-    load_states<S>(in.A, pl, me, A2, kLog2e);
-    float bias[V], skip[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const int c = X::col(me.lane) + j;
-        bias[j] = in.delta_bias && c < me.nch ? in.delta_bias[me.c0 + c] : 0.0f;
-        skip[j] = in.D && c < me.nch ? in.D[me.c0 + c] : 0.0f;
+    float* const bias = s_par[me.w] + X::col(me.lane);
+    float* const skip = bias + CW;
+    if (me.lane < 2 * CW) {
+        const int c = me.lane % CW;
+        const float* p = me.lane < CW ? in.delta_bias : in.D;
+        s_par[me.w][me.lane] = p && c < me.nch ? p[me.c0 + c] : 0.0f;
     }
+    LaneStates<S, CH> A2, h;
+    A2.load(in.A, pl, me, kLog2e);
     const uint32_t bc_at = me.group * pl.states;
 
     uint32_t pos = r0, st, en;
@@ -357,24 +403,22 @@ __global__ __launch_bounds__(kWaves * 64) void scan_kernel(Plan pl, Inputs in, S
             pos = e;
             continue;
         }
-        if (pos == st) {
-            start_state<S>(in.initial, pl, me, (uint32_t)s, h);
-        } else if (TOTALS) {
-#pragma unroll
-            for (int i = 0; i < S; ++i) h[i] = 0.0f;
-        } else {
-            join_spans<S>(totals, pl, me, pl.span_of(span, st), span - 1, 1, A2, h);
-        }
-        float sum = 0.0f;
+        if (pos == st)
+            h.start(in.initial, pl, me, (uint32_t)s);
+        else if (TOTALS)
+            h.zero();
+        else
+            join_spans<S, CH>(totals, pl, me, pl.span_of(span, st), span - 1, 1, A2, h);
+        float sum[CH] = {};
         typename X::P px[X::PIECES], pd[X::PIECES], pz[X::PIECES];
         typename BC::P pb[BC::PIECES], pc[BC::PIECES];
         const auto fetch = [&](uint32_t at, int len) {
-            X::load(px, in.x, in.x_stride, at, len, me.c0, me.nch, in.vec, me.lane);
-            X::load(pd, in.delta, in.delta_stride, at, len, me.c0, me.nch, in.vec, me.lane);
-            BC::load(pb, in.B, in.b_stride, at, len, bc_at, pl.states, in.vec_bc, me.lane);
+            X::load(px, in.x, in.x_stride, at, len, me.c0, me.nch, me.lane);
+            X::load(pd, in.delta, in.delta_stride, at, len, me.c0, me.nch, me.lane);
+            BC::load(pb, in.B, in.b_stride, at, len, bc_at, pl.states, me.lane);
             if (!TOTALS) {
-                BC::load(pc, in.C, in.c_stride, at, len, bc_at, pl.states, in.vec_bc, me.lane);
-                if (in.z) X::load(pz, in.z, in.z_stride, at, len, me.c0, me.nch, in.vec, me.lane);
+                BC::load(pc, in.C, in.c_stride, at, len, bc_at, pl.states, me.lane);
+                if (in.z) X::load(pz, in.z, in.z_stride, at, len, me.c0, me.nch, me.lane);
             }
         };
         const auto tile_len = [&](uint32_t at) { return (int)(min(r0 + ((at - r0) / TT + 1) * TT, e) - at); };
@@ -382,22 +426,24 @@ __global__ __launch_bounds__(kWaves * 64) void scan_kernel(Plan pl, Inputs in, S
         fetch(pos, len);
         while (true) {
             if (!TOTALS && saved && (pos - r0) % TT == 0)
-                store_padded<S>(saved, pl, me, (size_t)span * pl.tiles_per_span + (pos - r0) / TT, h);
+                h.store_padded(saved, pl, me, (size_t)span * pl.tiles_per_span + (pos - r0) / TT);
             // (dt, dt x) of the tile; rows behind len keep the state: dt = 0
-            float xf[X::PIECES][V], zf[X::PIECES][V];
+            typename X::P cx[X::PIECES], cz[X::PIECES];
+            wave_sync();
 #pragma unroll
             for (int i = 0; i < X::PIECES; ++i) {
-                float df[V];
-                unpack(px[i], xf[i]);
+                float xf[V], df[V], bf[V];
+                cx[i] = px[i];
+                if (!TOTALS) cz[i] = pz[i];
+                unpack(cx[i], xf);
                 unpack(pd[i], df);
-                if (!TOTALS && in.z) unpack(pz[i], zf[i]);
                 const int r = X::row(i, me.lane);
                 if (TT % X::RPL && r >= TT) continue;
+                lds_states<V>(bias, bf);
+                step_sizes<V>(df, bf, in.softplus, r < len, df);
+                f32x2* const out = dt + r * CW + X::col(me.lane);
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float v = r < len ? step_size(df[j] + bias[j], in.softplus) : 0.0f;
-                    dt[r * kWaveChannels + X::col(me.lane) + j] = f32x2{v, v * xf[i][j]};
-                }
+                for (int j = 0; j < V; ++j) out[j] = f32x2{df[j], df[j] * xf[j]};
             }
             BC::put(lb, pb, me.lane);
             if (!TOTALS) BC::put(lc, pc, me.lane);
@@ -408,23 +454,50 @@ __global__ __launch_bounds__(kWaves * 64) void scan_kernel(Plan pl, Inputs in, S
                 next_len = tile_len(next);
                 fetch(next, next_len);
             }
-            for (int t = 0; t < len; t += 4) {
-                float part[4];
+            // four rows at a time, the LDS reads two rows ahead of their use
+            struct Two {
+                f32x2 v[2][CH];
+                float b[2][S], c[2][S];
+            };
+            const auto read = [&](Two& w, int t) {
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const f32x2 v = dt[(t + u) * kWaveChannels + me.d];
-                    float b[S], c[S];
-                    lds_states<S>(lb + (t + u) * NP + me.q * S, b);
-                    if (!TOTALS) lds_states<S>(lc + (t + u) * NP + me.q * S, c);
-                    if (TOTALS) sum += v[0];
-                    part[u] = 0.0f;
+                for (int u = 0; u < 2; ++u) {
 #pragma unroll
-                    for (int i = 0; i < S; ++i) {
-                        h[i] = fmaf(exp2_fast(v[0] * A2[i]), h[i], v[1] * b[i]);
-                        if (!TOTALS) part[u] = fmaf(c[i], h[i], part[u]);
-                    }
+                    for (int c = 0; c < CH; ++c) w.v[u][c] = dt[(t + u) * CW + me.d + 16 * c];
+                    lds_states<S>(lb + (t + u) * NP + me.q * S, w.b[u]);
+                    if (!TOTALS) lds_states<S>(lc + (t + u) * NP + me.q * S, w.c[u]);
                 }
-                if (!TOTALS) ly[(t + me.q) * kWaveChannels + me.d] = quad_transpose_sum(part, me.q);
+            };
+            const auto walk = [&](const Two& w, float (*part)[4], int at) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int c = 0; c < CH; ++c) {
+                        const f32x2 v = w.v[u][c];
+                        if (TOTALS) sum[c] += v[0];
+                        float p = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < S; ++i) {
+                            h.v[c][i] = fmaf(exp2_fast(v[0] * A2.v[c][i]), h.v[c][i], v[1] * w.b[u][i]);
+                            if (!TOTALS) p = i ? fmaf(w.c[u][i], h.v[c][i], p) : w.c[u][i] * h.v[c][i];
+                        }
+                        part[c][at + u] = p;
+                    }
+            };
+            Two w0, w1;
+            read(w0, 0);
+            for (int t = 0; t < len; t += 4) {
+                float part[CH][4];
+                read(w1, t + 2);
+                __builtin_amdgcn_sched_barrier(0);
+                walk(w0, part, 0);
+                read(w0, t + 4);
+                __builtin_amdgcn_sched_barrier(0);
+                walk(w1, part, 2);
+                if (!TOTALS) {
+#pragma unroll
+                    for (int c = 0; c < CH; ++c) ly[(t + me.q) * CW + me.d + 16 * c] = quad_transpose_sum(part[c], me.q);
+                }
             }
             if (!TOTALS && y) {
                 wave_sync();
@@ -432,38 +505,47 @@ __global__ __launch_bounds__(kWaves * 64) void scan_kernel(Plan pl, Inputs in, S
                 for (int i = 0; i < X::PIECES; ++i) {
                     const int r = X::row(i, me.lane);
                     if (r >= len) continue;
-                    float f[V];
+                    float f[V], xf[V], zf[V], df[V];
+                    opaque(cx[i]);
+                    unpack(cx[i], xf);
+                    unpack(cz[i], zf);
+                    lds_states<V>(skip, df);
+                    lds_states<V>(ly + r * CW + X::col(me.lane), f);
 #pragma unroll
                     for (int j = 0; j < V; ++j) {
-                        f[j] = fmaf(skip[j], xf[i][j], ly[r * kWaveChannels + X::col(me.lane) + j]);
-                        if (in.z) f[j] *= silu(zf[i][j]);
+                        f[j] = fmaf(df[j], xf[j], f[j]);
+                        if (in.z) f[j] *= silu(zf[j]);
                     }
-                    X::store(y, y_stride, pos, len, me.c0, me.nch, in.vec, me.lane, i, f);
+                    X::store(y, y_stride, pos, len, me.c0, me.nch, me.lane, i, f);
                 }
             }
-            wave_sync();
             pos = next;
             if (pos >= e) break;
             len = next_len;
         }
         if (TOTALS) {
-            store_padded<S>(totals.states, pl, me, span, h);
-            if (me.q == 0 && me.d < me.nch) totals.dt_sum[(size_t)span * pl.channels + me.c0 + me.d] = sum;
+            h.store_padded(totals.states, pl, me, span);
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+                if (me.q == 0 && me.d + 16 * c < me.nch)
+                    totals.dt_sum[(size_t)span * pl.channels + me.c0 + me.d + 16 * c] = sum[c];
         } else if (final_state && en <= r1) {
-            store_states<S>(final_state + (size_t)s * pl.channels * pl.states, pl, me, h);
+            h.store(final_state + (size_t)s * pl.channels * pl.states, pl, me);
         }
     }
 }
 
 // ------------------------------------------------------------ single tokens
-// A wavefront takes 16 channels of one row, lanes as above.
+// A wavefront takes 16 channels of one row.
+constexpr int kGradWaves = kWgChannels / 16;
+
 template <typename T, int S>
-__global__ __launch_bounds__(kWaves * 64) void scan_step_kernel(Plan pl, Inputs in, const int32_t* __restrict__ slots,
+__global__ __launch_bounds__(kGradWaves * 64) void scan_step_kernel(Plan pl, Inputs in, const int32_t* __restrict__ slots,
                                                                 uint32_t n_slots, float* __restrict__ state,
                                                                 T* __restrict__ y, int64_t y_stride)
 {
     const uint32_t block = blockIdx.x % pl.blocks, r = blockIdx.x / pl.blocks;
-    const Place me(pl, block);
+    const Place<16> me(pl, block);
     if (me.d >= me.nch) return;
     const int32_t slot = slots ? slots[r] : (int32_t)r;
     if (slot < 0 || (uint32_t)slot >= n_slots) return;
@@ -473,7 +555,7 @@ __global__ __launch_bounds__(kWaves * 64) void scan_step_kernel(Plan pl, Inputs 
     const T* bp = static_cast<const T*>(in.B) + (int64_t)r * in.b_stride + me.group * pl.states + me.q * S;
     const T* cp = static_cast<const T*>(in.C) + (int64_t)r * in.c_stride + me.group * pl.states + me.q * S;
     float h[S], a[S], b[S], cc[S];
-    const bool whole = in.vec_bc;  // states = 4 S, state and A 16-byte aligned
+    const bool whole = in.vec;  // states = 4 S, state and A 16-byte aligned
 #pragma unroll
     for (int i = 0; i < S; i += 4) {
         if (whole) {
@@ -544,19 +626,19 @@ struct Grads {
 //   dh = dv C + g;  g' = a dh         (dv = dy silu(z))
 // Totals of a span for the spans before it: g at its first row from g = 0 behind its last (or from
 // dfinal where the sequence ends in it), and the sum of dt.
-template <typename T, int S>
-__global__ __launch_bounds__(kWaves * 64) void grad_totals_kernel(Plan pl, Inputs in, Grads gr, SpanTotals totals)
+template <typename T, int S, bool VEC>
+__global__ __launch_bounds__(kGradWaves * 64) void grad_totals_kernel(Plan pl, Inputs in, Grads gr, SpanTotals totals)
 {
     using C = Cfg<S>;
     constexpr int TT = C::TT, NP = C::NP;
-    using X = Tile<T, TT>;
-    using BC = StateTile<T, TT, NP, 64>;
+    using X = Tile<T, TT, 16, VEC>;
+    using BC = StateTile<T, TT, NP, 64, VEC>;
     constexpr int V = X::V;
-    __shared__ __align__(16) f32x2 s_dt[kWaves][TT * kWaveChannels];
-    __shared__ __align__(16) float s_c[kWaves][TT * NP];
+    __shared__ __align__(16) f32x2 s_dt[kGradWaves][TT * 16];
+    __shared__ __align__(16) float s_c[kGradWaves][TT * NP];
 
     const uint32_t block = blockIdx.x % pl.blocks, span = blockIdx.x / pl.blocks;
-    const Place me(pl, block);
+    const Place<16> me(pl, block);
     if (me.nch == 0) return;
     uint32_t r0, r1, st, en;
     pl.rows_of(span, r0, r1);
@@ -566,8 +648,8 @@ __global__ __launch_bounds__(kWaves * 64) void grad_totals_kernel(Plan pl, Input
     if (!pl.seqs.seek(s, pos, r1, st, en) || pos != r0 || st == r0) return;
     f32x2* const dt = s_dt[me.w];
     float* const lc = s_c[me.w];
-    float A2[S], g[S];
-    load_states<S>(in.A, pl, me, A2, kLog2e);
+    LaneStates<S, 1> A2, g;
+    A2.load(in.A, pl, me, kLog2e);
     float bias[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -575,19 +657,18 @@ __global__ __launch_bounds__(kWaves * 64) void grad_totals_kernel(Plan pl, Input
         bias[j] = in.delta_bias && c < me.nch ? in.delta_bias[me.c0 + c] : 0.0f;
     }
     if (en <= r1)
-        start_state<S>(gr.dfinal, pl, me, (uint32_t)s, g);
+        g.start(gr.dfinal, pl, me, (uint32_t)s);
     else
-#pragma unroll
-        for (int i = 0; i < S; ++i) g[i] = 0.0f;
+        g.zero();
     uint32_t hi = (uint32_t)uniform((int)min(en, r1));
     float sum = 0.0f;
     typename X::P pd[X::PIECES], pz[X::PIECES], py[X::PIECES];
     typename BC::P pc[BC::PIECES];
     const auto fetch = [&](uint32_t at, int len) {
-        X::load(pd, in.delta, in.delta_stride, at, len, me.c0, me.nch, in.vec, me.lane);
-        X::load(py, gr.dy, gr.dy_stride, at, len, me.c0, me.nch, in.vec, me.lane);
-        if (in.z) X::load(pz, in.z, in.z_stride, at, len, me.c0, me.nch, in.vec, me.lane);
-        BC::load(pc, in.C, in.c_stride, at, len, me.group * pl.states, pl.states, in.vec_bc, me.lane);
+        X::load(pd, in.delta, in.delta_stride, at, len, me.c0, me.nch, me.lane);
+        X::load(py, gr.dy, gr.dy_stride, at, len, me.c0, me.nch, me.lane);
+        if (in.z) X::load(pz, in.z, in.z_stride, at, len, me.c0, me.nch, me.lane);
+        BC::load(pc, in.C, in.c_stride, at, len, me.group * pl.states, pl.states, me.lane);
     };
     uint32_t lo = r0 + (hi - 1 - r0) / TT * TT;
     fetch(lo, (int)(hi - lo));
@@ -601,11 +682,10 @@ __global__ __launch_bounds__(kWaves * 64) void grad_totals_kernel(Plan pl, Input
             if (in.z) unpack(pz[i], zf);
             const int r = X::row(i, me.lane);
             if (TT % X::RPL && r >= TT) continue;
+            step_sizes<V>(df, bias, in.softplus, r < len, df);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float v = r < len ? step_size(df[j] + bias[j], in.softplus) : 0.0f;
-                dt[r * kWaveChannels + X::col(me.lane) + j] = f32x2{v, in.z ? yf[j] * silu(zf[j]) : yf[j]};
-            }
+            for (int j = 0; j < V; ++j)
+                dt[r * 16 + X::col(me.lane) + j] = f32x2{df[j], in.z ? yf[j] * silu(zf[j]) : yf[j]};
         }
         BC::put(lc, pc, me.lane);
         wave_sync();
@@ -614,12 +694,12 @@ __global__ __launch_bounds__(kWaves * 64) void grad_totals_kernel(Plan pl, Input
         for (int t = (len - 1) | 3; t >= 0; t -= 4) {
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const f32x2 v = dt[(t - u) * kWaveChannels + me.d];
+                const f32x2 v = dt[(t - u) * 16 + me.d];
                 float c[S];
                 lds_states<S>(lc + (t - u) * NP + me.q * S, c);
                 sum += v[0];
 #pragma unroll
-                for (int i = 0; i < S; ++i) g[i] = exp2_fast(v[0] * A2[i]) * fmaf(v[1], c[i], g[i]);
+                for (int i = 0; i < S; ++i) g.v[0][i] = exp2_fast(v[0] * A2.v[0][i]) * fmaf(v[1], c[i], g.v[0][i]);
             }
         }
         wave_sync();
@@ -627,7 +707,7 @@ __global__ __launch_bounds__(kWaves * 64) void grad_totals_kernel(Plan pl, Input
         hi = lo;
         lo -= TT;
     }
-    store_padded<S>(totals.states, pl, me, span, g);
+    g.store_padded(totals.states, pl, me, span);
     if (me.q == 0 && me.d < me.nch) totals.dt_sum[(size_t)span * pl.channels + me.c0 + me.d] = sum;
 }
 
@@ -644,32 +724,34 @@ __global__ __launch_bounds__(kWaves * 64) void grad_totals_kernel(Plan pl, Input
 // vector units; what is left is a sum over the 4 channels of a lane row, every 16 rows.  The
 // wavefronts of a workgroup add theirs in LDS, the workgroups theirs in a second launch, always in
 // the same order.
-template <typename T, int S>
-__global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(S == 4 ? 2 : 1))) void grad_kernel(Plan pl, Inputs in, Grads gr, SpanTotals totals)
+template <typename T, int S, bool VEC>
+__global__ __launch_bounds__(kGradWaves * 64) __attribute__((amdgpu_waves_per_eu(S == 4 ? 2 : 1))) void grad_kernel(Plan pl, Inputs in, Grads gr, SpanTotals totals)
 {
     using C = Cfg<S>;
     constexpr int TT = C::TT, NP = C::NP, SUB = C::SUB, BLOCKS = TT / SUB;
-    using X = Tile<T, TT>;
-    using BC = StateTile<T, TT, NP, kWaves * 64>;
+    using X = Tile<T, TT, 16, VEC>;
+    using BC = StateTile<T, TT, NP, kGradWaves * 64, VEC>;
     constexpr int V = X::V;
-    __shared__ __align__(16) f32x2 s_dt[kWaves][TT * kWaveChannels];  // (dt, dt x), then the row's sums (dt part, x part)
-    __shared__ __align__(16) float s_dv[kWaves][TT * kWaveChannels];  // dv, then sum_n C h
-    __shared__ __align__(16) float s_h[kWaves][BLOCKS * 64 * S];      // state in front of every SUB rows
+    __shared__ __align__(16) f32x2 s_dt[kGradWaves][TT * 16];  // (dt, dt x), then the row's sums (dt part, x part)
+    __shared__ __align__(16) float s_dv[kGradWaves][TT * 16];  // dv, then sum_n C h
+    __shared__ __align__(16) float s_h[kGradWaves][BLOCKS * 64 * S];      // state in front of every SUB rows
     __shared__ __align__(16) float s_b[TT * NP], s_c[TT * NP];
     // the wavefront's sums for dB and dC, 16 rows at a time, take the place of states that are used up
     constexpr int SUMS = BLOCKS * 64 * S - TT * 2 * NP;
     static_assert(SUMS >= 0 && SUMS % 4 == 0, "the sums fit behind the states still needed");
 
     const uint32_t block = blockIdx.x % pl.blocks, span = blockIdx.x / pl.blocks;
-    const Place me(pl, block);
+    const Place<16> me(pl, block);
     uint32_t r0, r1;
     pl.rows_of(span, r0, r1);
     f32x2* const dt = s_dt[me.w];
     float* const ldv = s_dv[me.w];
     float* const lh = s_h[me.w];
     float* const lsum = lh + SUMS;
-    float A2[S], g[S], dA[S] = {};
-    load_states<S>(in.A, pl, me, A2, kLog2e);
+    LaneStates<S, 1> lane_A2, lane_g, lane_h, lane_dA;
+    lane_A2.load(in.A, pl, me, kLog2e);
+    lane_dA.zero();
+    auto &A2 = lane_A2.v[0], &g = lane_g.v[0], &h = lane_h.v[0], &dA = lane_dA.v[0];
     float bias[V], skip[V], dskip[V] = {}, dbias[V] = {};
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -693,19 +775,19 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(S =
         const uint32_t st = pl.seqs.start((uint32_t)s), en = max(pl.seqs.end((uint32_t)s), hi);
         const uint32_t first = (uint32_t)uniform((int)max(st, r0));
         if (hi == en) {
-            start_state<S>(gr.dfinal, pl, me, (uint32_t)s, g);
+            lane_g.start(gr.dfinal, pl, me, (uint32_t)s);
         } else {
-            join_spans<S>(totals, pl, me, pl.span_of(span, en - 1), span + 1, -1, A2, g);
+            join_spans<S, 1>(totals, pl, me, pl.span_of(span, en - 1), span + 1, -1, lane_A2, lane_g);
         }
         typename X::P px[X::PIECES], pd[X::PIECES], pz[X::PIECES], py[X::PIECES];
         typename BC::P pb[BC::PIECES], pc[BC::PIECES];
         const auto fetch = [&](uint32_t at, int len) {
-            X::load(px, in.x, in.x_stride, at, len, me.c0, me.nch, in.vec, me.lane);
-            X::load(pd, in.delta, in.delta_stride, at, len, me.c0, me.nch, in.vec, me.lane);
-            X::load(py, gr.dy, gr.dy_stride, at, len, me.c0, me.nch, in.vec, me.lane);
-            if (in.z) X::load(pz, in.z, in.z_stride, at, len, me.c0, me.nch, in.vec, me.lane);
-            BC::load(pb, in.B, in.b_stride, at, len, bc_at, pl.states, in.vec_bc, threadIdx.x);
-            BC::load(pc, in.C, in.c_stride, at, len, bc_at, pl.states, in.vec_bc, threadIdx.x);
+            X::load(px, in.x, in.x_stride, at, len, me.c0, me.nch, me.lane);
+            X::load(pd, in.delta, in.delta_stride, at, len, me.c0, me.nch, me.lane);
+            X::load(py, gr.dy, gr.dy_stride, at, len, me.c0, me.nch, me.lane);
+            if (in.z) X::load(pz, in.z, in.z_stride, at, len, me.c0, me.nch, me.lane);
+            BC::load(pb, in.B, in.b_stride, at, len, bc_at, pl.states, threadIdx.x);
+            BC::load(pc, in.C, in.c_stride, at, len, bc_at, pl.states, threadIdx.x);
         };
         uint32_t lo = max(r0 + (hi - 1 - r0) / TT * TT, first);
         constexpr bool AHEAD = S < 16;  // the next tile's pieces in registers (64 states leave none for them)
@@ -714,11 +796,10 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(S =
             const int len = (int)(hi - lo);
             if (!AHEAD) fetch(lo, len);
             // the state in front of the tile
-            float h[S];
             if (lo == st)
-                start_state<S>(in.initial, pl, me, (uint32_t)s, h);
+                lane_h.start(in.initial, pl, me, (uint32_t)s);
             else
-                load_padded<S>(gr.saved, pl, me, (size_t)span * pl.tiles_per_span + (lo - r0) / TT, h);
+                lane_h.load_padded(gr.saved, pl, me, (size_t)span * pl.tiles_per_span + (lo - r0) / TT);
             float xf[X::PIECES][V], df[X::PIECES][V], zf[X::PIECES][V], yf[X::PIECES][V];
 #pragma unroll
             for (int i = 0; i < X::PIECES; ++i) {
@@ -732,7 +813,7 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(S =
                 for (int j = 0; j < V; ++j) {
                     df[i][j] += bias[j];
                     const float v = r < len ? step_size(df[i][j], in.softplus) : 0.0f;
-                    const int at = r * kWaveChannels + X::col(me.lane) + j;
+                    const int at = r * 16 + X::col(me.lane) + j;
                     dt[at] = f32x2{v, v * xf[i][j]};
                     ldv[at] = in.z ? yf[i][j] * silu(zf[i][j]) : yf[i][j];
                 }
@@ -754,7 +835,7 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(S =
 #pragma unroll
                 for (int u = 0; u < SUB; ++u) {
                     const int t = k * SUB + u;
-                    const f32x2 v = dt[t * kWaveChannels + me.d];
+                    const f32x2 v = dt[t * 16 + me.d];
                     float b[S];
                     lds_states<S>(s_b + t * NP + me.q * S, b);
 #pragma unroll
@@ -771,7 +852,7 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(S =
 #pragma unroll
                 for (int u = 0; u < SUB; ++u) {
                     const int t = k * SUB + u;
-                    const f32x2 v = dt[t * kWaveChannels + me.d];
+                    const f32x2 v = dt[t * 16 + me.d];
                     float b[S];
                     lds_states<S>(s_b + t * NP + me.q * S, b);
 #pragma unroll
@@ -784,8 +865,8 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(S =
 #pragma unroll
                 for (int u = SUB - 1; u >= 0; --u) {
                     const int t = k * SUB + u;
-                    const f32x2 v = dt[t * kWaveChannels + me.d];
-                    const float dv = ldv[t * kWaveChannels + me.d];
+                    const f32x2 v = dt[t * 16 + me.d];
+                    const float dv = ldv[t * 16 + me.d];
                     float b[S], c[S];
                     lds_states<S>(s_b + t * NP + me.q * S, b);
                     lds_states<S>(s_c + t * NP + me.q * S, c);
@@ -808,8 +889,8 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(S =
                     sd = quad_sum(sd);
                     sx = quad_sum(sx);
                     if (me.q == (t & 3)) {  // every lane of the quad has read the row's values
-                        dt[t * kWaveChannels + me.d] = f32x2{sd * kLn2, sx};
-                        ldv[t * kWaveChannels + me.d] = ch;
+                        dt[t * 16 + me.d] = f32x2{sd * kLn2, sx};
+                        ldv[t * 16 + me.d] = ch;
                     }
                 }
                 if ((k * SUB) % 16 == 0) {
@@ -844,10 +925,10 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(S =
             }
             __syncthreads();
             // the workgroup's sums for dB and dC
-            for (int i = threadIdx.x; i < len * 2 * NP / 4; i += kWaves * 64) {
+            for (int i = threadIdx.x; i < len * 2 * NP / 4; i += kGradWaves * 64) {
                 f32x4 v = *reinterpret_cast<const f32x4*>(&s_h[0][SUMS + i * 4]);
 #pragma unroll
-                for (int w = 1; w < kWaves; ++w) v += *reinterpret_cast<const f32x4*>(&s_h[w][SUMS + i * 4]);
+                for (int w = 1; w < kGradWaves; ++w) v += *reinterpret_cast<const f32x4*>(&s_h[w][SUMS + i * 4]);
                 *reinterpret_cast<f32x4*>(bc_out + (size_t)lo * (2 * NP) + (size_t)i * 4) = v;
             }
             // the rows' own gradients
@@ -858,7 +939,7 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(S =
                 float ox[V], od[V], oz[V];
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    const int at = r * kWaveChannels + X::col(me.lane) + j;
+                    const int at = r * 16 + X::col(me.lane) + j;
                     const f32x2 q = dt[at];
                     const float raw = df[i][j], v = step_size(raw, in.softplus), x = xf[i][j], dy = yf[i][j];
                     float dv = dy;
@@ -873,9 +954,9 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(S =
                     dskip[j] = fmaf(dv, x, dskip[j]);
                     dbias[j] += od[j];
                 }
-                X::store(gr.dx, gr.dx_stride, lo, len, me.c0, me.nch, in.vec, me.lane, i, ox);
-                X::store(gr.ddelta, gr.ddelta_stride, lo, len, me.c0, me.nch, in.vec, me.lane, i, od);
-                if (in.z) X::store(gr.dz, gr.dz_stride, lo, len, me.c0, me.nch, in.vec, me.lane, i, oz);
+                X::store(gr.dx, gr.dx_stride, lo, len, me.c0, me.nch, me.lane, i, ox);
+                X::store(gr.ddelta, gr.ddelta_stride, lo, len, me.c0, me.nch, me.lane, i, od);
+                if (in.z) X::store(gr.dz, gr.dz_stride, lo, len, me.c0, me.nch, me.lane, i, oz);
             }
             __syncthreads();
             hi = lo;
@@ -883,9 +964,9 @@ __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(S =
             lo = next;
         }
         if (first == st && gr.dinitial)
-            store_states<S>(gr.dinitial + (size_t)s * pl.channels * pl.states, pl, me, g);
+            lane_g.store(gr.dinitial + (size_t)s * pl.channels * pl.states, pl, me);
     }
-    store_padded<S>(gr.dA, pl, me, span, dA);
+    lane_dA.store_padded(gr.dA, pl, me, span);
     // lanes that loaded the same channels
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -953,21 +1034,24 @@ __global__ __launch_bounds__(256) void join_spans_kernel(Plan pl, const float* _
 
 // dinitial of empty sequences is dfinal.
 template <int S>
-__global__ __launch_bounds__(kWaves * 64) void grad_empty_kernel(Plan pl, const float* __restrict__ dfinal,
+__global__ __launch_bounds__(kGradWaves * 64) void grad_empty_kernel(Plan pl, const float* __restrict__ dfinal,
                                                                  float* __restrict__ dinitial)
 {
     const uint32_t block = blockIdx.x % pl.blocks;
-    const Place me(pl, block);
+    const Place<16> me(pl, block);
     for (uint32_t s = blockIdx.x / pl.blocks; s < pl.seqs.count; s += kEmptyStep) {
         if (pl.seqs.end(s) > pl.seqs.start(s)) continue;
-        float g[S];
-        start_state<S>(dfinal, pl, me, s, g);
-        store_states<S>(dinitial + (size_t)s * pl.channels * pl.states, pl, me, g);
+        LaneStates<S, 1> g;
+        g.start(dfinal, pl, me, s);
+        g.store(dinitial + (size_t)s * pl.channels * pl.states, pl, me);
     }
 }
 
 // ------------------------------------------------------------ host side
-constexpr uint32_t kTargetWorkgroups = 512;  // two per compute unit
+// Workgroups that the rows are cut for: 1024 make two wavefronts of the forward kernels per SIMD.
+// Measured (16384 x 2048 channels / ragged 6001 x 4096 / training 4 x 2048 x 4096): 512 workgroups
+// 475 / 349 / 1478 us, 1024 259 / 212 / 1239, 2048 316 / 215 / 1250.
+constexpr uint32_t kTargetWorkgroups = 1024;
 constexpr uint32_t kMinSpanRows = 128;
 
 Plan make_plan(uint32_t channels, uint32_t states, uint32_t groups, uint64_t rows, uint64_t seqs, const int32_t* offsets)
@@ -1091,8 +1175,8 @@ Inputs make_inputs(const A& a, const Rows& r)
     in.softplus = a.delta_softplus != 0;
     const uint32_t v = 16 / (uint32_t)dtype_size(a.dtype);
     in.vec = a.channels / a.groups % v == 0 && r.vec(a.x, a.x_stride) && r.vec(a.delta, a.delta_stride) &&
-             (!a.z || r.vec(a.z, a.z_stride));
-    in.vec_bc = a.states == padded_states(a.states) && r.vec(a.B, a.b_stride) && r.vec(a.C, a.c_stride);
+             (!a.z || r.vec(a.z, a.z_stride)) && a.states == padded_states(a.states) && r.vec(a.B, a.b_stride) &&
+             r.vec(a.C, a.c_stride);
     return in;
 }
 
@@ -1125,11 +1209,13 @@ scan_status_t forward(const selective_scan_args_t& a, hipStream_t stream)
         const uint64_t extra = a.final_state ? (uint64_t)std::min<uint64_t>(p.seqs.count, kEmptyStep) * p.blocks : 0;
         if (wgs + extra > 0x7FFFFFFFu) return SCAN_ERR_INVALID;
         if (p.per_seq > 1)
-            hipLaunchKernelGGL((scan_kernel<T, S, true>), dim3((unsigned)wgs), dim3(kWaves * 64), 0, stream, p, in, w.totals,
-                               (void*)nullptr, (int64_t)0, (float*)nullptr, (float*)nullptr);
+            hipLaunchKernelGGL((in.vec ? scan_kernel<T, S, true, true> : scan_kernel<T, S, false, true>), dim3((unsigned)wgs),
+                               dim3(kFwdWaves * 64), 0, stream, p, in, w.totals, (void*)nullptr, (int64_t)0, (float*)nullptr,
+                               (float*)nullptr);
         if (wgs + extra)
-            hipLaunchKernelGGL((scan_kernel<T, S, false>), dim3((unsigned)(wgs + extra)), dim3(kWaves * 64), 0, stream, p, in,
-                               w.totals, a.y, a.y_stride, a.final_state, a.saved);
+            hipLaunchKernelGGL((in.vec ? scan_kernel<T, S, true, false> : scan_kernel<T, S, false, false>),
+                               dim3((unsigned)(wgs + extra)), dim3(kFwdWaves * 64), 0, stream, p, in, w.totals, a.y, a.y_stride,
+                               a.final_state, a.saved);
         return launched();
     });
 }
@@ -1153,11 +1239,11 @@ scan_status_t gradient(const selective_scan_grad_args_t& g, hipStream_t stream)
         const uint64_t wgs = (uint64_t)p.spans * p.blocks;
         const uint64_t bc = ((uint64_t)a.rows * a.groups * (np / 2) + 255) / 256;
         if (wgs > 0x7FFFFFFFu || bc > 0x7FFFFFFFu) return SCAN_ERR_INVALID;
-        const dim3 block(kWaves * 64);
+        const dim3 block(kGradWaves * 64);
         if (p.per_seq > 1)
-            hipLaunchKernelGGL((grad_totals_kernel<T, S>), dim3((unsigned)wgs), block, 0, stream, p, in, gr, w.totals);
+            hipLaunchKernelGGL((in.vec ? grad_totals_kernel<T, S, true> : grad_totals_kernel<T, S, false>), dim3((unsigned)wgs), block, 0, stream, p, in, gr, w.totals);
         if (wgs) {
-            hipLaunchKernelGGL((grad_kernel<T, S>), dim3((unsigned)wgs), block, 0, stream, p, in, gr, w.totals);
+            hipLaunchKernelGGL((in.vec ? grad_kernel<T, S, true> : grad_kernel<T, S, false>), dim3((unsigned)wgs), block, 0, stream, p, in, gr, w.totals);
             hipLaunchKernelGGL((join_bc_kernel<T>), dim3((unsigned)bc), dim3(256), 0, stream, p, (const float*)w.bc, np,
                                static_cast<T*>(g.dB), g.db_stride, static_cast<T*>(g.dC), g.dc_stride);
         }
@@ -1307,11 +1393,11 @@ scan_status_t selective_scan_step(const selective_scan_step_args_t* args, void* 
     const uint64_t wgs = a.rows * (uint64_t)p.blocks;
     if (wgs > 0x7FFFFFFFu) return SCAN_ERR_INVALID;
     Inputs in = make_inputs(a, r);
-    in.vec_bc = a.states == padded_states(a.states) && aligned(a.state, 16) && aligned(a.A, 16);
+    in.vec = a.states == padded_states(a.states) && aligned(a.state, 16) && aligned(a.A, 16);
     return dispatch(a.dtype, a.states, [&](auto te, auto se) -> scan_status_t {
         using T = decltype(te);
         constexpr int S = decltype(se)::value;
-        hipLaunchKernelGGL((scan_step_kernel<T, S>), dim3((unsigned)wgs), dim3(kWaves * 64), 0,
+        hipLaunchKernelGGL((scan_step_kernel<T, S>), dim3((unsigned)wgs), dim3(kGradWaves * 64), 0,
                            static_cast<hipStream_t>(stream), p, in, a.slots, (uint32_t)a.n_slots, a.state,
                            static_cast<T*>(a.y), a.y_stride);
         return launched();

@@ -56,6 +56,16 @@ __device__ __forceinline__ Pack<T, V> zero_pack()
     return p;
 }
 
+// Hides from the compiler that p is what it was, so that values made of it earlier are made again
+// instead of being kept in registers.
+template <typename P>
+__device__ __forceinline__ void opaque(P& p)
+{
+    u32x4 v = __builtin_bit_cast(u32x4, p);
+    asm volatile("" : "+v"(v));
+    p = __builtin_bit_cast(P, v);
+}
+
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
