@@ -192,21 +192,39 @@ __device__ __forceinline__ void lds_states(const float* p, float (&f)[S])
     }
 }
 
-// The four lanes of a quad hold four values each; lane q receives the sum over the quad of value q.
-__device__ __forceinline__ float quad_transpose_sum(const float (&v)[4], int q)
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// Exchanges the upper half of a with the lower half of b (32 lanes), or the odd 16-lane rows of a
+// with the even ones of b.
+__device__ __forceinline__ float swap32_sum(float a, float b)
 {
-    const bool odd = q & 1, high = q & 2;
-    float a = odd ? v[1] : v[0], b = odd ? v[3] : v[2];
-    a += dpp<kQuadXor1>(odd ? v[0] : v[1]);
-    b += dpp<kQuadXor1>(odd ? v[2] : v[3]);
-    const float keep = high ? b : a, give = high ? a : b;
-    return keep + dpp<kQuadXor2>(give);
+    const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), false, false);
+    const uint32_t x = r[0], y = r[1];  // a bit cast of a vector's element would take the first one both times
+    return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
+}
+__device__ __forceinline__ float swap16_sum(float a, float b)
+{
+    const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), false, false);
+    const uint32_t x = r[0], y = r[1];  // a bit cast of a vector's element would take the first one both times
+    return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
+}
+// Row q of the lanes receives the sum of v[q] over the four rows.
+__device__ __forceinline__ float row_transpose_sum(const float (&v)[4])
+{
+    return swap16_sum(swap32_sum(v[0], v[2]), swap32_sum(v[1], v[3]));
 }
 
-// Where a wavefront stands: its CW channels, and its lane's part of them (channel d, and d + 16 ...).
-template <int CW>
+// Where a wavefront stands: its CW channels, and its lane's part of them: channel d (and d + 16 ...),
+// quarter q of its states.  QUADS: lane = 4 d + q, and the lane's states are S q .. S q + S - 1; else
+// lane = 16 q + d, and they are 4 q .. 4 q + 3 of every 16.
+template <int CW, bool QUADS>
 struct Place {
     static constexpr int CH = CW / 16;  // channels per lane
+    template <int S>
+    __device__ __forceinline__ uint32_t state(int i) const
+    {
+        return QUADS ? q * S + i : (i / 4) * 16 + 4 * q + i % 4;
+    }
     int lane, w, d, q;                  // channel and quarter of the lane
     uint32_t group, c0;                 // first channel of the wavefront
     int nch;                            // channels of the wavefront (0: none)
@@ -214,8 +232,8 @@ struct Place {
     {
         lane = threadIdx.x & 63;
         w = uniform(threadIdx.x >> 6);
-        d = lane >> 2;
-        q = lane & 3;
+        d = QUADS ? lane >> 2 : lane & 15;
+        q = QUADS ? lane & 3 : lane >> 4;
         group = block / p.blocks_per_group;
         const uint32_t first = (block % p.blocks_per_group) * kWgChannels + w * CW;
         c0 = group * p.group_channels + first;
@@ -224,8 +242,9 @@ struct Place {
 };
 
 // The lane's S states of each of its channels.
-template <int S, int CH>
+template <int S, int CH, bool QUADS>
 struct LaneStates {
+    using Me = Place<16 * CH, QUADS>;
     float v[CH][S];
 
     __device__ __forceinline__ void zero()
@@ -236,31 +255,30 @@ struct LaneStates {
             for (int i = 0; i < S; ++i) v[c][i] = 0.0f;
     }
     // from and to an array (channels x states); zeros where padded
-    __device__ __forceinline__ void load(const float* __restrict__ p, const Plan& pl, const Place<16 * CH>& me,
-                                         float scale = 1.0f)
+    __device__ __forceinline__ void load(const float* __restrict__ p, const Plan& pl, const Me& me, float scale = 1.0f)
     {
 #pragma unroll
         for (int c = 0; c < CH; ++c)
 #pragma unroll
             for (int i = 0; i < S; ++i) {
-                const uint32_t n = me.q * S + i;
+                const uint32_t n = me.template state<S>(i);
                 const int ch = me.d + 16 * c;
                 v[c][i] = ch < me.nch && n < pl.states ? p[(size_t)(me.c0 + ch) * pl.states + n] * scale : 0.0f;
             }
     }
-    __device__ __forceinline__ void store(float* __restrict__ p, const Plan& pl, const Place<16 * CH>& me) const
+    __device__ __forceinline__ void store(float* __restrict__ p, const Plan& pl, const Me& me) const
     {
 #pragma unroll
         for (int c = 0; c < CH; ++c)
 #pragma unroll
             for (int i = 0; i < S; ++i) {
-                const uint32_t n = me.q * S + i;
+                const uint32_t n = me.template state<S>(i);
                 const int ch = me.d + 16 * c;
                 if (ch < me.nch && n < pl.states) p[(size_t)(me.c0 + ch) * pl.states + n] = v[c][i];
             }
     }
     // the state of sequence s in an array of them, or zero without one
-    __device__ __forceinline__ void start(const float* __restrict__ p, const Plan& pl, const Place<16 * CH>& me, uint32_t s)
+    __device__ __forceinline__ void start(const float* __restrict__ p, const Plan& pl, const Me& me, uint32_t s)
     {
         if (p)
             load(p + (size_t)s * pl.channels * pl.states, pl, me);
@@ -268,31 +286,35 @@ struct LaneStates {
             zero();
     }
     // from and to the workspace, padded to 4 S states per channel: [index][channels][4 S]
-    __device__ __forceinline__ void load_padded(const float* __restrict__ p, const Plan& pl, const Place<16 * CH>& me,
-                                                size_t index)
+    __device__ __forceinline__ void load_padded(const float* __restrict__ p, const Plan& pl, const Me& me, size_t index)
     {
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             const int ch = me.d + 16 * c;
             if (ch < me.nch) {
-                lds_states<S>(p + (index * pl.channels + me.c0 + ch) * (4 * S) + me.q * S, v[c]);
+                const float* o = p + (index * pl.channels + me.c0 + ch) * (4 * S);
+#pragma unroll
+                for (int i = 0; i < S; i += 4) {
+                    const f32x4 f = *reinterpret_cast<const f32x4*>(o + me.template state<S>(i));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[c][i + j] = f[j];
+                }
             } else {
 #pragma unroll
                 for (int i = 0; i < S; ++i) v[c][i] = 0.0f;
             }
         }
     }
-    __device__ __forceinline__ void store_padded(float* __restrict__ p, const Plan& pl, const Place<16 * CH>& me,
-                                                 size_t index) const
+    __device__ __forceinline__ void store_padded(float* __restrict__ p, const Plan& pl, const Me& me, size_t index) const
     {
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             const int ch = me.d + 16 * c;
             if (ch >= me.nch) continue;
-            float* o = p + (index * pl.channels + me.c0 + ch) * (4 * S) + me.q * S;
+            float* o = p + (index * pl.channels + me.c0 + ch) * (4 * S);
 #pragma unroll
             for (int i = 0; i < S; i += 4)
-                *reinterpret_cast<f32x4*>(o + i) = f32x4{v[c][i], v[c][i + 1], v[c][i + 2], v[c][i + 3]};
+                *reinterpret_cast<f32x4*>(o + me.template state<S>(i)) = f32x4{v[c][i], v[c][i + 1], v[c][i + 2], v[c][i + 3]};
         }
     }
 };
@@ -304,15 +326,16 @@ struct SpanTotals {
     float* dt_sum;  // [span][channels]
 };
 // h = the state behind spans [first, last], joined in order (`step` 1) or in reverse (-1).
-template <int S, int CH>
-__device__ __forceinline__ void join_spans(const SpanTotals& t, const Plan& pl, const Place<16 * CH>& me, uint32_t first,
-                                           uint32_t last, int step, const LaneStates<S, CH>& A2, LaneStates<S, CH>& h)
+template <int S, int CH, bool QUADS>
+__device__ __forceinline__ void join_spans(const SpanTotals& t, const Plan& pl, const Place<16 * CH, QUADS>& me,
+                                           uint32_t first, uint32_t last, int step, const LaneStates<S, CH, QUADS>& A2,
+                                           LaneStates<S, CH, QUADS>& h)
 {
     h.load_padded(t.states, pl, me, first);
 #pragma unroll 4
     while (first != last) {
         first += step;
-        LaneStates<S, CH> e;
+        LaneStates<S, CH, QUADS> e;
         e.load_padded(t.states, pl, me, first);
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
@@ -342,36 +365,43 @@ __device__ __forceinline__ void step_sizes(const float (&delta)[V], const float 
 }
 
 // ------------------------------------------------------------ forward
-// A lane has two channels: the B and C that it reads from LDS serve both (with one, those reads
-// keep the LDS busy for three quarters of the time that the vector units need).
-constexpr int kFwdChannels = 32;
-constexpr int kFwdWaves = kWgChannels / kFwdChannels;
+// Bound by the issue of vector instructions, so what can be done elsewhere is: the products dt x B of
+// four rows, 16 channels and 16 states come from one v_mfma_f32_16x16x1_4b_f32, which multiplies four
+// columns of 16 by four rows of 16 (a fused product of 32-bit values, exact but for its one rounding)
+// and leaves state 4 q + i of channel d in lane 16 q + d, where the recurrence wants it.  Left per row,
+// channel and state: a product and an exponential for the factor, a fused multiply-add for the state,
+// one for the output.  With up to 16 states a lane has two channels, which share what it reads of C.
+template <int S>
+struct Fwd {
+    static constexpr int CW = S == 4 ? 32 : 16, WAVES = kWgChannels / CW;
+};
 
 // TOTALS: the span's totals only.
 template <typename T, int S, bool VEC, bool TOTALS>
-__global__ __launch_bounds__(kFwdWaves * 64) void scan_kernel(Plan pl, Inputs in, SpanTotals totals, void* y,
-                                                              int64_t y_stride, float* final_state, float* saved)
+__global__ __launch_bounds__(Fwd<S>::WAVES * 64) __attribute__((amdgpu_waves_per_eu(S == 16 ? 1 : 2))) void scan_kernel(Plan pl, Inputs in, SpanTotals totals, void* y,
+                                                                  int64_t y_stride, float* final_state, float* saved)
 {
     using C = Cfg<S>;
-    constexpr int TT = C::TT, NP = C::NP, CW = kFwdChannels, CH = CW / 16;
+    constexpr int TT = C::TT, NP = C::NP, CW = Fwd<S>::CW, CH = CW / 16, WAVES = Fwd<S>::WAVES, BLK = S / 4;
     using X = Tile<T, TT, CW, VEC>;
     using BC = StateTile<T, TT, NP, 64, VEC>;
     constexpr int V = X::V;
-    // two rows more than a tile: the walk over the rows reads two ahead
-    __shared__ __align__(16) f32x2 s_dt[kFwdWaves][(TT + 2) * CW];
-    __shared__ __align__(16) float s_b[kFwdWaves][(TT + 2) * NP];
-    __shared__ __align__(16) float s_c[TOTALS ? 1 : kFwdWaves][TOTALS ? 4 : (TT + 2) * NP];
-    __shared__ __align__(16) float s_y[TOTALS ? 1 : kFwdWaves][TOTALS ? 4 : TT * CW];
-    __shared__ __align__(16) float s_par[kFwdWaves][2 * CW];  // delta_bias and D of the wavefront's channels
+    // four rows more than a tile: the walk over the rows reads that far ahead
+    __shared__ __align__(16) float s_dt[WAVES][(TT + 4) * CW];  // dt, as [row / 4][channel][row % 4]
+    __shared__ __align__(16) float s_dx[WAVES][(TT + 4) * CW];  // dt x, as [row][channel]
+    __shared__ __align__(16) float s_b[WAVES][(TT + 4) * NP];
+    __shared__ __align__(16) float s_c[TOTALS ? 1 : WAVES][TOTALS ? 4 : (TT + 4) * NP];
+    __shared__ __align__(16) float s_y[TOTALS ? 1 : WAVES][TOTALS ? 4 : TT * CW];
+    __shared__ __align__(16) float s_par[WAVES][2 * CW];  // delta_bias and D of the wavefront's channels
 
     const uint32_t block = blockIdx.x % pl.blocks, span = blockIdx.x / pl.blocks;
-    const Place<CW> me(pl, block);
+    const Place<CW, false> me(pl, block);
     if (me.nch == 0) return;
     if (span >= pl.spans) {
         // behind the spans: the final states of empty sequences
         for (uint32_t s = span - pl.spans; s < pl.seqs.count; s += kEmptyStep) {
             if (pl.seqs.end(s) > pl.seqs.start(s)) continue;
-            LaneStates<S, CH> h;
+            LaneStates<S, CH, false> h;
             h.start(in.initial, pl, me, s);
             h.store(final_state + (size_t)s * pl.channels * pl.states, pl, me);
         }
@@ -379,18 +409,19 @@ __global__ __launch_bounds__(kFwdWaves * 64) void scan_kernel(Plan pl, Inputs in
     }
     uint32_t r0, r1;
     pl.rows_of(span, r0, r1);
-    f32x2* const dt = s_dt[me.w];
+    float* const dt = s_dt[me.w];
+    float* const dx = s_dx[me.w];
     float* const lb = s_b[me.w];
     float* const lc = s_c[TOTALS ? 0 : me.w];
     float* const ly = s_y[TOTALS ? 0 : me.w];
     float* const bias = s_par[me.w] + X::col(me.lane);
     float* const skip = bias + CW;
-    if (me.lane < 2 * CW) {
+    if (me.lane < 2 * CW) {  // 64 lanes or fewer
         const int c = me.lane % CW;
         const float* p = me.lane < CW ? in.delta_bias : in.D;
         s_par[me.w][me.lane] = p && c < me.nch ? p[me.c0 + c] : 0.0f;
     }
-    LaneStates<S, CH> A2, h;
+    LaneStates<S, CH, false> A2, h;
     A2.load(in.A, pl, me, kLog2e);
     const uint32_t bc_at = me.group * pl.states;
 
@@ -408,7 +439,7 @@ __global__ __launch_bounds__(kFwdWaves * 64) void scan_kernel(Plan pl, Inputs in
         else if (TOTALS)
             h.zero();
         else
-            join_spans<S, CH>(totals, pl, me, pl.span_of(span, st), span - 1, 1, A2, h);
+            join_spans<S, CH, false>(totals, pl, me, pl.span_of(span, st), span - 1, 1, A2, h);
         float sum[CH] = {};
         typename X::P px[X::PIECES], pd[X::PIECES], pz[X::PIECES];
         typename BC::P pb[BC::PIECES], pc[BC::PIECES];
@@ -441,9 +472,14 @@ __global__ __launch_bounds__(kFwdWaves * 64) void scan_kernel(Plan pl, Inputs in
                 if (TT % X::RPL && r >= TT) continue;
                 lds_states<V>(bias, bf);
                 step_sizes<V>(df, bf, in.softplus, r < len, df);
-                f32x2* const out = dt + r * CW + X::col(me.lane);
 #pragma unroll
-                for (int j = 0; j < V; ++j) out[j] = f32x2{df[j], df[j] * xf[j]};
+                for (int j = 0; j < V; ++j) {
+                    dt[((r >> 2) * CW + X::col(me.lane) + j) * 4 + (r & 3)] = df[j];
+                    xf[j] *= df[j];
+                }
+#pragma unroll
+                for (int j = 0; j < V; j += 4)
+                    *reinterpret_cast<f32x4*>(dx + r * CW + X::col(me.lane) + j) = f32x4{xf[j], xf[j + 1], xf[j + 2], xf[j + 3]};
             }
             BC::put(lb, pb, me.lane);
             if (!TOTALS) BC::put(lc, pc, me.lane);
@@ -454,50 +490,69 @@ __global__ __launch_bounds__(kFwdWaves * 64) void scan_kernel(Plan pl, Inputs in
                 next_len = tile_len(next);
                 fetch(next, next_len);
             }
-            // four rows at a time, the LDS reads two rows ahead of their use
-            struct Two {
-                f32x2 v[2][CH];
-                float b[2][S], c[2][S];
+            // four rows at a time, their LDS reads and products made while the four before are walked
+            struct Four {
+                f32x4 dt[CH];
+                f32x4 c[4][BLK];
+                float left[BLK], right[CH];
             };
-            const auto read = [&](Two& w, int t) {
+            const auto read = [&](Four& w, int t) {
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
+                for (int c = 0; c < CH; ++c) {
+                    w.dt[c] = *reinterpret_cast<const f32x4*>(dt + t * CW + (me.d + 16 * c) * 4);
+                    w.right[c] = dx[(t + me.q) * CW + me.d + 16 * c];
+                }
 #pragma unroll
-                    for (int c = 0; c < CH; ++c) w.v[u][c] = dt[(t + u) * CW + me.d + 16 * c];
-                    lds_states<S>(lb + (t + u) * NP + me.q * S, w.b[u]);
-                    if (!TOTALS) lds_states<S>(lc + (t + u) * NP + me.q * S, w.c[u]);
+                for (int k = 0; k < BLK; ++k) {
+                    w.left[k] = lb[(t + me.q) * NP + 16 * k + me.d];
+                    if (!TOTALS) {
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) w.c[u][k] = *reinterpret_cast<const f32x4*>(lc + (t + u) * NP + 16 * k + 4 * me.q);
+                    }
                 }
             };
-            const auto walk = [&](const Two& w, float (*part)[4], int at) {
+            const auto products = [&](const Four& w, f32x16 (*p)[BLK]) {
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
+                for (int c = 0; c < CH; ++c)
+#pragma unroll
+                    for (int k = 0; k < BLK; ++k)
+                        p[c][k] = __builtin_amdgcn_mfma_f32_16x16x1f32(w.left[k], w.right[c], f32x16{}, 0, 0, 0);
+            };
+            const auto walk = [&](const Four& w, const f32x16 (*p)[BLK], int t) {
+                float part[CH][4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
 #pragma unroll
                     for (int c = 0; c < CH; ++c) {
-                        const f32x2 v = w.v[u][c];
-                        if (TOTALS) sum[c] += v[0];
-                        float p = 0.0f;
+                        const float v = w.dt[c][u];
+                        if (TOTALS) sum[c] += v;
+                        float y_ = 0.0f;
 #pragma unroll
                         for (int i = 0; i < S; ++i) {
-                            h.v[c][i] = fmaf(exp2_fast(v[0] * A2.v[c][i]), h.v[c][i], v[1] * w.b[u][i]);
-                            if (!TOTALS) p = i ? fmaf(w.c[u][i], h.v[c][i], p) : w.c[u][i] * h.v[c][i];
+                            float& hi = h.v[c][i];
+                            hi = fmaf(exp2_fast(v * A2.v[c][i]), hi, p[c][i / 4][4 * u + i % 4]);
+                            if (!TOTALS) y_ = i ? fmaf(w.c[u][i / 4][i % 4], hi, y_) : w.c[u][0][0] * hi;
                         }
-                        part[c][at + u] = p;
+                        part[c][u] = y_;
                     }
-            };
-            Two w0, w1;
-            read(w0, 0);
-            for (int t = 0; t < len; t += 4) {
-                float part[CH][4];
-                read(w1, t + 2);
-                __builtin_amdgcn_sched_barrier(0);
-                walk(w0, part, 0);
-                read(w0, t + 4);
-                __builtin_amdgcn_sched_barrier(0);
-                walk(w1, part, 2);
                 if (!TOTALS) {
 #pragma unroll
-                    for (int c = 0; c < CH; ++c) ly[(t + me.q) * CW + me.d + 16 * c] = quad_transpose_sum(part[c], me.q);
+                    for (int c = 0; c < CH; ++c) ly[(t + me.q) * CW + me.d + 16 * c] = row_transpose_sum(part[c]);
                 }
+            };
+            Four w0, w1;
+            f32x16 p0[CH][BLK], p1[CH][BLK];
+            read(w0, 0);
+            products(w0, p0);
+            for (int t = 0; t < len; t += 8) {
+                read(w1, t + 4);
+                __builtin_amdgcn_sched_barrier(0);
+                walk(w0, p0, t);
+                products(w1, p1);
+                read(w0, t + 8);
+                __builtin_amdgcn_sched_barrier(0);
+                walk(w1, p1, t + 4);
+                products(w0, p0);
             }
             if (!TOTALS && y) {
                 wave_sync();
@@ -545,7 +600,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void scan_step_kernel(Plan pl, Inp
                                                                 T* __restrict__ y, int64_t y_stride)
 {
     const uint32_t block = blockIdx.x % pl.blocks, r = blockIdx.x / pl.blocks;
-    const Place<16> me(pl, block);
+    const Place<16, true> me(pl, block);
     if (me.d >= me.nch) return;
     const int32_t slot = slots ? slots[r] : (int32_t)r;
     if (slot < 0 || (uint32_t)slot >= n_slots) return;
@@ -638,7 +693,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void grad_totals_kernel(Plan pl, I
     __shared__ __align__(16) float s_c[kGradWaves][TT * NP];
 
     const uint32_t block = blockIdx.x % pl.blocks, span = blockIdx.x / pl.blocks;
-    const Place<16> me(pl, block);
+    const Place<16, true> me(pl, block);
     if (me.nch == 0) return;
     uint32_t r0, r1, st, en;
     pl.rows_of(span, r0, r1);
@@ -648,7 +703,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void grad_totals_kernel(Plan pl, I
     if (!pl.seqs.seek(s, pos, r1, st, en) || pos != r0 || st == r0) return;
     f32x2* const dt = s_dt[me.w];
     float* const lc = s_c[me.w];
-    LaneStates<S, 1> A2, g;
+    LaneStates<S, 1, true> A2, g;
     A2.load(in.A, pl, me, kLog2e);
     float bias[V];
 #pragma unroll
@@ -741,14 +796,14 @@ __global__ __launch_bounds__(kGradWaves * 64) __attribute__((amdgpu_waves_per_eu
     static_assert(SUMS >= 0 && SUMS % 4 == 0, "the sums fit behind the states still needed");
 
     const uint32_t block = blockIdx.x % pl.blocks, span = blockIdx.x / pl.blocks;
-    const Place<16> me(pl, block);
+    const Place<16, true> me(pl, block);
     uint32_t r0, r1;
     pl.rows_of(span, r0, r1);
     f32x2* const dt = s_dt[me.w];
     float* const ldv = s_dv[me.w];
     float* const lh = s_h[me.w];
     float* const lsum = lh + SUMS;
-    LaneStates<S, 1> lane_A2, lane_g, lane_h, lane_dA;
+    LaneStates<S, 1, true> lane_A2, lane_g, lane_h, lane_dA;
     lane_A2.load(in.A, pl, me, kLog2e);
     lane_dA.zero();
     auto &A2 = lane_A2.v[0], &g = lane_g.v[0], &h = lane_h.v[0], &dA = lane_dA.v[0];
@@ -777,7 +832,7 @@ __global__ __launch_bounds__(kGradWaves * 64) __attribute__((amdgpu_waves_per_eu
         if (hi == en) {
             lane_g.start(gr.dfinal, pl, me, (uint32_t)s);
         } else {
-            join_spans<S, 1>(totals, pl, me, pl.span_of(span, en - 1), span + 1, -1, lane_A2, lane_g);
+            join_spans<S, 1, true>(totals, pl, me, pl.span_of(span, en - 1), span + 1, -1, lane_A2, lane_g);
         }
         typename X::P px[X::PIECES], pd[X::PIECES], pz[X::PIECES], py[X::PIECES];
         typename BC::P pb[BC::PIECES], pc[BC::PIECES];
@@ -1038,10 +1093,10 @@ __global__ __launch_bounds__(kGradWaves * 64) void grad_empty_kernel(Plan pl, co
                                                                  float* __restrict__ dinitial)
 {
     const uint32_t block = blockIdx.x % pl.blocks;
-    const Place<16> me(pl, block);
+    const Place<16, true> me(pl, block);
     for (uint32_t s = blockIdx.x / pl.blocks; s < pl.seqs.count; s += kEmptyStep) {
         if (pl.seqs.end(s) > pl.seqs.start(s)) continue;
-        LaneStates<S, 1> g;
+        LaneStates<S, 1, true> g;
         g.start(dfinal, pl, me, s);
         g.store(dinitial + (size_t)s * pl.channels * pl.states, pl, me);
     }
@@ -1210,11 +1265,11 @@ scan_status_t forward(const selective_scan_args_t& a, hipStream_t stream)
         if (wgs + extra > 0x7FFFFFFFu) return SCAN_ERR_INVALID;
         if (p.per_seq > 1)
             hipLaunchKernelGGL((in.vec ? scan_kernel<T, S, true, true> : scan_kernel<T, S, false, true>), dim3((unsigned)wgs),
-                               dim3(kFwdWaves * 64), 0, stream, p, in, w.totals, (void*)nullptr, (int64_t)0, (float*)nullptr,
+                               dim3(Fwd<S>::WAVES * 64), 0, stream, p, in, w.totals, (void*)nullptr, (int64_t)0, (float*)nullptr,
                                (float*)nullptr);
         if (wgs + extra)
             hipLaunchKernelGGL((in.vec ? scan_kernel<T, S, true, false> : scan_kernel<T, S, false, false>),
-                               dim3((unsigned)(wgs + extra)), dim3(kFwdWaves * 64), 0, stream, p, in, w.totals, a.y, a.y_stride,
+                               dim3((unsigned)(wgs + extra)), dim3(Fwd<S>::WAVES * 64), 0, stream, p, in, w.totals, a.y, a.y_stride,
                                a.final_state, a.saved);
         return launched();
     });
