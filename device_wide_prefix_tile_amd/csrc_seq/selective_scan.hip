@@ -370,19 +370,22 @@ __device__ __forceinline__ void step_sizes(const float (&delta)[V], const float 
 // columns of 16 by four rows of 16 (a fused product of 32-bit values, exact but for its one rounding)
 // and leaves state 4 q + i of channel d in lane 16 q + d, where the recurrence wants it.  Left per row,
 // channel and state: a product and an exponential for the factor, a fused multiply-add for the state,
-// one for the output.  With up to 16 states a lane has two channels, which share what it reads of C.
-template <int S>
-struct Fwd {
-    static constexpr int CW = S == 4 ? 32 : 16, WAVES = kWgChannels / CW;
-};
+// one for the output.  Counted on 16384 rows of 2048 channels: 56 vector instructions per row and 16
+// channels for 64 lanes x 4 states, the vector units busy 83% of the time.
+//
+// CH channels per lane: two would share what a lane reads of C, but need 248 registers (two wavefronts
+// per SIMD); one, held to 168 for three, measured 190 against 207 us on ragged prompts (6001 x 4096)
+// and the same on one prompt (16384 x 2048).
+constexpr int kFwdWaveChannels = 16;
+constexpr int kFwdWaves = kWgChannels / kFwdWaveChannels;
 
 // TOTALS: the span's totals only.
 template <typename T, int S, bool VEC, bool TOTALS>
-__global__ __launch_bounds__(Fwd<S>::WAVES * 64) __attribute__((amdgpu_waves_per_eu(S == 16 ? 1 : 2))) void scan_kernel(Plan pl, Inputs in, SpanTotals totals, void* y,
+__global__ __launch_bounds__(kFwdWaves * 64) __attribute__((amdgpu_waves_per_eu(S == 16 ? 1 : S == 8 ? 2 : 3))) void scan_kernel(Plan pl, Inputs in, SpanTotals totals, void* y,
                                                                   int64_t y_stride, float* final_state, float* saved)
 {
     using C = Cfg<S>;
-    constexpr int TT = C::TT, NP = C::NP, CW = Fwd<S>::CW, CH = CW / 16, WAVES = Fwd<S>::WAVES, BLK = S / 4;
+    constexpr int TT = C::TT, NP = C::NP, CW = kFwdWaveChannels, CH = CW / 16, WAVES = kFwdWaves, BLK = S / 4;
     using X = Tile<T, TT, CW, VEC>;
     using BC = StateTile<T, TT, NP, 64, VEC>;
     constexpr int V = X::V;
@@ -1103,7 +1106,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void grad_empty_kernel(Plan pl, co
 }
 
 // ------------------------------------------------------------ host side
-// Workgroups that the rows are cut for: 1024 make two wavefronts of the forward kernels per SIMD.
+// Workgroups (of four wavefronts) that the rows are cut for.
 // Measured (16384 x 2048 channels / ragged 6001 x 4096 / training 4 x 2048 x 4096): 512 workgroups
 // 475 / 349 / 1478 us, 1024 259 / 212 / 1239, 2048 316 / 215 / 1250.
 constexpr uint32_t kTargetWorkgroups = 1024;
@@ -1265,11 +1268,11 @@ scan_status_t forward(const selective_scan_args_t& a, hipStream_t stream)
         if (wgs + extra > 0x7FFFFFFFu) return SCAN_ERR_INVALID;
         if (p.per_seq > 1)
             hipLaunchKernelGGL((in.vec ? scan_kernel<T, S, true, true> : scan_kernel<T, S, false, true>), dim3((unsigned)wgs),
-                               dim3(Fwd<S>::WAVES * 64), 0, stream, p, in, w.totals, (void*)nullptr, (int64_t)0, (float*)nullptr,
+                               dim3(kFwdWaves * 64), 0, stream, p, in, w.totals, (void*)nullptr, (int64_t)0, (float*)nullptr,
                                (float*)nullptr);
         if (wgs + extra)
             hipLaunchKernelGGL((in.vec ? scan_kernel<T, S, true, false> : scan_kernel<T, S, false, false>),
-                               dim3((unsigned)(wgs + extra)), dim3(Fwd<S>::WAVES * 64), 0, stream, p, in, w.totals, a.y, a.y_stride,
+                               dim3((unsigned)(wgs + extra)), dim3(kFwdWaves * 64), 0, stream, p, in, w.totals, a.y, a.y_stride,
                                a.final_state, a.saved);
         return launched();
     });
