@@ -96,12 +96,15 @@ def _lib():
 
 
 # ---------------------------------------------------------------------- calls
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _enqueue(x: torch.Tensor, stream, call):
     """call(handle) with x's device current, on the stream asked for: torch allocates on that
     stream inside, so memory that is let go is reused in its order."""
-    index = x.device.index
-    if stream is None and torch.cuda.current_device() == index:  # the usual case, without context managers
-        return call(_raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream)
+    index = x.get_device()
+    if stream is None and _raw_stream is not None and _current_device() == index:
+        return call(_raw_stream(index))  # the usual case, without context managers
     with torch.cuda.device(index):
         if stream is None:
             return call(torch.cuda.current_stream().cuda_stream)
@@ -127,21 +130,28 @@ def _ptr(t):
 
 
 def _on(x: torch.Tensor, name: str, t: torch.Tensor):
-    if t.device != x.device:
+    if t.get_device() != x.get_device():
         raise ValueError("%s must be on the device of the other tensors" % name)
 
 
-def _rows(t: torch.Tensor, name: str, shape=None, like: Optional[torch.Tensor] = None, inner: int = 1):
-    """Row stride of t, whose last `inner` dimensions are contiguous and whose leading ones are one flat run of rows."""
-    if shape is not None and t.shape != shape:
+def _refuse(t: torch.Tensor, name: str, shape, dtype):
+    """What is wrong with t, which was to have that shape and type and lie on the other tensors' device."""
+    if t.shape != shape:
         raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
-    if like is not None:
-        if t.dtype != like.dtype:
-            raise TypeError("%s must be %s" % (name, like.dtype))
-        if t.device != like.device:
-            raise ValueError("%s must be on the device of the other tensors" % name)
-    size, st = t.shape, t.stride()
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s" % (name, dtype))
+    raise ValueError("%s must be on the device of the other tensors" % name)
+
+
+def _rows(t: torch.Tensor, name: str, inner: int = 1):
+    """Row stride of t, whose last `inner` dimensions are contiguous and whose leading ones are one flat run of rows."""
+    size = t.shape
+    if t.is_contiguous():
+        return size[-1] if inner == 1 else size[-1] * size[-2]
+    st = t.stride()
     n = len(size)
+    if n == 2 and inner == 1 and st[1] == 1 and st[0] >= size[1]:  # a slice of wider rows
+        return st[0]
     width = 1
     for k in range(n - 1, n - 1 - inner, -1):
         if size[k] != 1 and st[k] != width:
@@ -162,16 +172,24 @@ def _rows(t: torch.Tensor, name: str, shape=None, like: Optional[torch.Tensor] =
     return max(row, width)
 
 
-def _plain(t: torch.Tensor, name: str, shape, dtype, device):
-    if t.shape != tuple(shape):
-        raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s" % (name, dtype))
-    if t.device != device:
-        raise ValueError("%s must be on the device of the other tensors" % name)
+def _plain(t: torch.Tensor, name: str, shape, dtype, device: int):
+    """Address of t, a contiguous tensor of that shape, type and device (its index; -1: the host); None for None."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype != dtype or t.get_device() != device:
+        _refuse(t, name, shape, dtype)
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
     return t.data_ptr()
+
+
+def _like(t: torch.Tensor, name: str, shape, dtype, device: int, width: int, inner: int = 1):
+    """(address, row stride) of t, rows of `width` values in that shape, type and device; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if t.shape != shape or t.dtype != dtype or t.get_device() != device:
+        _refuse(t, name, shape, dtype)
+    return t.data_ptr(), width if t.is_contiguous() else _rows(t, name, inner)
 
 
 def _x(x: torch.Tensor, name: str = "x"):
@@ -195,20 +213,22 @@ def _lengths(x: torch.Tensor, seq_offsets):
     return x.shape[0], seq_offsets.shape[0] - 1, seq_offsets.data_ptr()
 
 
-def _out(out, x: torch.Tensor, name: str, shape=None):
-    shape = x.shape if shape is None else shape
+def _out(out, x: torch.Tensor, name: str):
+    """(tensor, address, row stride) of an output shaped like x: `out`, or a new one."""
     if out is None:
-        return torch.empty(shape, dtype=x.dtype, device=x.device)
-    if out.shape != shape:
-        raise ValueError("%s must have shape %s" % (name, tuple(shape)))
-    return out
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        return out, out.data_ptr(), x.shape[-1]
+    return (out,) + _like(out, name, x.shape, x.dtype, x.get_device(), x.shape[-1])
 
 
-def _optional_state(state, shape, dtype, device):
-    """`state` may be a tensor to write into, or True for a new one."""
+def _optional_state(state, name: str, shape, dtype, x: torch.Tensor):
+    """(tensor, address) of an output state: `state` may be a tensor to write into, or True for a new one."""
     if state is None or state is False:
-        return None
-    return torch.empty(shape, dtype=dtype, device=device) if state is True else state
+        return None, None
+    if state is True:
+        state = torch.empty(shape, dtype=dtype, device=x.device)
+        return state, state.data_ptr()
+    return state, _plain(state, name, shape, dtype, x.get_device())
 
 
 # ---------------------------------------------------------------------- embedding
@@ -227,18 +247,24 @@ def embedding_lookup(tokens: torch.Tensor, table: torch.Tensor, scale: float = 1
     tokens: int32 or int64 of any shape; table: (V, D) float32, float16 or bfloat16."""
     size = _tokens(tokens)
     _x(table, "table")
-    if table.dim() != 2 or table.shape[0] < 1 or table.shape[1] < 1:
+    if table.dim() != 2:
+        raise ValueError("table must be (V, D)")
+    v, d = table.shape
+    if v < 1 or d < 1:
         raise ValueError("table must be (V, D)")
     _on(tokens, "table", table)
     stride = _rows(table, "table")
-    shape = tokens.shape + table.shape[1:]
+    shape = tokens.shape + (d,)
 
     def call(handle):
-        y = _out(out, table, "out", shape)
-        if y.dtype != table.dtype or y.device != table.device or not y.is_contiguous():
-            raise ValueError("out must be a contiguous tensor of the table's type and device")
+        if out is None:
+            y = torch.empty(shape, dtype=table.dtype, device=table.device)
+            to = y.data_ptr()
+        else:
+            y = out
+            to = _plain(y, "out", shape, table.dtype, table.get_device())
         _check(_lib().embedding_lookup(_DTYPE[table.dtype], tokens.data_ptr(), size, tokens.numel(), table.data_ptr(), stride,
-                                       table.shape[0], table.shape[1], scale, y.data_ptr(), handle), "embedding_lookup")
+                                       v, d, scale, to, handle), "embedding_lookup")
         return y
 
     return _enqueue(tokens, stream, call)
@@ -267,9 +293,8 @@ def embedding_grad(tokens: torch.Tensor, dout: torch.Tensor, n_rows: int, scale:
 
     def call(handle):
         L = _lib()
-        g = _out(out, dout, "out", (n_rows, d))
-        if g.dtype not in (dout.dtype, torch.float32) or g.device != dout.device or not g.is_contiguous():
-            raise ValueError("out must be a contiguous tensor of dout's type or float32, on its device")
+        g = torch.empty((n_rows, d), dtype=dout.dtype, device=dout.device) if out is None else out
+        _plain(g, "out", (n_rows, d), torch.float32 if g.dtype == torch.float32 else dout.dtype, dout.get_device())
         need = L.embedding_grad_workspace(n, n_rows, d)
         ws = torch.empty(need, dtype=torch.uint8, device=dout.device)
         _check(L.embedding_grad(_DTYPE[dout.dtype], _DTYPE[g.dtype], tokens.data_ptr(), size, n, dout.data_ptr(), stride,
@@ -289,25 +314,30 @@ class ConvGrads(NamedTuple):
     dinitial_state: Optional[torch.Tensor]
 
 
-def _conv_args(x, weight, bias, activation, seq_offsets, initial_state):
-    _x(x)
-    rows, seqs, offsets = _lengths(x, seq_offsets)
-    d = x.shape[-1]
-    if weight.dim() != 2 or weight.shape[0] != d or not 2 <= weight.shape[1] <= 4:
+def _conv_weights(x, weight, bias, activation):
+    """(weight type code, activation code, K, D, weight address, bias address)"""
+    if weight.dim() != 2:
+        raise ValueError("weight must be (D, K) with K in 2 .. 4")
+    d, k = weight.shape
+    if d != x.shape[-1] or not 2 <= k <= 4:
         raise ValueError("weight must be (D, K) with K in 2 .. 4")
     if activation not in _ACT:
         raise ValueError("activation must be None or 'silu'")
-    k, wt = weight.shape[1], weight.dtype
+    wt, device = weight.dtype, x.get_device()
     if wt != x.dtype and wt != torch.float32:
         raise TypeError("weight must be of x's type or float32")
-    a = _ConvArgs(dtype=_DTYPE[x.dtype], weight_dtype=_DTYPE[wt], activation=_ACT[activation], width=k, rows=rows, seqs=seqs,
-                  seq_offsets=offsets, channels=d, x=x.data_ptr(), x_stride=_rows(x, "x"),
-                  weight=_plain(weight, "weight", (d, k), wt, x.device))
-    if bias is not None:
-        a.bias = _plain(bias, "bias", (d,), wt, x.device)
-    if initial_state is not None:
-        a.initial_state = _plain(initial_state, "initial_state", (seqs, k - 1, d), x.dtype, x.device)
-    return a, seqs, k, d
+    return (_DTYPE[wt], _ACT[activation], k, d, _plain(weight, "weight", (d, k), wt, device),
+            _plain(bias, "bias", (d,), wt, device))
+
+
+def _conv_args(x, weight, bias, activation, seq_offsets, initial_state):
+    _x(x)
+    rows, seqs, offsets = _lengths(x, seq_offsets)
+    wt, act, k, d, w, b = _conv_weights(x, weight, bias, activation)
+    state = (seqs, k - 1, d)
+    a = _ConvArgs(_DTYPE[x.dtype], wt, act, k, rows, seqs, offsets, d, 0, x.data_ptr(), _rows(x, "x"), w, b,
+                  _plain(initial_state, "initial_state", state, x.dtype, x.get_device()))
+    return a, state
 
 
 def causal_conv1d(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
@@ -321,14 +351,11 @@ def causal_conv1d(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Te
     first, else they are zero.  final_state: a tensor (S, K - 1, D) for the last K - 1 inputs of
     every sequence, or True for a new one: (y, final_state) is returned then, else y.  Rows of y
     that belong to no sequence are not written."""
-    a, seqs, k, d = _conv_args(x, weight, bias, activation, seq_offsets, initial_state)
+    a, state = _conv_args(x, weight, bias, activation, seq_offsets, initial_state)
 
     def call(handle):
-        y = _out(out, x, "out")
-        a.y, a.y_stride = y.data_ptr(), _rows(y, "out", x.shape, x)
-        fin = _optional_state(final_state, (seqs, k - 1, d), x.dtype, x.device)
-        if fin is not None:
-            a.final_state = _plain(fin, "final_state", (seqs, k - 1, d), x.dtype, x.device)
+        y, a.y, a.y_stride = _out(out, x, "out")
+        fin, a.final_state = _optional_state(final_state, "final_state", state, x.dtype, x)
         _check(_lib().causal_conv1d(ctypes.byref(a), handle), "causal_conv1d")
         return y if fin is None else (y, fin)
 
@@ -342,15 +369,13 @@ def causal_conv1d_grad(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, 
     """Gradients of ``causal_conv1d`` (its arguments) for dy, and for dfinal_state if given.
 
     dx may be given to write into (a slice of a wider tensor, say)."""
-    a, seqs, k, d = _conv_args(x, weight, bias, activation, seq_offsets, initial_state)
-    g = _ConvGradArgs(args=a, dy=dy.data_ptr(), dy_stride=_rows(dy, "dy", x.shape, x))
-    if dfinal_state is not None:
-        g.dfinal_state = _plain(dfinal_state, "dfinal_state", (seqs, k - 1, d), x.dtype, x.device)
+    a, state = _conv_args(x, weight, bias, activation, seq_offsets, initial_state)
+    d, k = weight.shape
+    g = _ConvGradArgs(a, *_like(dy, "dy", x.shape, x.dtype, x.get_device(), x.shape[-1]), _plain(dfinal_state, "dfinal_state", state, x.dtype, x.get_device()))
 
     def call(handle):
         L = _lib()
-        ox = _out(dx, x, "dx")
-        g.dx, g.dx_stride = ox.data_ptr(), _rows(ox, "dx", x.shape, x)
+        ox, g.dx, g.dx_stride = _out(dx, x, "dx")
         dw = torch.empty(d, k, dtype=torch.float32, device=x.device)
         db = None if bias is None else torch.empty(d, dtype=torch.float32, device=x.device)
         di = None if initial_state is None else torch.empty_like(initial_state)
@@ -369,7 +394,7 @@ def _slots(x, slots, n_slots):
         if n_slots < x.shape[0]:
             raise ValueError("state has fewer slots than x has rows")
         return None
-    return _plain(slots, "slots", (x.shape[0],), torch.int32, x.device)
+    return _plain(slots, "slots", (x.shape[0],), torch.int32, x.get_device())
 
 
 def causal_conv1d_step(x: torch.Tensor, state: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
@@ -381,25 +406,15 @@ def causal_conv1d_step(x: torch.Tensor, state: torch.Tensor, weight: torch.Tenso
     slots: int32 (rows,), distinct within a call; None: row i has slot i.  A row whose slot lies
     outside the state is skipped: its row of y is not written."""
     _x(x)
-    if x.dim() != 2 or state.dim() != 3 or weight.dim() != 2:
-        raise ValueError("x must be (rows, D), state (n_slots, K - 1, D), weight (D, K)")
-    if activation not in _ACT:
-        raise ValueError("activation must be None or 'silu'")
-    d, k, wt = x.shape[1], weight.shape[1], weight.dtype
-    if weight.shape[0] != d or not 2 <= k <= 4:
-        raise ValueError("weight must be (D, K) with K in 2 .. 4")
-    if wt != x.dtype and wt != torch.float32:
-        raise TypeError("weight must be of x's type or float32")
-    n = state.shape[0]
-    a = _ConvStepArgs(dtype=_DTYPE[x.dtype], weight_dtype=_DTYPE[wt], activation=_ACT[activation], width=k, rows=x.shape[0],
-                      n_slots=n, slots=_slots(x, slots, n), channels=d, x=x.data_ptr(), x_stride=_rows(x, "x"),
-                      weight=_plain(weight, "weight", (d, k), wt, x.device),
-                      bias=None if bias is None else _plain(bias, "bias", (d,), wt, x.device),
-                      state=_plain(state, "state", (n, k - 1, d), x.dtype, x.device))
+    if x.dim() != 2 or state.dim() != 3:
+        raise ValueError("x must be (rows, D), state (n_slots, K - 1, D)")
+    wt, act, k, d, w, b = _conv_weights(x, weight, bias, activation)
+    n, device = state.shape[0], x.get_device()
+    a = _ConvStepArgs(_DTYPE[x.dtype], wt, act, k, x.shape[0], n, _slots(x, slots, n), d, 0, x.data_ptr(), _rows(x, "x"), w, b,
+                      _plain(state, "state", (n, k - 1, d), x.dtype, device))
 
     def call(handle):
-        y = _out(out, x, "out")
-        a.y, a.y_stride = y.data_ptr(), _rows(y, "out", x.shape, x)
+        y, a.y, a.y_stride = _out(out, x, "out")
         _check(_lib().causal_conv1d_step(ctypes.byref(a), handle), "causal_conv1d_step")
         return y
 
@@ -420,41 +435,31 @@ class ScanGrads(NamedTuple):
     dinitial_state: Optional[torch.Tensor]
 
 
-def _scan_inputs(a, x, delta, A, B, C, D, z, delta_bias, delta_softplus):
-    """Fills the fields that every form of the scan has; returns (channels, states)."""
+def _scan_inputs(x, delta, A, B, C, D, z, delta_bias):
+    """The fields of _SCAN_INPUTS."""
     if A.dim() != 2 or B.dim() < 2:
         raise ValueError("A must be (D, N), B and C x.shape[:-1] + (groups, N)")
     d, n = A.shape
-    groups = B.shape[-2]
-    if x.shape[-1] != d or not 1 <= n <= 64:
+    groups, shape, device, t = B.shape[-2], x.shape, x.get_device(), x.dtype
+    if shape[-1] != d or not 1 <= n <= 64:
         raise ValueError("A must be (D, N) with N in 1 .. 64")
     if groups < 1 or d % groups:
         raise ValueError("the groups of B and C must divide the channels")
-    bc = x.shape[:-1] + (groups, n)
-    a.dtype, a.delta_softplus = _DTYPE[x.dtype], 1 if delta_softplus else 0
-    a.channels, a.states, a.groups = d, n, groups
-    a.x, a.x_stride = x.data_ptr(), _rows(x, "x")
-    a.delta, a.delta_stride = delta.data_ptr(), _rows(delta, "delta", x.shape, x)
-    a.A = _plain(A, "A", (d, n), torch.float32, x.device)
-    a.B, a.b_stride = B.data_ptr(), _rows(B, "B", bc, x, 2)
-    a.C, a.c_stride = C.data_ptr(), _rows(C, "C", bc, x, 2)
-    if D is not None:
-        a.D = _plain(D, "D", (d,), torch.float32, x.device)
-    if z is not None:
-        a.z, a.z_stride = z.data_ptr(), _rows(z, "z", x.shape, x)
-    if delta_bias is not None:
-        a.delta_bias = _plain(delta_bias, "delta_bias", (d,), torch.float32, x.device)
-    return d, n
+    bc = shape[:-1] + (groups, n)
+    f32 = torch.float32
+    return (d, n, groups, 0, x.data_ptr(), _rows(x, "x"), *_like(delta, "delta", shape, t, device, d),
+            _plain(A, "A", (d, n), f32, device), *_like(B, "B", bc, t, device, groups * n, 2),
+            *_like(C, "C", bc, t, device, groups * n, 2), _plain(D, "D", (d,), f32, device),
+            *_like(z, "z", shape, t, device, d), _plain(delta_bias, "delta_bias", (d,), f32, device))
 
 
 def _scan_args(x, delta, A, B, C, D, z, delta_bias, delta_softplus, seq_offsets, initial_state):
     _x(x)
-    a = _ScanArgs()
-    a.rows, a.seqs, a.seq_offsets = _lengths(x, seq_offsets)
-    d, n = _scan_inputs(a, x, delta, A, B, C, D, z, delta_bias, delta_softplus)
-    if initial_state is not None:
-        a.initial_state = _plain(initial_state, "initial_state", (a.seqs, d, n), torch.float32, x.device)
-    return a, (a.seqs, d, n)
+    rows, seqs, offsets = _lengths(x, seq_offsets)
+    inputs = _scan_inputs(x, delta, A, B, C, D, z, delta_bias)
+    state = (seqs, inputs[0], inputs[1])
+    return _ScanArgs(_DTYPE[x.dtype], 1 if delta_softplus else 0, rows, seqs, offsets, *inputs,
+                     _plain(initial_state, "initial_state", state, torch.float32, x.get_device())), state
 
 
 def selective_scan(x: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
@@ -477,12 +482,10 @@ def selective_scan(x: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, B: tor
 
     def call(handle):
         L = _lib()
-        y = _out(out, x, "out")
-        a.y, a.y_stride = y.data_ptr(), _rows(y, "out", x.shape, x)
+        y, a.y, a.y_stride = _out(out, x, "out")
         got = [y]
-        fin = _optional_state(final_state, state, torch.float32, x.device)
+        fin, a.final_state = _optional_state(final_state, "final_state", state, torch.float32, x)
         if fin is not None:
-            a.final_state = _plain(fin, "final_state", state, torch.float32, x.device)
             got.append(fin)
         if save_for_grad:
             saved = torch.empty(L.selective_scan_saved(ctypes.byref(a)), dtype=torch.float32, device=x.device)
@@ -509,9 +512,8 @@ def selective_scan_grad(dy: torch.Tensor, x: torch.Tensor, delta: torch.Tensor, 
     it the states are scanned again.  dx and dz may be given to write into (two slices of one
     tensor, say)."""
     a, state = _scan_args(x, delta, A, B, C, D, z, delta_bias, delta_softplus, seq_offsets, initial_state)
-    g = _ScanGradArgs(dy=dy.data_ptr(), dy_stride=_rows(dy, "dy", x.shape, x))
-    if dfinal_state is not None:
-        g.dfinal_state = _plain(dfinal_state, "dfinal_state", state, torch.float32, x.device)
+    g = _ScanGradArgs(a, *_like(dy, "dy", x.shape, x.dtype, x.get_device(), x.shape[-1]),
+                      _plain(dfinal_state, "dfinal_state", state, torch.float32, x.get_device()))
     if dz is not None and z is None:
         raise ValueError("dz given without z")
 
@@ -526,23 +528,18 @@ def selective_scan_grad(dy: torch.Tensor, x: torch.Tensor, delta: torch.Tensor, 
             ws = torch.empty(need, dtype=torch.uint8, device=x.device)
             a.saved, a.workspace, a.workspace_bytes = states.data_ptr(), ws.data_ptr(), need
             _check(L.selective_scan(ctypes.byref(a), handle), "selective_scan")
-        a.saved = _plain(states, "saved", (need_saved,), torch.float32, x.device)
-        ox = _out(dx, x, "dx")
-        od = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        oz = None if z is None else _out(dz, x, "dz")
+        a.saved = _plain(states, "saved", (need_saved,), torch.float32, x.get_device())
+        g.args = a
+        ox, g.dx, g.dx_stride = _out(dx, x, "dx")
+        od, g.ddelta, g.ddelta_stride = _out(None, x, "ddelta")
+        oz, g.dz, g.dz_stride = (None, None, 0) if z is None else _out(dz, x, "dz")
         oB = torch.empty(B.shape, dtype=x.dtype, device=x.device)
         oC = torch.empty(C.shape, dtype=x.dtype, device=x.device)
         oA = torch.empty(A.shape, **f32)
         oD = None if D is None else torch.empty(D.shape, **f32)
         ob = None if delta_bias is None else torch.empty(delta_bias.shape, **f32)
         oi = None if initial_state is None else torch.empty(state, **f32)
-        g.args = a
-        g.dx, g.dx_stride = ox.data_ptr(), _rows(ox, "dx", x.shape, x)
-        g.ddelta, g.ddelta_stride = od.data_ptr(), _rows(od, "ddelta")
-        if oz is not None:
-            g.dz, g.dz_stride = oz.data_ptr(), _rows(oz, "dz", x.shape, x)
-        g.dB, g.db_stride = oB.data_ptr(), _rows(oB, "dB", inner=2)
-        g.dC, g.dc_stride = oC.data_ptr(), _rows(oC, "dC", inner=2)
+        g.dB, g.db_stride, g.dC, g.dc_stride = oB.data_ptr(), _rows(oB, "dB", 2), oC.data_ptr(), _rows(oC, "dC", 2)
         g.dA, g.dD, g.ddelta_bias, g.dinitial_state = oA.data_ptr(), _ptr(oD), _ptr(ob), _ptr(oi)
         need = L.selective_scan_grad_workspace(ctypes.byref(g))
         ws = torch.empty(need, dtype=torch.uint8, device=x.device)
@@ -565,15 +562,13 @@ def selective_scan_step(x: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, B
     _x(x)
     if x.dim() != 2 or state.dim() != 3:
         raise ValueError("x must be (rows, D), state (n_slots, D, N)")
-    a = _ScanStepArgs()
-    d, n = _scan_inputs(a, x, delta, A, B, C, D, z, delta_bias, delta_softplus)
-    a.rows, a.n_slots = x.shape[0], state.shape[0]
-    a.slots = _slots(x, slots, state.shape[0])
-    a.state = _plain(state, "state", (state.shape[0], d, n), torch.float32, x.device)
+    inputs = _scan_inputs(x, delta, A, B, C, D, z, delta_bias)
+    slot_count = state.shape[0]
+    a = _ScanStepArgs(_DTYPE[x.dtype], 1 if delta_softplus else 0, x.shape[0], slot_count, _slots(x, slots, slot_count), *inputs,
+                      _plain(state, "state", (slot_count, inputs[0], inputs[1]), torch.float32, x.get_device()))
 
     def call(handle):
-        y = _out(out, x, "out")
-        a.y, a.y_stride = y.data_ptr(), _rows(y, "out", x.shape, x)
+        y, a.y, a.y_stride = _out(out, x, "out")
         _check(_lib().selective_scan_step(ctypes.byref(a), handle), "selective_scan_step")
         return y
 
