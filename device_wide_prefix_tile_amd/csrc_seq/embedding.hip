@@ -17,11 +17,11 @@
 //           place of each token, and a second walk that writes the positions.
 //           Up to 65536 tokens that is one launch; above, the counts of every
 //           segment go through memory (three launches).
-//   pieces: rows with more than kPiece positions are cut along the windows of
-//           kPiece sorted positions; each window's part of such a row is
-//           summed by a wavefront of its own (32 bits, to the workspace).
-//   rows:   every row of the table: the sum of its positions, or of its
-//           pieces, or zero.
+//   sums:   rows with more than kPiece positions are cut along the windows of
+//           kPiece sorted positions, and each window's part of such a row is
+//           summed by a workgroup of its own (32 bits, to the workspace);
+//           every other row is summed whole, or zero.  One launch.
+//   join:   the rows of pieces.
 #include "seq_common.hpp"
 
 namespace dwpt_seq {
@@ -36,6 +36,9 @@ constexpr size_t kMaxRows = (size_t)1 << 24;
 
 struct GroupPlan {
     uint32_t n, v, segments, buckets, log_buckets, per;  // per: table rows per bucket
+    // place of table row r in start and count, and the row of a place
+    __host__ __device__ uint32_t slot(uint32_t r) const { return (r & (buckets - 1)) * per + (r >> log_buckets); }
+    __host__ __device__ uint32_t row(uint32_t slot) const { return slot % per << log_buckets | slot / per; }
 };
 
 GroupPlan make_plan(size_t n, size_t v)
@@ -54,9 +57,10 @@ GroupPlan make_plan(size_t n, size_t v)
     return p;
 }
 
-// Workspace: order[n], start[v], count[v] (uint32); with several segments the counts
-// [segment][bucket][per] and the buckets' totals [segment][bucket]; the pieces' sums
-// [window][2][channels] (float).
+// Workspace: order[n], start[buckets * per], count[buckets * per] (uint32, a bucket's rows side by
+// side: scattered over the table's order, their 4-byte writes took as long as the rest of the
+// grouping); with several segments the counts [segment][bucket][per] and the buckets' totals
+// [segment][bucket]; the pieces' sums [window][2][channels] (float).
 struct GroupSpace {
     uint32_t *order, *start, *count, *grouped, *seg_counts, *totals;  // grouped: number of positions in order
     float* pieces;
@@ -73,8 +77,8 @@ GroupSpace lay_out(const GroupPlan& p, uint32_t channels, void* base)
         return q;
     };
     s.order = reinterpret_cast<uint32_t*>(take((size_t)p.n * 4));
-    s.start = reinterpret_cast<uint32_t*>(take((size_t)p.v * 4));
-    s.count = reinterpret_cast<uint32_t*>(take((size_t)p.v * 4));
+    s.start = reinterpret_cast<uint32_t*>(take((size_t)p.buckets * p.per * 4));
+    s.count = reinterpret_cast<uint32_t*>(take((size_t)p.buckets * p.per * 4));
     s.grouped = reinterpret_cast<uint32_t*>(take(4));
     if (p.segments > 1) {
         s.seg_counts = reinterpret_cast<uint32_t*>(take((size_t)p.segments * p.buckets * p.per * 4));
@@ -91,6 +95,35 @@ __device__ __forceinline__ uint32_t table_row(const I* __restrict__ tokens, uint
 {
     const I t = tokens[i];
     return t >= 0 && t < (I)v ? (uint32_t)t : v;
+}
+
+// Rounds of 64 tokens whose loads are in flight together.  Every workgroup looks at every token, so
+// what that costs bounds the grouping: per round four vector instructions in the first walk, three
+// in the second, the rest on the scalar unit (with branches per lane instead, and one round's loads
+// at a time, 65536 tokens took 54 us).
+constexpr int kRounds = 16;
+
+// Token as an unsigned number that is at least 2^31 for every token outside a table.
+__device__ __forceinline__ uint32_t as_row(int32_t t) { return (uint32_t)t; }
+__device__ __forceinline__ uint32_t as_row(int64_t t) { return (uint64_t)t >> 31 ? 0xFFFFFFFFu : (uint32_t)t; }
+
+template <typename I>
+__device__ __forceinline__ void load_rounds(const I* __restrict__ tokens, uint32_t base, uint32_t hi, int lane,
+                                            uint32_t (&r)[kRounds])
+{
+    if (base + 64 * kRounds <= hi) {
+        I t[kRounds];
+#pragma unroll
+        for (int u = 0; u < kRounds; ++u) t[u] = tokens[base + lane + u * 64];
+#pragma unroll
+        for (int u = 0; u < kRounds; ++u) r[u] = as_row(t[u]);
+    } else {
+#pragma unroll
+        for (int u = 0; u < kRounds; ++u) {
+            const uint32_t i = base + lane + u * 64;
+            r[u] = i < hi ? as_row(tokens[i]) : 0xFFFFFFFFu;
+        }
+    }
 }
 
 // ------------------------------------------------------------ grouping
@@ -116,22 +149,30 @@ __global__ __launch_bounds__(kGroupBlock) void group_kernel(const I* __restrict_
     const uint32_t first = seg * kSegment;
     const uint32_t cnt = p.n - first < kSegment ? p.n - first : kSegment;
     const uint32_t m = (((cnt + kGroupWaves - 1) / kGroupWaves) + 63u) & ~63u;
-    const uint32_t lo = min((uint32_t)w * m, cnt) + first, hi = min((uint32_t)(w + 1) * m, cnt) + first;
+    const uint32_t lo = (uint32_t)uniform((int)(min((uint32_t)w * m, cnt) + first));
+    const uint32_t hi = (uint32_t)uniform((int)(min((uint32_t)(w + 1) * m, cnt) + first));
     uint32_t* my = s_cnt + (uint32_t)w * p.per;
-    uint32_t lower = 0;  // tokens of smaller buckets, in this lane
-#pragma unroll 4
-    for (uint32_t i = lo + lane; i < hi; i += 64) {
-        const uint32_t r = table_row(tokens, i, p.v);
-        if (r < p.v) {
-            const uint32_t bk = r & mask;
-            if (bk == b) atomicAdd(my + (r >> p.log_buckets), 1u);
-            lower += bk < b;
+    uint32_t lower = 0;  // the wavefront's tokens of smaller buckets
+    for (uint32_t base = lo; base < hi; base += 64 * kRounds) {
+        uint32_t r[kRounds];
+        load_rounds(tokens, base, hi, lane, r);
+#pragma unroll
+        for (int u = 0; u < kRounds; ++u) {
+            const uint32_t bk = r[u] & mask;
+            const uint64_t inside = __builtin_amdgcn_ballot_w64(r[u] < p.v);
+            const uint64_t mine = __builtin_amdgcn_ballot_w64(bk == b) & inside;
+            if (MODE == 0) lower += __builtin_popcountll(__builtin_amdgcn_ballot_w64(bk < b) & inside);
+            if (mine) {
+                // LDS adds of many lanes to one word are slow: a round whose lanes hold one token adds once
+                const int leader = __builtin_ctzll(mine);
+                const uint32_t token = (uint32_t)__builtin_amdgcn_readlane((int)r[u], leader);
+                const bool one = (__builtin_amdgcn_ballot_w64(r[u] == token) & mine) == mine;
+                if (one ? lane == leader : (bool)(mine >> lane & 1))
+                    atomicAdd(my + (r[u] >> p.log_buckets), one ? (uint32_t)__builtin_popcountll(mine) : 1u);
+            }
         }
     }
-    if (MODE == 0) {
-        for (int o = 32; o > 0; o >>= 1) lower += __shfl_xor(lower, o, 64);
-        if (lane == 0) s_low[w] = lower;
-    }
+    if (MODE == 0 && lane == 0) s_low[w] = lower;
     __syncthreads();
 
     // the tokens' totals in this segment and their exclusive scan, each thread a run of them
@@ -170,17 +211,14 @@ __global__ __launch_bounds__(kGroupBlock) void group_kernel(const I* __restrict_
         uint32_t at = incl - sum;
         for (int q = 0; q < kGroupWaves; ++q) at += s_low[q] + (q < w ? s_part[q] : 0u);
         for (uint32_t l = l0; l < l1; ++l) {
-            const uint32_t row = (l << p.log_buckets) | b;
             const uint32_t begin = at;
             for (int q = 0; q < kGroupWaves; ++q) {
                 const uint32_t c = s_cnt[q * p.per + l];
                 s_cnt[q * p.per + l] = at;
                 at += c;
             }
-            if (row < p.v) {
-                start[row] = begin;
-                count[row] = at - begin;
-            }
+            start[b * p.per + l] = begin;
+            count[b * p.per + l] = at - begin;
         }
         if (b == p.buckets - 1 && threadIdx.x == kGroupBlock - 1) *grouped = at;  // the end of the last token's run
     } else {
@@ -197,23 +235,24 @@ __global__ __launch_bounds__(kGroupBlock) void group_kernel(const I* __restrict_
     __syncthreads();
 
     // second walk: the lanes of a round that hold one token take consecutive places
-    for (uint32_t base = lo; base < hi; base += 64) {
-        const uint32_t i = base + lane;
-        const uint32_t r = i < hi ? table_row(tokens, i, p.v) : p.v;
-        const bool mine = r < p.v && (r & mask) == b;
-        uint64_t left = __builtin_amdgcn_ballot_w64(mine);
-        while (left) {
-            const int leader = __builtin_ctzll(left);
-            const uint32_t token = (uint32_t)__builtin_amdgcn_readlane((int)r, leader);
-            const bool same = mine && r == token;
-            const uint64_t eq = __builtin_amdgcn_ballot_w64(same);
-            uint32_t* place = my + (token >> p.log_buckets);
-            const uint32_t at = *place;
-            if (same) order[at + __builtin_popcountll(eq & ((1ull << lane) - 1))] = i;
-            wave_sync();
-            if (lane == leader) *place = at + (uint32_t)__builtin_popcountll(eq);
-            wave_sync();
-            left &= ~eq;
+    for (uint32_t base = lo; base < hi; base += 64 * kRounds) {
+        uint32_t r[kRounds];
+        load_rounds(tokens, base, hi, lane, r);
+#pragma unroll
+        for (int u = 0; u < kRounds; ++u) {
+            const bool mine = r[u] < p.v && (r[u] & mask) == b;
+            uint64_t left = __builtin_amdgcn_ballot_w64(mine);
+            while (left) {
+                const int leader = __builtin_ctzll(left);
+                const uint32_t token = (uint32_t)__builtin_amdgcn_readlane((int)r[u], leader);
+                const bool same = mine && r[u] == token;
+                const uint64_t eq = __builtin_amdgcn_ballot_w64(same);
+                uint32_t at = 0;
+                if (lane == leader) at = atomicAdd(my + (token >> p.log_buckets), (uint32_t)__builtin_popcountll(eq));
+                at = (uint32_t)__builtin_amdgcn_readlane((int)at, leader);
+                if (same) order[at + __builtin_popcountll(eq & ((1ull << lane) - 1))] = base + u * 64 + lane;
+                left &= ~eq;
+            }
         }
     }
 }
@@ -251,17 +290,14 @@ __global__ __launch_bounds__(kGroupBlock) void group_places_kernel(GroupPlan p, 
     uint32_t at = incl - sum;
     for (int q = 0; q < kGroupWaves; ++q) at += s_low[q] + (q < w ? s_part[q] : 0u);
     for (uint32_t l = l0; l < l1; ++l) {
-        const uint32_t row = (l << p.log_buckets) | b;
         const uint32_t begin = at;
         for (uint32_t s = 0; s < p.segments; ++s) {
             const uint32_t c = mine[s * step + l];
             mine[s * step + l] = at;
             at += c;
         }
-        if (row < p.v) {
-            start[row] = begin;
-            count[row] = at - begin;
-        }
+        start[b * p.per + l] = begin;
+        count[b * p.per + l] = at - begin;
     }
     if (b == p.buckets - 1 && threadIdx.x == kGroupBlock - 1) *grouped = at;
 }
@@ -291,63 +327,18 @@ __device__ __forceinline__ void sum_rows(const T* __restrict__ dout, int64_t str
     }
 }
 
-// Window x (sorted positions [x * kPiece, ..)): the sums of its parts of rows with more than
-// kPiece positions.  At most two such rows touch a window: one that began before it or at its
-// start (slot 0), one that begins inside it (slot 1) and reaches its end.
-template <typename T, typename I, int V>
-__global__ __launch_bounds__(256) void piece_kernel(const I* __restrict__ tokens, const T* __restrict__ dout,
-                                                    int64_t stride, uint32_t v, uint32_t channels,
-                                                    const uint32_t* __restrict__ order,
-                                                    const uint32_t* __restrict__ start,
-                                                    const uint32_t* __restrict__ count, const uint32_t* __restrict__ grouped_at,
-                                                    float* __restrict__ pieces)
-{
-    const uint32_t x = blockIdx.x;
-    const uint32_t c = (blockIdx.y * 256 + threadIdx.x) * V;
-    // places behind the last grouped position (tokens outside the table have none) hold nothing
-    const uint32_t lo = x * kPiece;
-    const uint32_t grouped = *grouped_at;
-    if (lo >= grouped) return;
-    const uint32_t hi = min(lo + (uint32_t)kPiece, grouped);
-    const uint32_t r0 = table_row(tokens, order[lo], v), r1 = table_row(tokens, order[hi - 1], v);
-    if (c >= channels) return;
-#pragma unroll
-    for (int slot = 0; slot < 2; ++slot) {
-        const uint32_t r = slot ? r1 : r0;
-        const uint32_t s = start[r], n = count[r];
-        if (n <= (uint32_t)kPiece || (slot == 1) != (s > lo)) continue;
-        float acc[V] = {};
-        sum_rows<T, V>(dout, stride, order, max(s, lo), min(s + n, hi), c, acc);
-        float* out = pieces + ((size_t)x * 2 + slot) * channels + c;
-#pragma unroll
-        for (int k = 0; k < V; ++k) out[k] = acc[k];
-    }
-}
+// One launch sums everything but the pieces themselves.  Workgroups below `windows * columns`: window
+// x (sorted positions [x * kPiece, ..)), the sums of its parts of rows with more than kPiece
+// positions.  At most two such rows touch a window: one that began before it or at its start (slot
+// 0), one that begins inside it (slot 1) and reaches its end.  The others: kRows rows of the table per
+// wavefront, 64 * V columns; the first position of each is in flight together, as most rows have one
+// or none.  Rows of pieces are left to join_kernel.
+constexpr int kRows = 8;
 
-// Four rows of the table, one per wavefront: columns [c, c + V) per lane.
 template <typename T, typename O, int V>
-__global__ __launch_bounds__(256) void rows_kernel(const T* __restrict__ dout, int64_t stride, uint32_t v,
-                                                  uint32_t channels, const uint32_t* __restrict__ order,
-                                                  const uint32_t* __restrict__ start, const uint32_t* __restrict__ count,
-                                                  const float* __restrict__ pieces, float scale, int accumulate,
-                                                  O* __restrict__ dtable)
+__device__ __forceinline__ void store_row(O* __restrict__ dtable, uint32_t channels, uint32_t r, uint32_t c, float scale,
+                                          int accumulate, float (&acc)[V])
 {
-    const uint32_t r = blockIdx.x * 4 + (threadIdx.x >> 6);
-    const uint32_t c = (blockIdx.y * 64 + (threadIdx.x & 63)) * V;
-    if (r >= v || c >= channels) return;
-    const uint32_t n = (uint32_t)uniform((int)count[r]), s = (uint32_t)uniform((int)start[r]);
-    if (accumulate && n == 0) return;
-    float acc[V] = {};
-    if (n <= (uint32_t)kPiece) {
-        sum_rows<T, V>(dout, stride, order, s, s + n, c, acc);
-    } else {
-        const uint32_t last = (s + n - 1) / kPiece;
-        for (uint32_t x = s / kPiece; x <= last; ++x) {
-            const float* p = pieces + ((size_t)x * 2 + (s > x * kPiece ? 1 : 0)) * channels + c;
-#pragma unroll
-            for (int k = 0; k < V; ++k) acc[k] += p[k];
-        }
-    }
     O* out = dtable + (size_t)r * channels + c;
 #pragma unroll
     for (int k = 0; k < V; ++k) acc[k] *= scale;
@@ -358,6 +349,104 @@ __global__ __launch_bounds__(256) void rows_kernel(const T* __restrict__ dout, i
         for (int k = 0; k < V; ++k) acc[k] += had[k];
     }
     *reinterpret_cast<Pack<O, V>*>(out) = pack<O, V>(acc);
+}
+
+struct Sums {
+    GroupPlan plan;
+    uint32_t channels, columns, windows;  // columns: workgroups (of 256 * V columns) per window
+    int64_t stride;
+    const uint32_t *order, *start, *count, *grouped;
+    float* pieces;
+    float scale;
+    int accumulate;
+};
+
+template <typename T, typename O, typename I, int V>
+__global__ __launch_bounds__(256) void sums_kernel(Sums a, const I* __restrict__ tokens, const T* __restrict__ dout,
+                                                   O* __restrict__ dtable)
+{
+    if (blockIdx.x < a.windows * a.columns) {
+        const uint32_t x = blockIdx.x / a.columns;
+        const uint32_t c = (blockIdx.x % a.columns * 256 + threadIdx.x) * V;
+        // places behind the last grouped position (tokens outside the table have none) hold nothing
+        const uint32_t lo = x * kPiece;
+        const uint32_t grouped = *a.grouped;
+        if (lo >= grouped) return;
+        const uint32_t hi = min(lo + (uint32_t)kPiece, grouped);
+        const uint32_t r0 = table_row(tokens, a.order[lo], a.plan.v), r1 = table_row(tokens, a.order[hi - 1], a.plan.v);
+        if (c >= a.channels) return;
+#pragma unroll
+        for (int slot = 0; slot < 2; ++slot) {
+            const uint32_t at = a.plan.slot(slot ? r1 : r0);
+            const uint32_t s = a.start[at], n = a.count[at];
+            if (n <= (uint32_t)kPiece || (slot == 1) != (s > lo)) continue;
+            float acc[V] = {};
+            sum_rows<T, V>(dout, a.stride, a.order, max(s, lo), min(s + n, hi), c, acc);
+            *reinterpret_cast<Pack<float, V>*>(a.pieces + ((size_t)x * 2 + slot) * a.channels + c) = pack<float, V>(acc);
+        }
+        return;
+    }
+    const uint32_t chunks = (a.channels + 64 * V - 1) / (64 * V);
+    const uint32_t unit = (blockIdx.x - a.windows * a.columns) * 4 + (uint32_t)uniform((int)(threadIdx.x >> 6));
+    const uint32_t first = unit / chunks * kRows;
+    const uint32_t c = (unit % chunks * 64 + (threadIdx.x & 63)) * V;
+    const uint32_t slots = a.plan.buckets * a.plan.per;  // rows in the order of start and count
+    if (first >= slots || c >= a.channels) return;
+    uint32_t s[kRows], n[kRows];
+    Pack<T, V> p[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const bool in = first + i < slots;
+        n[i] = in ? a.count[first + i] : 0u;
+        s[i] = in ? a.start[first + i] : 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+        p[i] = n[i] && n[i] <= (uint32_t)kPiece ? load_pack<T, V>(dout + (int64_t)a.order[s[i]] * a.stride + c) : zero_pack<T, V>();
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const uint32_t r = a.plan.row(first + i);
+        if (first + i >= slots || r >= a.plan.v || n[i] > (uint32_t)kPiece || (a.accumulate && n[i] == 0)) continue;
+        float acc[V];
+        unpack(p[i], acc);
+        if (n[i] > 1) sum_rows<T, V>(dout, a.stride, a.order, s[i] + 1, s[i] + n[i], c, acc);
+        store_row<T, O, V>(dtable, a.channels, r, c, a.scale, a.accumulate, acc);
+    }
+}
+
+// Window x: the row of pieces that begins in it, if there is one, from its windows' sums in order.
+template <typename T, typename O, typename I, int V>
+__global__ __launch_bounds__(256) void join_kernel(Sums a, const I* __restrict__ tokens, O* __restrict__ dtable)
+{
+    const uint32_t x = blockIdx.x / a.columns;
+    const uint32_t c = (blockIdx.x % a.columns * 256 + threadIdx.x) * V;
+    const uint32_t lo = x * kPiece, grouped = *a.grouped;
+    if (lo >= grouped || c >= a.channels) return;
+    // it reaches the end of the window, for it is longer than one
+    const uint32_t r = table_row(tokens, a.order[min(lo + (uint32_t)kPiece, grouped) - 1], a.plan.v);
+    const uint32_t s = a.start[a.plan.slot(r)], n = a.count[a.plan.slot(r)];
+    if (n <= (uint32_t)kPiece || s < lo) return;
+    const uint32_t last = (s + n - 1) / kPiece;
+    // it began before the later windows: slot 0 there
+    const auto piece = [&](uint32_t w) { return load_pack<float, V>(a.pieces + (size_t)w * 2 * a.channels + c); };
+    float acc[V];
+    unpack(load_pack<float, V>(a.pieces + ((size_t)x * 2 + (s > lo ? 1 : 0)) * a.channels + c), acc);
+    uint32_t w = x + 1;
+    for (; w + 8 <= last + 1; w += 8) {
+        Pack<float, V> p[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) p[u] = piece(w + u);
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+#pragma unroll
+            for (int k = 0; k < V; ++k) acc[k] += p[u].v[k];
+    }
+    for (; w <= last; ++w) {
+        const Pack<float, V> p = piece(w);
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[k] += p.v[k];
+    }
+    store_row<T, O, V>(dtable, a.channels, r, c, a.scale, a.accumulate, acc);
 }
 
 // ------------------------------------------------------------ lookup
@@ -431,12 +520,14 @@ template <typename T, typename O, int V, typename I>
 void run_sums(const I* tokens, const GroupPlan& p, const GroupSpace& w, const T* dout, int64_t stride,
               uint32_t channels, float scale, int accumulate, O* dtable, hipStream_t s)
 {
-    if (p.n > kPiece)  // otherwise no row is that long
-        hipLaunchKernelGGL((piece_kernel<T, I, V>), dim3((p.n + kPiece - 1) / kPiece, (channels + 256 * V - 1) / (256 * V)),
-                           dim3(256), 0, s, tokens, dout, stride, p.v, channels, w.order, w.start, w.count, w.grouped,
-                           w.pieces);
-    hipLaunchKernelGGL((rows_kernel<T, O, V>), dim3((p.v + 3) / 4, (channels + 64 * V - 1) / (64 * V)), dim3(256), 0, s,
-                       dout, stride, p.v, channels, w.order, w.start, w.count, w.pieces, scale, accumulate, dtable);
+    const uint32_t columns = (channels + 256 * V - 1) / (256 * V), chunks = (channels + 64 * V - 1) / (64 * V);
+    const uint32_t windows = p.n > kPiece ? (p.n + kPiece - 1) / kPiece : 0;  // else no row is that long
+    const Sums a{p, channels, columns, windows, stride, w.order, w.start, w.count, w.grouped, w.pieces, scale, accumulate};
+    const uint64_t units = ((uint64_t)p.buckets * p.per + kRows - 1) / kRows * chunks;
+    hipLaunchKernelGGL((sums_kernel<T, O, I, V>), dim3((unsigned)(windows * columns + (units + 3) / 4)), dim3(256), 0, s, a,
+                       tokens, dout, dtable);
+    if (windows)
+        hipLaunchKernelGGL((join_kernel<T, O, I, V>), dim3(windows * columns), dim3(256), 0, s, a, tokens, dtable);
 }
 
 template <typename T, typename O, typename I>
