@@ -18,6 +18,10 @@ namespace dwpt_seq {
 namespace {
 
 constexpr int kBlock = 256;
+// Channels per lane on the vector path (8 bytes of a 16-bit type).  With 8 the gradient needs 240
+// registers and two wavefronts per SIMD do not hide the loads: 8 x 2048 x 4096 bfloat16, forward and
+// gradient, 216 us against 155.  The single-token kernel, which keeps little, takes 16 bytes.
+constexpr int kPack = 4;
 constexpr uint32_t kMaxChannels = 1u << 20;
 
 // Channel vectors per row of a workgroup (a power of two up to 64); the other lanes take other row blocks.
@@ -138,7 +142,6 @@ __global__ __launch_bounds__(kBlock) void conv_kernel(Shape sh, Conv<T> a, const
         for (int k = 0; k < K - 1; ++k)
             unpack(input<T, K, V>(a.x, a.x_stride, a.initial, (uint32_t)s, st, (int64_t)pos - (K - 1) + k, c, sh.channels),
                    win[k + 1]);
-        const T* xp = a.x + (int64_t)pos * a.x_stride + c;
         T* yp = a.y + (int64_t)pos * a.y_stride + c;
         const auto step = [&](const Pack<T, V>& p) {
 #pragma unroll
@@ -151,17 +154,18 @@ __global__ __launch_bounds__(kBlock) void conv_kernel(Shape sh, Conv<T> a, const
 #pragma unroll
             for (int j = 0; j < V; ++j) u[j] = act<ACT>(u[j]);
             *reinterpret_cast<Pack<T, V>*>(yp) = pack<T, V>(u);
-            xp += a.x_stride;
             yp += a.y_stride;
         };
+        const T* xp = a.x + (int64_t)pos * a.x_stride + c;
         for (; pos + 4 <= e; pos += 4) {
             Pack<T, V> p[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) p[i] = load_pack<T, V>(xp + i * a.x_stride);
 #pragma unroll
             for (int i = 0; i < 4; ++i) step(p[i]);
+            xp += 4 * a.x_stride;
         }
-        for (; pos < e; ++pos) step(load_pack<T, V>(xp));
+        for (; pos < e; ++pos, xp += a.x_stride) step(load_pack<T, V>(xp));
     }
 }
 
@@ -291,18 +295,36 @@ __global__ __launch_bounds__(kBlock) void conv_grad_kernel(Shape sh, Conv<T> a, 
                     *reinterpret_cast<Pack<T, V>*>(g.dx + (int64_t)r * g.dx_stride + c) = pack<T, V>(d);
                 }
             };
-            const uint32_t stop = e + K - 1;
-            for (uint32_t t = pos; t < stop; t += 4) {
-                Pack<T, V> px[4], pdy[4];
+            // rows up to e + K - 2, four at a time, the next four on their way
+            const uint32_t stop = e + K - 1, in = min(stop, en);
+            struct Four {
+                Pack<T, V> x[4], dy[4];
+            };
+            const auto fetch = [&](Four& f, uint32_t at) {
+                const T *xs = a.x + (int64_t)at * a.x_stride + c, *ds = g.dy + (int64_t)at * g.dy_stride + c;
+                if (at + 4 <= in) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bool in = t + i < stop && t + i < en;
-                    px[i] = in ? load_pack<T, V>(a.x + (int64_t)(t + i) * a.x_stride + c) : zero_pack<T, V>();
-                    pdy[i] = in ? load_pack<T, V>(g.dy + (int64_t)(t + i) * g.dy_stride + c) : zero_pack<T, V>();
+                    for (int i = 0; i < 4; ++i) {
+                        f.x[i] = load_pack<T, V>(xs + i * a.x_stride);
+                        f.dy[i] = load_pack<T, V>(ds + i * g.dy_stride);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (at + i < in) {
+                            f.x[i] = load_pack<T, V>(xs + i * a.x_stride);
+                            f.dy[i] = load_pack<T, V>(ds + i * g.dy_stride);
+                        }
                 }
+            };
+            Four f, next;
+            fetch(f, pos);
+            for (uint32_t t = pos; t < stop; t += 4) {
+                if (t + 4 < in) fetch(next, t + 4);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (t + i < stop) step(t + i, px[i], pdy[i]);
+                    if (t + i < stop) step(t + i, f.x[i], f.dy[i]);
+                f = next;
             }
             pos = e;
         }
@@ -381,7 +403,10 @@ __global__ __launch_bounds__(kBlock) void conv_step_kernel(uint32_t rows, uint32
 }
 
 // ------------------------------------------------------------ host side
-// Rows per lane of the forward kernel: long blocks re-read fewer rows, short ones fill the chip.
+// Rows per lane.  Long blocks re-read fewer rows (K - 1 in front of each) and leave fewer sums to
+// join, short ones fill the chip: blocks are halved while there are fewer lanes than the numbers
+// below.  Forward 16 rows 29.9 us, 32 rows 30.7 (8191 x 4096); gradient 32 / 64 / 128 rows 158 / 157 /
+// 152 us (8 x 2048 x 4096, with the forward pass).
 uint32_t forward_rows(uint64_t rows, uint32_t nvec)
 {
     uint32_t r = 16;
@@ -390,8 +415,8 @@ uint32_t forward_rows(uint64_t rows, uint32_t nvec)
 }
 uint32_t grad_rows(uint64_t rows, uint32_t nvec)
 {
-    uint32_t r = 32;
-    while (r > 4 && rows / r * nvec < 256 * 4 * 64) r /= 2;
+    uint32_t r = 128;
+    while (r > 4 && rows / r * nvec < 65536) r /= 2;
     return r;
 }
 
@@ -466,7 +491,7 @@ scan_status_t forward(const causal_conv1d_args_t& a, hipStream_t s)
     return dispatch(a.dtype, a.weight_dtype, a.width, [&](auto te, auto we, auto ke) {
         using T = decltype(te);
         using W = decltype(we);
-        constexpr int K = decltype(ke)::value, V = 16 / sizeof(T);
+        constexpr int K = decltype(ke)::value, V = kPack;
         const Shape sh = make_shape(a, vec ? V : 1, false);
         const Conv<T> p{static_cast<const T*>(a.x), a.x_stride, static_cast<const T*>(a.initial_state), static_cast<T*>(a.y),
                         a.y_stride, static_cast<T*>(a.final_state)};
@@ -490,7 +515,7 @@ scan_status_t gradient(const causal_conv1d_grad_args_t& g, hipStream_t s)
     return dispatch(a.dtype, a.weight_dtype, a.width, [&](auto te, auto we, auto ke) {
         using T = decltype(te);
         using W = decltype(we);
-        constexpr int K = decltype(ke)::value, V = 16 / sizeof(T);
+        constexpr int K = decltype(ke)::value, V = kPack;
         const int v = vec ? V : 1;
         const Shape sh = make_shape(a, v, true);
         const Conv<T> p{static_cast<const T*>(a.x), a.x_stride, static_cast<const T*>(a.initial_state), nullptr, 0, nullptr};
@@ -548,7 +573,7 @@ size_t causal_conv1d_grad_workspace(const causal_conv1d_args_t* args)
     if (!args || check_common(*args) != SCAN_OK) return 0;
     // the element-wise path has the most row blocks
     size_t most = 0;
-    for (int v : {1, 16 / (int)dtype_size(args->dtype)}) {
+    for (int v : {1, kPack}) {
         const Shape sh = make_shape(*args, v, true);
         most = std::max(most, (size_t)sh.ny);
     }
