@@ -40,17 +40,17 @@ constexpr int kWgChannels = 64;       // channels per workgroup
 constexpr uint32_t kMaxChannels = 1u << 20;
 constexpr uint32_t kEmptyStep = 32;   // workgroups per channel block that look for empty sequences
 
-// S states per lane: TT rows per tile, SUB rows whose factors the gradient keeps in registers
-// (SUB * S factors and as many products: 2 * 32 registers).
+constexpr int kSaveRows = 16;         // rows between the states that the gradient starts from; rows of its tiles
+constexpr int kSub = 4;               // rows whose factors and states the gradient keeps in registers
+
+// S states per lane: TT rows per tile of the forward kernels.
 template <int S>
 struct Cfg {
     static constexpr int NP = 4 * S;  // states, padded
     static constexpr int TT = S == 16 ? 16 : 32;
-    static constexpr int SUB = 32 / S;
 };
 
 int states_per_lane(uint32_t states) { return states <= 16 ? 4 : states <= 32 ? 8 : 16; }
-uint32_t tile_rows(int s) { return s == 16 ? 16 : 32; }
 
 // Rows cut into spans.  Sequences of one length: `per_seq` spans of `span_rows` rows for each (the
 // last one shorter); packed sequences: every span_rows rows, wherever sequences begin.
@@ -190,6 +190,17 @@ __device__ __forceinline__ void lds_states(const float* p, float (&f)[S])
 #pragma unroll
         for (int j = 0; j < 4; ++j) f[s + j] = v[j];
     }
+}
+
+// The four lanes of a quad hold four values each; lane q receives the sum over the quad of value q.
+__device__ __forceinline__ float quad_transpose_sum(const float (&v)[4], int q)
+{
+    const bool odd = q & 1, high = q & 2;
+    float a = odd ? v[1] : v[0], b = odd ? v[3] : v[2];
+    a += dpp<kQuadXor1>(odd ? v[0] : v[1]);
+    b += dpp<kQuadXor1>(odd ? v[2] : v[3]);
+    const float keep = high ? b : a, give = high ? a : b;
+    return keep + dpp<kQuadXor2>(give);
 }
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
@@ -455,12 +466,16 @@ __global__ __launch_bounds__(kFwdWaves * 64) __attribute__((amdgpu_waves_per_eu(
                 if (in.z) X::load(pz, in.z, in.z_stride, at, len, me.c0, me.nch, me.lane);
             }
         };
-        const auto tile_len = [&](uint32_t at) { return (int)(min(r0 + ((at - r0) / TT + 1) * TT, e) - at); };
+        // whole tiles where a state is saved, up to there elsewhere
+        const auto tile_len = [&](uint32_t at) {
+            const uint32_t off = (at - r0) % kSaveRows;
+            return (int)(min(at + (off ? kSaveRows - off : (uint32_t)TT), e) - at);
+        };
         int len = tile_len(pos);
         fetch(pos, len);
         while (true) {
-            if (!TOTALS && saved && (pos - r0) % TT == 0)
-                h.store_padded(saved, pl, me, (size_t)span * pl.tiles_per_span + (pos - r0) / TT);
+            const bool save = !TOTALS && saved && (pos - r0) % kSaveRows == 0;
+            const size_t slot = (size_t)span * pl.tiles_per_span + (pos - r0) / kSaveRows;
             // (dt, dt x) of the tile; rows behind len keep the state: dt = 0
             typename X::P cx[X::PIECES], cz[X::PIECES];
             wave_sync();
@@ -548,6 +563,7 @@ __global__ __launch_bounds__(kFwdWaves * 64) __attribute__((amdgpu_waves_per_eu(
             read(w0, 0);
             products(w0, p0);
             for (int t = 0; t < len; t += 8) {
+                if (save && t % kSaveRows == 0) h.store_padded(saved, pl, me, slot + t / kSaveRows);
                 read(w1, t + 4);
                 __builtin_amdgcn_sched_barrier(0);
                 walk(w0, p0, t);
@@ -770,53 +786,58 @@ __global__ __launch_bounds__(kGradWaves * 64) void grad_totals_kernel(Plan pl, I
 }
 
 // Every gradient of a span's rows.  Tiles are taken from the last to the first.  A tile's states
-// are recomputed from its saved one: once forwards, keeping the state in front of every SUB rows,
-// then SUB rows at a time with their factors a and products a h' in registers, which the walk
-// back over those rows uses.
+// are recomputed from its saved one: once forwards, keeping the state in front of every kSub rows,
+// then kSub rows at a time with their factors a and states h in registers, which the walk back over
+// those rows uses:
+//   dh = dv C + g;  g' = a dh;  dA += dt g' h[t-1];  ddt = sum A g' h[t-1] + x sum dh B
 //
 // dB and dC are sums over channels, which lie across the lanes: the matrix unit adds them up.
 // v_mfma_f32_16x16x4_f32 multiplies a 16 x 4 matrix by a 4 x 16 one whose element (k, j) is in
 // lane 16 k + j; with a first matrix that is 1 in row t mod 16 and 0 elsewhere it adds, into row
-// t mod 16 of the accumulator, the four 16-lane rows of any register.  So 16 rows of the tile
-// collect in one accumulator per state, at one instruction per row and state and none on the
-// vector units; what is left is a sum over the 4 channels of a lane row, every 16 rows.  The
-// wavefronts of a workgroup add theirs in LDS, the workgroups theirs in a second launch, always in
-// the same order.
+// t mod 16 of the accumulator, the four 16-lane rows of any register.  So the 16 rows of the tile
+// collect in one accumulator per state, at one instruction per row and state (a lane's channels
+// are added up before) and none on the vector units; what is left is a sum over the 4 channels of a
+// lane row, once a tile.  The wavefronts of a workgroup add theirs in LDS, the workgroups theirs in
+// a second launch, always in the same order.
+template <int S>
+struct Bwd {
+    static constexpr int CW = S == 4 ? 32 : 16, WAVES = kWgChannels / CW;
+};
+
 template <typename T, int S, bool VEC>
-__global__ __launch_bounds__(kGradWaves * 64) __attribute__((amdgpu_waves_per_eu(S == 4 ? 2 : 1))) void grad_kernel(Plan pl, Inputs in, Grads gr, SpanTotals totals)
+__global__ __launch_bounds__(Bwd<S>::WAVES * 64) __attribute__((amdgpu_waves_per_eu(S == 16 ? 1 : 2))) void grad_kernel(
+    Plan pl, Inputs in, Grads gr, SpanTotals totals)
 {
-    using C = Cfg<S>;
-    constexpr int TT = C::TT, NP = C::NP, SUB = C::SUB, BLOCKS = TT / SUB;
-    using X = Tile<T, TT, 16, VEC>;
-    using BC = StateTile<T, TT, NP, kGradWaves * 64, VEC>;
+    constexpr int TT = kSaveRows, NP = 4 * S, CW = Bwd<S>::CW, CH = CW / 16, WAVES = Bwd<S>::WAVES, BLOCKS = TT / kSub;
+    using X = Tile<T, TT, CW, VEC>;
+    using BC = StateTile<T, TT, NP, WAVES * 64, VEC>;
     constexpr int V = X::V;
-    __shared__ __align__(16) f32x2 s_dt[kGradWaves][TT * 16];  // (dt, dt x), then the row's sums (dt part, x part)
-    __shared__ __align__(16) float s_dv[kGradWaves][TT * 16];  // dv, then sum_n C h
-    __shared__ __align__(16) float s_h[kGradWaves][BLOCKS * 64 * S];      // state in front of every SUB rows
+    __shared__ __align__(16) f32x2 s_dt[WAVES][TT * CW];  // (dt, dt x), then the row's sums (dt part, x part)
+    __shared__ __align__(16) float s_dv[WAVES][TT * CW];  // dv, then sum_n C h
+    __shared__ __align__(16) float s_h[WAVES][BLOCKS * 64 * S * CH];  // state in front of every kSub rows
     __shared__ __align__(16) float s_b[TT * NP], s_c[TT * NP];
-    // the wavefront's sums for dB and dC, 16 rows at a time, take the place of states that are used up
-    constexpr int SUMS = BLOCKS * 64 * S - TT * 2 * NP;
-    static_assert(SUMS >= 0 && SUMS % 4 == 0, "the sums fit behind the states still needed");
+    __shared__ __align__(16) float s_par[WAVES][2 * CW];  // delta_bias and D of the wavefront's channels
+    // the wavefront's sums for dB and dC take the place of the states, which are used up by then
+    static_assert(BLOCKS * 64 * S * CH >= TT * 2 * NP, "the sums fit");
 
     const uint32_t block = blockIdx.x % pl.blocks, span = blockIdx.x / pl.blocks;
-    const Place<16, true> me(pl, block);
+    const Place<CW, true> me(pl, block);
     uint32_t r0, r1;
     pl.rows_of(span, r0, r1);
     f32x2* const dt = s_dt[me.w];
     float* const ldv = s_dv[me.w];
     float* const lh = s_h[me.w];
-    float* const lsum = lh + SUMS;
-    LaneStates<S, 1, true> lane_A2, lane_g, lane_h, lane_dA;
-    lane_A2.load(in.A, pl, me, kLog2e);
-    lane_dA.zero();
-    auto &A2 = lane_A2.v[0], &g = lane_g.v[0], &h = lane_h.v[0], &dA = lane_dA.v[0];
-    float bias[V], skip[V], dskip[V] = {}, dbias[V] = {};
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const int c = X::col(me.lane) + j;
-        bias[j] = in.delta_bias && c < me.nch ? in.delta_bias[me.c0 + c] : 0.0f;
-        skip[j] = in.D && c < me.nch ? in.D[me.c0 + c] : 0.0f;
+    const float* const bias = s_par[me.w] + X::col(me.lane);
+    const float* const skip = bias + CW;
+    if (me.lane < 2 * CW) {  // 64 lanes or fewer
+        const int c = me.lane % CW;
+        const float* p = me.lane < CW ? in.delta_bias : in.D;
+        s_par[me.w][me.lane] = p && c < me.nch ? p[me.c0 + c] : 0.0f;
     }
+    LaneStates<S, CH, true> A2, g, h, dA;
+    A2.load(in.A, pl, me, kLog2e);
+    dA.zero();
+    float dskip[V] = {}, dbias[V] = {};
     const uint32_t bc_at = me.group * pl.states;
     float* const bc_out = gr.bc + (size_t)block * pl.seqs.rows * (2 * NP);
 
@@ -832,11 +853,10 @@ __global__ __launch_bounds__(kGradWaves * 64) __attribute__((amdgpu_waves_per_eu
         s = uniform(s);
         const uint32_t st = pl.seqs.start((uint32_t)s), en = max(pl.seqs.end((uint32_t)s), hi);
         const uint32_t first = (uint32_t)uniform((int)max(st, r0));
-        if (hi == en) {
-            lane_g.start(gr.dfinal, pl, me, (uint32_t)s);
-        } else {
-            join_spans<S, 1, true>(totals, pl, me, pl.span_of(span, en - 1), span + 1, -1, lane_A2, lane_g);
-        }
+        if (hi == en)
+            g.start(gr.dfinal, pl, me, (uint32_t)s);
+        else
+            join_spans<S, CH, true>(totals, pl, me, pl.span_of(span, en - 1), span + 1, -1, A2, g);
         typename X::P px[X::PIECES], pd[X::PIECES], pz[X::PIECES], py[X::PIECES];
         typename BC::P pb[BC::PIECES], pc[BC::PIECES];
         const auto fetch = [&](uint32_t at, int len) {
@@ -848,32 +868,36 @@ __global__ __launch_bounds__(kGradWaves * 64) __attribute__((amdgpu_waves_per_eu
             BC::load(pc, in.C, in.c_stride, at, len, bc_at, pl.states, threadIdx.x);
         };
         uint32_t lo = max(r0 + (hi - 1 - r0) / TT * TT, first);
-        constexpr bool AHEAD = S < 16;  // the next tile's pieces in registers (64 states leave none for them)
-        if (AHEAD) fetch(lo, (int)(hi - lo));
+        fetch(lo, (int)(hi - lo));
         while (true) {
             const int len = (int)(hi - lo);
-            if (!AHEAD) fetch(lo, len);
             // the state in front of the tile
             if (lo == st)
-                lane_h.start(in.initial, pl, me, (uint32_t)s);
+                h.start(in.initial, pl, me, (uint32_t)s);
             else
-                lane_h.load_padded(gr.saved, pl, me, (size_t)span * pl.tiles_per_span + (lo - r0) / TT);
-            float xf[X::PIECES][V], df[X::PIECES][V], zf[X::PIECES][V], yf[X::PIECES][V];
+                h.load_padded(gr.saved, pl, me, (size_t)span * pl.tiles_per_span + (lo - r0) / TT);
+            typename X::P cx[X::PIECES], cd[X::PIECES], cz[X::PIECES], cy[X::PIECES];
+            wave_sync();
 #pragma unroll
             for (int i = 0; i < X::PIECES; ++i) {
-                unpack(px[i], xf[i]);
-                unpack(pd[i], df[i]);
-                unpack(py[i], yf[i]);
-                if (in.z) unpack(pz[i], zf[i]);
+                cx[i] = px[i];
+                cd[i] = pd[i];
+                cy[i] = py[i];
+                cz[i] = pz[i];
+                float xf[V], df[V], yf[V], zf[V], bf[V];
+                unpack(cx[i], xf);
+                unpack(cd[i], df);
+                unpack(cy[i], yf);
+                unpack(cz[i], zf);
                 const int r = X::row(i, me.lane);
                 if (TT % X::RPL && r >= TT) continue;
+                lds_states<V>(bias, bf);
+                step_sizes<V>(df, bf, in.softplus, r < len, df);
+                const int at = r * CW + X::col(me.lane);
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    df[i][j] += bias[j];
-                    const float v = r < len ? step_size(df[i][j], in.softplus) : 0.0f;
-                    const int at = r * 16 + X::col(me.lane) + j;
-                    dt[at] = f32x2{v, v * xf[i][j]};
-                    ldv[at] = in.z ? yf[i][j] * silu(zf[i][j]) : yf[i][j];
+                    dt[at + j] = f32x2{df[j], df[j] * xf[j]};
+                    ldv[at + j] = in.z ? yf[j] * silu(zf[j]) : yf[j];
                 }
             }
             BC::put(s_b, pb, threadIdx.x);
@@ -881,112 +905,131 @@ __global__ __launch_bounds__(kGradWaves * 64) __attribute__((amdgpu_waves_per_eu
             __syncthreads();
             const bool more = lo > first;
             const uint32_t next = more ? max(r0 + (lo - 1 - r0) / TT * TT, first) : lo;
-            if (AHEAD && more) fetch(next, (int)(lo - next));
+            if (more) fetch(next, (int)(lo - next));
 
-            // forwards: the states in front of every SUB rows
-            const int blocks = (len + SUB - 1) / SUB;
+            // forwards: the states in front of every kSub rows
+            const int blocks = (len + kSub - 1) / kSub;
             for (int k = 0;; ++k) {
 #pragma unroll
-                for (int i = 0; i < S; i += 4)
-                    *reinterpret_cast<f32x4*>(lh + (k * 64 + me.lane) * S + i) = f32x4{h[i], h[i + 1], h[i + 2], h[i + 3]};
+                for (int c = 0; c < CH; ++c)
+#pragma unroll
+                    for (int i = 0; i < S; i += 4)
+                        *reinterpret_cast<f32x4*>(lh + ((k * CH + c) * 64 + me.lane) * S + i) =
+                            f32x4{h.v[c][i], h.v[c][i + 1], h.v[c][i + 2], h.v[c][i + 3]};
                 if (k + 1 >= blocks) break;
 #pragma unroll
-                for (int u = 0; u < SUB; ++u) {
-                    const int t = k * SUB + u;
-                    const f32x2 v = dt[t * 16 + me.d];
+                for (int u = 0; u < kSub; ++u) {
+                    const int t = k * kSub + u;
                     float b[S];
                     lds_states<S>(s_b + t * NP + me.q * S, b);
 #pragma unroll
-                    for (int i = 0; i < S; ++i) h[i] = fmaf(exp2_fast(v[0] * A2[i]), h[i], v[1] * b[i]);
+                    for (int c = 0; c < CH; ++c) {
+                        const f32x2 v = dt[t * CW + me.d + 16 * c];
+#pragma unroll
+                        for (int i = 0; i < S; ++i) h.v[c][i] = fmaf(exp2_fast(v[0] * A2.v[c][i]), h.v[c][i], v[1] * b[i]);
+                    }
                 }
             }
-            // backwards, SUB rows at a time
+            // backwards, kSub rows at a time
             f32x4 accB[S], accC[S];
 #pragma unroll
             for (int i = 0; i < S; ++i) accB[i] = accC[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
             for (int k = blocks - 1; k >= 0; --k) {
-                lds_states<S>(lh + (k * 64 + me.lane) * S, h);
-                float a[SUB][S], p[SUB][S];  // the factor and a h'
+                float a[kSub][CH][S], hs[kSub + 1][CH][S];  // the factors; the states before each row and behind the last
 #pragma unroll
-                for (int u = 0; u < SUB; ++u) {
-                    const int t = k * SUB + u;
-                    const f32x2 v = dt[t * 16 + me.d];
+                for (int c = 0; c < CH; ++c) lds_states<S>(lh + ((k * CH + c) * 64 + me.lane) * S, hs[0][c]);
+#pragma unroll
+                for (int u = 0; u < kSub; ++u) {
+                    const int t = k * kSub + u;
                     float b[S];
                     lds_states<S>(s_b + t * NP + me.q * S, b);
 #pragma unroll
-                    for (int i = 0; i < S; ++i) {
-                        a[u][i] = exp2_fast(v[0] * A2[i]);
-                        p[u][i] = a[u][i] * h[i];
-                        h[i] = fmaf(v[1], b[i], p[u][i]);
-                    }
-                }
+                    for (int c = 0; c < CH; ++c) {
+                        const f32x2 v = dt[t * CW + me.d + 16 * c];
 #pragma unroll
-                for (int u = SUB - 1; u >= 0; --u) {
-                    const int t = k * SUB + u;
-                    const f32x2 v = dt[t * 16 + me.d];
-                    const float dv = ldv[t * 16 + me.d];
-                    float b[S], c[S];
-                    lds_states<S>(s_b + t * NP + me.q * S, b);
-                    lds_states<S>(s_c + t * NP + me.q * S, c);
-                    const float select = (me.lane & 15) == (t & 15) ? 1.0f : 0.0f;
-                    float ch = 0.0f, sd = 0.0f, sx = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < S; ++i) {
-                        const float ht = fmaf(v[1], b[i], p[u][i]);
-                        ch = fmaf(c[i], ht, ch);
-                        accC[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(select, dv * ht, accC[i], 0, 0, 0);
-                        const float dh = fmaf(dv, c[i], g[i]);
-                        accB[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(select, dh * v[1], accB[i], 0, 0, 0);
-                        sx = fmaf(dh, b[i], sx);
-                        const float through = dh * p[u][i];
-                        dA[i] = fmaf(v[0], through, dA[i]);
-                        sd = fmaf(A2[i], through, sd);
-                        g[i] = a[u][i] * dh;
-                    }
-                    ch = quad_sum(ch);
-                    sd = quad_sum(sd);
-                    sx = quad_sum(sx);
-                    if (me.q == (t & 3)) {  // every lane of the quad has read the row's values
-                        dt[t * 16 + me.d] = f32x2{sd * kLn2, sx};
-                        ldv[t * 16 + me.d] = ch;
-                    }
-                }
-                if ((k * SUB) % 16 == 0) {
-                    // the accumulators hold 16 rows: lane 16 k + j has rows 4 k .. 4 k + 3, column j =
-                    // 4 (channel mod 4) + quarter; each of the four lanes of a quarter keeps one row
-                    const int row = k * SUB + 4 * (me.lane >> 4) + ((me.lane >> 2) & 3);
-                    const int pick = (me.lane >> 2) & 3;
-                    float fb[S], fc[S];
-#pragma unroll
-                    for (int i = 0; i < S; ++i) {
-                        float vb[4], vc[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            vb[j] = accB[i][j];
-                            vc[j] = accC[i][j];
-                            vb[j] += dpp<kRowRor4>(vb[j]);
-                            vc[j] += dpp<kRowRor4>(vc[j]);
-                            vb[j] += dpp<kRowRor8>(vb[j]);
-                            vc[j] += dpp<kRowRor8>(vc[j]);
+                        for (int i = 0; i < S; ++i) {
+                            a[u][c][i] = exp2_fast(v[0] * A2.v[c][i]);
+                            hs[u + 1][c][i] = fmaf(a[u][c][i], hs[u][c][i], v[1] * b[i]);
                         }
-                        fb[i] = pick == 0 ? vb[0] : pick == 1 ? vb[1] : pick == 2 ? vb[2] : vb[3];
-                        fc[i] = pick == 0 ? vc[0] : pick == 1 ? vc[1] : pick == 2 ? vc[2] : vc[3];
-                        accB[i] = accC[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
                     }
+                }
+                float ch[CH][kSub], sd[CH][kSub], sx[CH][kSub];  // the lane's sums of C h, A g h, dh B
 #pragma unroll
-                    for (int i = 0; i < S; i += 4) {
-                        *reinterpret_cast<f32x4*>(lsum + row * 2 * NP + me.q * S + i) = f32x4{fb[i], fb[i + 1], fb[i + 2], fb[i + 3]};
-                        *reinterpret_cast<f32x4*>(lsum + row * 2 * NP + NP + me.q * S + i) =
-                            f32x4{fc[i], fc[i + 1], fc[i + 2], fc[i + 3]};
+                for (int u = kSub - 1; u >= 0; --u) {
+                    const int t = k * kSub + u;
+                    float b[S], cc[S], pb_[S], pc_[S];
+                    lds_states<S>(s_b + t * NP + me.q * S, b);
+                    lds_states<S>(s_c + t * NP + me.q * S, cc);
+#pragma unroll
+                    for (int c = 0; c < CH; ++c) {
+                        const f32x2 v = dt[t * CW + me.d + 16 * c];
+                        const float dv = ldv[t * CW + me.d + 16 * c];
+                        ch[c][u] = sd[c][u] = sx[c][u] = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < S; ++i) {
+                            const float ht = hs[u + 1][c][i];
+                            const float dh = fmaf(dv, cc[i], g.v[c][i]);
+                            pc_[i] = c ? fmaf(dv, ht, pc_[i]) : dv * ht;
+                            pb_[i] = c ? fmaf(dh, v[1], pb_[i]) : dh * v[1];
+                            g.v[c][i] = a[u][c][i] * dh;
+                            const float through = g.v[c][i] * hs[u][c][i];
+                            dA.v[c][i] = fmaf(v[0], through, dA.v[c][i]);
+                            ch[c][u] = i ? fmaf(cc[i], ht, ch[c][u]) : cc[i] * ht;
+                            sx[c][u] = i ? fmaf(dh, b[i], sx[c][u]) : dh * b[i];
+                            sd[c][u] = i ? fmaf(A2.v[c][i], through, sd[c][u]) : A2.v[c][i] * through;
+                        }
                     }
+                    const float select = (me.lane & 15) == (t & 15) ? 1.0f : 0.0f;
+#pragma unroll
+                    for (int i = 0; i < S; ++i) {
+                        accC[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(select, pc_[i], accC[i], 0, 0, 0);
+                        accB[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(select, pb_[i], accB[i], 0, 0, 0);
+                    }
+                }
+                // every lane of the quad has read the rows' values: lane q writes row q's sums over them
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    const int at = (k * kSub + me.q) * CW + me.d + 16 * c;
+                    const float d = quad_transpose_sum(sd[c], me.q), x = quad_transpose_sum(sx[c], me.q);
+                    const float y = quad_transpose_sum(ch[c], me.q);
+                    dt[at] = f32x2{d * kLn2, x};
+                    ldv[at] = y;
+                }
+            }
+            {
+                // lane 16 k + j of the accumulators has rows 4 k .. 4 k + 3, column j = 4 (channel mod 4) +
+                // quarter; each of the four lanes of a quarter keeps one row
+                const int pick = (me.lane >> 2) & 3, row = 4 * (me.lane >> 4) + pick;
+                float fb[S], fc[S];
+#pragma unroll
+                for (int i = 0; i < S; ++i) {
+                    float vb[4], vc[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        vb[j] = accB[i][j];
+                        vc[j] = accC[i][j];
+                        vb[j] += dpp<kRowRor4>(vb[j]);
+                        vc[j] += dpp<kRowRor4>(vc[j]);
+                        vb[j] += dpp<kRowRor8>(vb[j]);
+                        vc[j] += dpp<kRowRor8>(vc[j]);
+                    }
+                    fb[i] = pick == 0 ? vb[0] : pick == 1 ? vb[1] : pick == 2 ? vb[2] : vb[3];
+                    fc[i] = pick == 0 ? vc[0] : pick == 1 ? vc[1] : pick == 2 ? vc[2] : vc[3];
+                }
+                wave_sync();
+#pragma unroll
+                for (int i = 0; i < S; i += 4) {
+                    *reinterpret_cast<f32x4*>(lh + row * 2 * NP + me.q * S + i) = f32x4{fb[i], fb[i + 1], fb[i + 2], fb[i + 3]};
+                    *reinterpret_cast<f32x4*>(lh + row * 2 * NP + NP + me.q * S + i) =
+                        f32x4{fc[i], fc[i + 1], fc[i + 2], fc[i + 3]};
                 }
             }
             __syncthreads();
             // the workgroup's sums for dB and dC
-            for (int i = threadIdx.x; i < len * 2 * NP / 4; i += kGradWaves * 64) {
-                f32x4 v = *reinterpret_cast<const f32x4*>(&s_h[0][SUMS + i * 4]);
+            for (int i = threadIdx.x; i < len * 2 * NP / 4; i += WAVES * 64) {
+                f32x4 v = *reinterpret_cast<const f32x4*>(&s_h[0][i * 4]);
 #pragma unroll
-                for (int w = 1; w < kGradWaves; ++w) v += *reinterpret_cast<const f32x4*>(&s_h[w][SUMS + i * 4]);
+                for (int w = 1; w < WAVES; ++w) v += *reinterpret_cast<const f32x4*>(&s_h[w][i * 4]);
                 *reinterpret_cast<f32x4*>(bc_out + (size_t)lo * (2 * NP) + (size_t)i * 4) = v;
             }
             // the rows' own gradients
@@ -994,24 +1037,41 @@ __global__ __launch_bounds__(kGradWaves * 64) __attribute__((amdgpu_waves_per_eu
             for (int i = 0; i < X::PIECES; ++i) {
                 const int r = X::row(i, me.lane);
                 if (r >= len) continue;
-                float ox[V], od[V], oz[V];
+                float ox[V], od[V], oz[V], xf[V], df[V], yf[V], zf[V], bf[V], sf[V], vf[V];
+                opaque(cx[i]);
+                opaque(cd[i]);
+                opaque(cy[i]);
+                opaque(cz[i]);
+                unpack(cx[i], xf);
+                unpack(cd[i], df);
+                unpack(cy[i], yf);
+                unpack(cz[i], zf);
+                const int at = r * CW + X::col(me.lane);
+                lds_states<V>(bias, bf);
+                lds_states<V>(skip, sf);
+                step_sizes<V>(df, bf, in.softplus, true, vf);
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    const int at = r * 16 + X::col(me.lane) + j;
-                    const f32x2 q = dt[at];
-                    const float raw = df[i][j], v = step_size(raw, in.softplus), x = xf[i][j], dy = yf[i][j];
-                    float dv = dy;
+                    const f32x2 q = dt[at + j];
+                    float dv = yf[j];
                     if (in.z) {
-                        const float z = zf[i][j], sg = sigmoid(z), full = fmaf(skip[j], x, ldv[at]);
-                        dv = dy * z * sg;
-                        oz[j] = dy * full * sg * (1.0f + z * (1.0f - sg));
+                        const float z = zf[j], sg = sigmoid(z), full = fmaf(sf[j], xf[j], ldv[at + j]);
+                        dv = yf[j] * z * sg;
+                        oz[j] = yf[j] * full * sg * (1.0f + z * (1.0f - sg));
                     }
-                    ox[j] = fmaf(dv, skip[j], v * q[1]);
-                    od[j] = fmaf(x, q[1], q[0]);
-                    if (in.softplus && !(raw > 20.0f)) od[j] *= sigmoid(raw);
-                    dskip[j] = fmaf(dv, x, dskip[j]);
-                    dbias[j] += od[j];
+                    ox[j] = fmaf(dv, sf[j], vf[j] * q[1]);
+                    od[j] = fmaf(xf[j], q[1], q[0]);
+                    dskip[j] = fmaf(dv, xf[j], dskip[j]);
                 }
+                if (in.softplus) {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        const float raw = df[j] + bf[j];
+                        od[j] *= raw > 20.0f ? 1.0f : sigmoid(raw);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < V; ++j) dbias[j] += od[j];
                 X::store(gr.dx, gr.dx_stride, lo, len, me.c0, me.nch, me.lane, i, ox);
                 X::store(gr.ddelta, gr.ddelta_stride, lo, len, me.c0, me.nch, me.lane, i, od);
                 if (in.z) X::store(gr.dz, gr.dz_stride, lo, len, me.c0, me.nch, me.lane, i, oz);
@@ -1021,10 +1081,9 @@ __global__ __launch_bounds__(kGradWaves * 64) __attribute__((amdgpu_waves_per_eu
             if (!more) break;
             lo = next;
         }
-        if (first == st && gr.dinitial)
-            lane_g.store(gr.dinitial + (size_t)s * pl.channels * pl.states, pl, me);
+        if (first == st && gr.dinitial) g.store(gr.dinitial + (size_t)s * pl.channels * pl.states, pl, me);
     }
-    lane_dA.store_padded(gr.dA, pl, me, span);
+    dA.store_padded(gr.dA, pl, me, span);
     // lanes that loaded the same channels
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -1122,7 +1181,7 @@ Plan make_plan(uint32_t channels, uint32_t states, uint32_t groups, uint64_t row
     p.group_channels = channels / groups;
     p.blocks_per_group = (p.group_channels + kWgChannels - 1) / kWgChannels;
     p.blocks = groups * p.blocks_per_group;
-    const uint32_t tt = tile_rows(states_per_lane(states));
+    constexpr uint32_t tt = 32;  // spans are whole tiles
     // rows of one sequence, or of all packed ones; and how many spans they may be cut into
     const uint64_t run = offsets ? rows : p.seqs.len, runs = offsets ? 1 : seqs;
     uint64_t cuts = 1;
@@ -1133,7 +1192,7 @@ Plan make_plan(uint32_t channels, uint32_t states, uint32_t groups, uint64_t row
     p.span_rows = (uint32_t)std::max<uint64_t>(tt, round_up((run + cuts - 1) / cuts, tt));
     p.per_seq = (uint32_t)((run + p.span_rows - 1) / p.span_rows);
     p.spans = offsets ? p.per_seq : (uint32_t)(p.per_seq * seqs);
-    p.tiles_per_span = p.span_rows / tt;
+    p.tiles_per_span = p.span_rows / kSaveRows;
     return p;
 }
 Plan make_plan(const selective_scan_args_t& a)
@@ -1301,7 +1360,7 @@ scan_status_t gradient(const selective_scan_grad_args_t& g, hipStream_t stream)
         if (p.per_seq > 1)
             hipLaunchKernelGGL((in.vec ? grad_totals_kernel<T, S, true> : grad_totals_kernel<T, S, false>), dim3((unsigned)wgs), block, 0, stream, p, in, gr, w.totals);
         if (wgs) {
-            hipLaunchKernelGGL((in.vec ? grad_kernel<T, S, true> : grad_kernel<T, S, false>), dim3((unsigned)wgs), block, 0, stream, p, in, gr, w.totals);
+            hipLaunchKernelGGL((in.vec ? grad_kernel<T, S, true> : grad_kernel<T, S, false>), dim3((unsigned)wgs), dim3(Bwd<S>::WAVES * 64), 0, stream, p, in, gr, w.totals);
             hipLaunchKernelGGL((join_bc_kernel<T>), dim3((unsigned)bc), dim3(256), 0, stream, p, (const float*)w.bc, np,
                                static_cast<T*>(g.dB), g.db_stride, static_cast<T*>(g.dC), g.dc_stride);
         }
