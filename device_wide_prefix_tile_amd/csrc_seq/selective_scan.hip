@@ -586,9 +586,10 @@ __global__ __launch_bounds__(kFwdWaves * 64) __attribute__((amdgpu_waves_per_eu(
                     lds_states<V>(skip, df);
                     lds_states<V>(ly + r * CW + X::col(me.lane), f);
 #pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        f[j] = fmaf(df[j], xf[j], f[j]);
-                        if (in.z) f[j] *= silu(zf[j]);
+                    for (int j = 0; j < V; ++j) f[j] = fmaf(df[j], xf[j], f[j]);
+                    if (in.z) {
+#pragma unroll
+                        for (int j = 0; j < V; ++j) f[j] *= silu(zf[j]);
                     }
                     X::store(y, y_stride, pos, len, me.c0, me.nch, me.lane, i, f);
                 }
@@ -757,9 +758,12 @@ __global__ __launch_bounds__(kGradWaves * 64) void grad_totals_kernel(Plan pl, I
             const int r = X::row(i, me.lane);
             if (TT % X::RPL && r >= TT) continue;
             step_sizes<V>(df, bias, in.softplus, r < len, df);
+            if (in.z) {
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                dt[r * 16 + X::col(me.lane) + j] = f32x2{df[j], in.z ? yf[j] * silu(zf[j]) : yf[j]};
+                for (int j = 0; j < V; ++j) yf[j] *= silu(zf[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < V; ++j) dt[r * 16 + X::col(me.lane) + j] = f32x2{df[j], yf[j]};
         }
         BC::put(lc, pc, me.lane);
         wave_sync();
@@ -866,16 +870,16 @@ __global__ __launch_bounds__(Bwd<S>::WAVES * 64) __attribute__((amdgpu_waves_per
             if (in.z) X::load(pz, in.z, in.z_stride, at, len, me.c0, me.nch, me.lane);
             BC::load(pb, in.B, in.b_stride, at, len, bc_at, pl.states, threadIdx.x);
             BC::load(pc, in.C, in.c_stride, at, len, bc_at, pl.states, threadIdx.x);
+            // the state in front of the tile
+            if (at == st)
+                h.start(in.initial, pl, me, (uint32_t)s);
+            else
+                h.load_padded(gr.saved, pl, me, (size_t)span * pl.tiles_per_span + (at - r0) / TT);
         };
         uint32_t lo = max(r0 + (hi - 1 - r0) / TT * TT, first);
         fetch(lo, (int)(hi - lo));
         while (true) {
             const int len = (int)(hi - lo);
-            // the state in front of the tile
-            if (lo == st)
-                h.start(in.initial, pl, me, (uint32_t)s);
-            else
-                h.load_padded(gr.saved, pl, me, (size_t)span * pl.tiles_per_span + (lo - r0) / TT);
             typename X::P cx[X::PIECES], cd[X::PIECES], cz[X::PIECES], cy[X::PIECES];
             wave_sync();
 #pragma unroll
@@ -893,20 +897,20 @@ __global__ __launch_bounds__(Bwd<S>::WAVES * 64) __attribute__((amdgpu_waves_per
                 if (TT % X::RPL && r >= TT) continue;
                 lds_states<V>(bias, bf);
                 step_sizes<V>(df, bf, in.softplus, r < len, df);
+                if (in.z) {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) yf[j] *= silu(zf[j]);
+                }
                 const int at = r * CW + X::col(me.lane);
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    dt[at + j] = f32x2{df[j], df[j] * xf[j]};
-                    ldv[at + j] = in.z ? yf[j] * silu(zf[j]) : yf[j];
-                }
+                for (int j = 0; j < V; ++j) dt[at + j] = f32x2{df[j], df[j] * xf[j]};
+#pragma unroll
+                for (int j = 0; j < V; j += 4)
+                    *reinterpret_cast<f32x4*>(ldv + at + j) = f32x4{yf[j], yf[j + 1], yf[j + 2], yf[j + 3]};
             }
             BC::put(s_b, pb, threadIdx.x);
             BC::put(s_c, pc, threadIdx.x);
             __syncthreads();
-            const bool more = lo > first;
-            const uint32_t next = more ? max(r0 + (lo - 1 - r0) / TT * TT, first) : lo;
-            if (more) fetch(next, (int)(lo - next));
-
             // forwards: the states in front of every kSub rows
             const int blocks = (len + kSub - 1) / kSub;
             for (int k = 0;; ++k) {
@@ -996,6 +1000,10 @@ __global__ __launch_bounds__(Bwd<S>::WAVES * 64) __attribute__((amdgpu_waves_per
                     ldv[at] = y;
                 }
             }
+            // the next tile's inputs, now that the registers of the walk are free
+            const bool more = lo > first;
+            const uint32_t next = more ? max(r0 + (lo - 1 - r0) / TT * TT, first) : lo;
+            if (more) fetch(next, (int)(lo - next));
             {
                 // lane 16 k + j of the accumulators has rows 4 k .. 4 k + 3, column j = 4 (channel mod 4) +
                 // quarter; each of the four lanes of a quarter keeps one row
@@ -1050,18 +1058,22 @@ __global__ __launch_bounds__(Bwd<S>::WAVES * 64) __attribute__((amdgpu_waves_per
                 lds_states<V>(bias, bf);
                 lds_states<V>(skip, sf);
                 step_sizes<V>(df, bf, in.softplus, true, vf);
+                if (in.z) {
+                    float full[V];
+                    lds_states<V>(ldv + at, full);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        const float z = zf[j], sg = sigmoid(z);
+                        oz[j] = yf[j] * fmaf(sf[j], xf[j], full[j]) * sg * (1.0f + z * (1.0f - sg));
+                        yf[j] *= z * sg;  // dv
+                    }
+                }
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     const f32x2 q = dt[at + j];
-                    float dv = yf[j];
-                    if (in.z) {
-                        const float z = zf[j], sg = sigmoid(z), full = fmaf(sf[j], xf[j], ldv[at + j]);
-                        dv = yf[j] * z * sg;
-                        oz[j] = yf[j] * full * sg * (1.0f + z * (1.0f - sg));
-                    }
-                    ox[j] = fmaf(dv, sf[j], vf[j] * q[1]);
+                    ox[j] = fmaf(yf[j], sf[j], vf[j] * q[1]);
                     od[j] = fmaf(xf[j], q[1], q[0]);
-                    dskip[j] = fmaf(dv, xf[j], dskip[j]);
+                    dskip[j] = fmaf(yf[j], xf[j], dskip[j]);
                 }
                 if (in.softplus) {
 #pragma unroll
