@@ -611,75 +611,89 @@ __global__ __launch_bounds__(kFwdWaves * 64) __attribute__((amdgpu_waves_per_eu(
 }
 
 // ------------------------------------------------------------ single tokens
-// A wavefront takes 16 channels of one row.
+// HBM-bound: the states are read and written once.  A wavefront takes 16 channels of R rows, whose
+// loads are in flight together: four rows where there are enough of them to fill the chip (256 rows
+// x 4096 channels: 41 us with one row per wavefront), else one.
 constexpr int kGradWaves = kWgChannels / 16;
 
-template <typename T, int S>
+template <typename T, int S, bool VEC, int R>
 __global__ __launch_bounds__(kGradWaves * 64) void scan_step_kernel(Plan pl, Inputs in, const int32_t* __restrict__ slots,
-                                                                uint32_t n_slots, float* __restrict__ state,
-                                                                T* __restrict__ y, int64_t y_stride)
+                                                                    uint32_t n_slots, float* __restrict__ state,
+                                                                    T* __restrict__ y, int64_t y_stride)
 {
-    const uint32_t block = blockIdx.x % pl.blocks, r = blockIdx.x / pl.blocks;
+    const uint32_t block = blockIdx.x % pl.blocks, r0 = blockIdx.x / pl.blocks * R;
     const Place<16, true> me(pl, block);
     if (me.d >= me.nch) return;
-    const int32_t slot = slots ? slots[r] : (int32_t)r;
-    if (slot < 0 || (uint32_t)slot >= n_slots) return;
-    const uint32_t c = me.c0 + me.d;
-    float* sp = state + ((size_t)slot * pl.channels + c) * pl.states + me.q * S;
-    const float* ap = in.A + (size_t)c * pl.states + me.q * S;
-    const T* bp = static_cast<const T*>(in.B) + (int64_t)r * in.b_stride + me.group * pl.states + me.q * S;
-    const T* cp = static_cast<const T*>(in.C) + (int64_t)r * in.c_stride + me.group * pl.states + me.q * S;
-    float h[S], a[S], b[S], cc[S];
-    const bool whole = in.vec;  // states = 4 S, state and A 16-byte aligned
+    const uint32_t c = me.c0 + me.d, first = me.q * S;
+    const size_t bc_at = me.group * pl.states + first;
+    const float* ap = in.A + (size_t)c * pl.states + first;
+    float h[R][S], a[S], x[R], raw[R], z[R];
+    Pack<T, S> b[R], cc[R];
+    float* sp[R];
 #pragma unroll
-    for (int i = 0; i < S; i += 4) {
-        if (whole) {
-            const f32x4 hv = *reinterpret_cast<const f32x4*>(sp + i), av = *reinterpret_cast<const f32x4*>(ap + i);
+    for (int u = 0; u < R; ++u) {
+        const uint32_t r = r0 + u;
+        const int32_t slot = r < pl.seqs.rows ? (slots ? slots[r] : (int32_t)r) : -1;
+        sp[u] = slot >= 0 && (uint32_t)slot < n_slots ? state + ((size_t)slot * pl.channels + c) * pl.states + first : nullptr;
+        if (!sp[u]) continue;
+        const T* bp = static_cast<const T*>(in.B) + (int64_t)r * in.b_stride + bc_at;
+        const T* cp = static_cast<const T*>(in.C) + (int64_t)r * in.c_stride + bc_at;
+        if (VEC) {
+            lds_states<S>(sp[u], h[u]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                h[i + j] = hv[j];
-                a[i + j] = av[j];
+            for (int i = 0; i < S; i += 4) {
+                const Pack<T, 4> p = load_pack<T, 4>(bp + i), q = load_pack<T, 4>(cp + i);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    b[u].v[i + j] = p.v[j];
+                    cc[u].v[i + j] = q.v[j];
+                }
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const bool ok = me.q * S + i + j < pl.states;
-                h[i + j] = ok ? sp[i + j] : 0.0f;
-                a[i + j] = ok ? ap[i + j] : 0.0f;
+            for (int i = 0; i < S; ++i) {
+                const bool ok = first + i < pl.states;
+                h[u][i] = ok ? sp[u][i] : 0.0f;
+                b[u].v[i] = ok ? bp[i] : (T)0.0f;
+                cc[u].v[i] = ok ? cp[i] : (T)0.0f;
             }
         }
+        x[u] = (float)static_cast<const T*>(in.x)[(int64_t)r * in.x_stride + c];
+        raw[u] = (float)static_cast<const T*>(in.delta)[(int64_t)r * in.delta_stride + c];
+        z[u] = in.z ? (float)static_cast<const T*>(in.z)[(int64_t)r * in.z_stride + c] : 0.0f;
+    }
+    if (VEC) {
+        lds_states<S>(ap, a);
+    } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const bool ok = me.q * S + i + j < pl.states;
-            b[i + j] = ok ? (float)bp[i + j] : 0.0f;
-            cc[i + j] = ok ? (float)cp[i + j] : 0.0f;
+        for (int i = 0; i < S; ++i) a[i] = first + i < pl.states ? ap[i] : 0.0f;
+    }
+    const float bias = in.delta_bias ? in.delta_bias[c] : 0.0f, skip = in.D ? in.D[c] : 0.0f;
+#pragma unroll
+    for (int u = 0; u < R; ++u) {
+        if (!sp[u]) continue;
+        const float dt = step_size(raw[u] + bias, in.softplus), dx = dt * x[u];
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+            h[u][i] = fmaf(exp2_fast(dt * (a[i] * kLog2e)), h[u][i], dx * (float)b[u].v[i]);
+            sum = fmaf((float)cc[u].v[i], h[u][i], sum);
         }
-    }
-    const float x = (float)static_cast<const T*>(in.x)[(int64_t)r * in.x_stride + c];
-    const float raw = (float)static_cast<const T*>(in.delta)[(int64_t)r * in.delta_stride + c] +
-                      (in.delta_bias ? in.delta_bias[c] : 0.0f);
-    const float dt = step_size(raw, in.softplus);
-    float sum = 0.0f;
+        if (VEC) {
 #pragma unroll
-    for (int i = 0; i < S; ++i) {
-        h[i] = fmaf(exp2_fast(dt * a[i] * kLog2e), h[i], dt * x * b[i]);
-        sum = fmaf(cc[i], h[i], sum);
-    }
-#pragma unroll
-    for (int i = 0; i < S; i += 4) {
-        if (whole) {
-            *reinterpret_cast<f32x4*>(sp + i) = f32x4{h[i], h[i + 1], h[i + 2], h[i + 3]};
+            for (int i = 0; i < S; i += 4)
+                *reinterpret_cast<f32x4*>(sp[u] + i) = f32x4{h[u][i], h[u][i + 1], h[u][i + 2], h[u][i + 3]};
         } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (me.q * S + i + j < pl.states) sp[i + j] = h[i + j];
+            for (int i = 0; i < S; ++i)
+                if (first + i < pl.states) sp[u][i] = h[u][i];
         }
-    }
-    sum = quad_sum(sum);
-    if (me.q == 0) {
-        if (in.D) sum = fmaf(in.D[c], x, sum);
-        if (in.z) sum *= silu((float)static_cast<const T*>(in.z)[(int64_t)r * in.z_stride + c]);
-        y[(int64_t)r * y_stride + c] = (T)sum;
+        sum = quad_sum(sum);
+        if (me.q == 0) {
+            sum = fmaf(skip, x[u], sum);
+            if (in.z) sum *= silu(z[u]);
+            y[(int64_t)(r0 + u) * y_stride + c] = (T)sum;
+        }
     }
 }
 
@@ -1519,16 +1533,20 @@ scan_status_t selective_scan_step(const selective_scan_step_args_t* args, void* 
                          range(a.slots, a.rows * 4)};
     if (any_overlap(outs, ins)) return SCAN_ERR_INVALID;
     const Plan p = make_plan(a.channels, a.states, a.groups, a.rows, 1, nullptr);
-    const uint64_t wgs = a.rows * (uint64_t)p.blocks;
+    const uint64_t all = a.rows * (uint64_t)p.blocks;
+    const bool four = all >= 4 * (uint64_t)kTargetWorkgroups;
+    const uint64_t wgs = four ? (a.rows + 3) / 4 * p.blocks : all;
     if (wgs > 0x7FFFFFFFu) return SCAN_ERR_INVALID;
     Inputs in = make_inputs(a, r);
-    in.vec = a.states == padded_states(a.states) && aligned(a.state, 16) && aligned(a.A, 16);
+    in.vec = a.states == padded_states(a.states) && aligned(a.state, 16) && aligned(a.A, 16) && r.vec(a.B, a.b_stride) &&
+             r.vec(a.C, a.c_stride);
     return dispatch(a.dtype, a.states, [&](auto te, auto se) -> scan_status_t {
         using T = decltype(te);
         constexpr int S = decltype(se)::value;
-        hipLaunchKernelGGL((scan_step_kernel<T, S>), dim3((unsigned)wgs), dim3(kGradWaves * 64), 0,
-                           static_cast<hipStream_t>(stream), p, in, a.slots, (uint32_t)a.n_slots, a.state,
-                           static_cast<T*>(a.y), a.y_stride);
+        const auto k = four ? (in.vec ? scan_step_kernel<T, S, true, 4> : scan_step_kernel<T, S, false, 4>)
+                            : (in.vec ? scan_step_kernel<T, S, true, 1> : scan_step_kernel<T, S, false, 1>);
+        hipLaunchKernelGGL(k, dim3((unsigned)wgs), dim3(kGradWaves * 64), 0, static_cast<hipStream_t>(stream), p, in, a.slots,
+                           (uint32_t)a.n_slots, a.state, static_cast<T*>(a.y), a.y_stride);
         return launched();
     });
 }
