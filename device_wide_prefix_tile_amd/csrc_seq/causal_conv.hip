@@ -6,7 +6,7 @@
 //   dw[k] = sum_t g[t] x[t - K + 1 + k];  dbias = sum_t g[t]
 //
 // A few operations per element: HBM-bound (read x, write y; read x and dy,
-// write dx).  A lane owns V neighbouring channels (16 bytes) and walks a block
+// write dx).  A lane owns V neighbouring channels and walks a block
 // of rows with the last K - 1 inputs in registers, so every input is read once
 // but for the K - 1 rows before each block.  The gradient recomputes u rather
 // than keep it, walks K - 1 rows past its block for the g that reach back into

@@ -181,8 +181,9 @@ struct StateTile {
     }
 };
 
+// S consecutive floats, 16-byte aligned.
 template <int S>
-__device__ __forceinline__ void lds_states(const float* p, float (&f)[S])
+__device__ __forceinline__ void read_floats(const float* p, float (&f)[S])
 {
 #pragma unroll
     for (int s = 0; s < S; s += 4) {
@@ -488,7 +489,7 @@ __global__ __launch_bounds__(kFwdWaves * 64) __attribute__((amdgpu_waves_per_eu(
                 unpack(pd[i], df);
                 const int r = X::row(i, me.lane);
                 if (TT % X::RPL && r >= TT) continue;
-                lds_states<V>(bias, bf);
+                read_floats<V>(bias, bf);
                 step_sizes<V>(df, bf, in.softplus, r < len, df);
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
@@ -583,10 +584,12 @@ __global__ __launch_bounds__(kFwdWaves * 64) __attribute__((amdgpu_waves_per_eu(
                     opaque(cx[i]);
                     unpack(cx[i], xf);
                     unpack(cz[i], zf);
-                    lds_states<V>(skip, df);
-                    lds_states<V>(ly + r * CW + X::col(me.lane), f);
+                    read_floats<V>(skip, df);
+                    read_floats<V>(ly + r * CW + X::col(me.lane), f);
+                    if (in.D) {  // without it no term: 0 * x is not 0 for every x
 #pragma unroll
-                    for (int j = 0; j < V; ++j) f[j] = fmaf(df[j], xf[j], f[j]);
+                        for (int j = 0; j < V; ++j) f[j] = fmaf(df[j], xf[j], f[j]);
+                    }
                     if (in.z) {
 #pragma unroll
                         for (int j = 0; j < V; ++j) f[j] *= silu(zf[j]);
@@ -639,7 +642,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void scan_step_kernel(Plan pl, Inp
         const T* bp = static_cast<const T*>(in.B) + (int64_t)r * in.b_stride + bc_at;
         const T* cp = static_cast<const T*>(in.C) + (int64_t)r * in.c_stride + bc_at;
         if (VEC) {
-            lds_states<S>(sp[u], h[u]);
+            read_floats<S>(sp[u], h[u]);
 #pragma unroll
             for (int i = 0; i < S; i += 4) {
                 const Pack<T, 4> p = load_pack<T, 4>(bp + i), q = load_pack<T, 4>(cp + i);
@@ -663,7 +666,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void scan_step_kernel(Plan pl, Inp
         z[u] = in.z ? (float)static_cast<const T*>(in.z)[(int64_t)r * in.z_stride + c] : 0.0f;
     }
     if (VEC) {
-        lds_states<S>(ap, a);
+        read_floats<S>(ap, a);
     } else {
 #pragma unroll
         for (int i = 0; i < S; ++i) a[i] = first + i < pl.states ? ap[i] : 0.0f;
@@ -690,7 +693,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void scan_step_kernel(Plan pl, Inp
         }
         sum = quad_sum(sum);
         if (me.q == 0) {
-            sum = fmaf(skip, x[u], sum);
+            if (in.D) sum = fmaf(skip, x[u], sum);
             if (in.z) sum *= silu(z[u]);
             y[(int64_t)(r0 + u) * y_stride + c] = (T)sum;
         }
@@ -788,7 +791,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void grad_totals_kernel(Plan pl, I
             for (int u = 0; u < 4; ++u) {
                 const f32x2 v = dt[(t - u) * 16 + me.d];
                 float c[S];
-                lds_states<S>(lc + (t - u) * NP + me.q * S, c);
+                read_floats<S>(lc + (t - u) * NP + me.q * S, c);
                 sum += v[0];
 #pragma unroll
                 for (int i = 0; i < S; ++i) g.v[0][i] = exp2_fast(v[0] * A2.v[0][i]) * fmaf(v[1], c[i], g.v[0][i]);
@@ -909,7 +912,7 @@ __global__ __launch_bounds__(Bwd<S>::WAVES * 64) __attribute__((amdgpu_waves_per
                 unpack(cz[i], zf);
                 const int r = X::row(i, me.lane);
                 if (TT % X::RPL && r >= TT) continue;
-                lds_states<V>(bias, bf);
+                read_floats<V>(bias, bf);
                 step_sizes<V>(df, bf, in.softplus, r < len, df);
                 if (in.z) {
 #pragma unroll
@@ -939,7 +942,7 @@ __global__ __launch_bounds__(Bwd<S>::WAVES * 64) __attribute__((amdgpu_waves_per
                 for (int u = 0; u < kSub; ++u) {
                     const int t = k * kSub + u;
                     float b[S];
-                    lds_states<S>(s_b + t * NP + me.q * S, b);
+                    read_floats<S>(s_b + t * NP + me.q * S, b);
 #pragma unroll
                     for (int c = 0; c < CH; ++c) {
                         const f32x2 v = dt[t * CW + me.d + 16 * c];
@@ -955,12 +958,12 @@ __global__ __launch_bounds__(Bwd<S>::WAVES * 64) __attribute__((amdgpu_waves_per
             for (int k = blocks - 1; k >= 0; --k) {
                 float a[kSub][CH][S], hs[kSub + 1][CH][S];  // the factors; the states before each row and behind the last
 #pragma unroll
-                for (int c = 0; c < CH; ++c) lds_states<S>(lh + ((k * CH + c) * 64 + me.lane) * S, hs[0][c]);
+                for (int c = 0; c < CH; ++c) read_floats<S>(lh + ((k * CH + c) * 64 + me.lane) * S, hs[0][c]);
 #pragma unroll
                 for (int u = 0; u < kSub; ++u) {
                     const int t = k * kSub + u;
                     float b[S];
-                    lds_states<S>(s_b + t * NP + me.q * S, b);
+                    read_floats<S>(s_b + t * NP + me.q * S, b);
 #pragma unroll
                     for (int c = 0; c < CH; ++c) {
                         const f32x2 v = dt[t * CW + me.d + 16 * c];
@@ -976,8 +979,8 @@ __global__ __launch_bounds__(Bwd<S>::WAVES * 64) __attribute__((amdgpu_waves_per
                 for (int u = kSub - 1; u >= 0; --u) {
                     const int t = k * kSub + u;
                     float b[S], cc[S], pb_[S], pc_[S];
-                    lds_states<S>(s_b + t * NP + me.q * S, b);
-                    lds_states<S>(s_c + t * NP + me.q * S, cc);
+                    read_floats<S>(s_b + t * NP + me.q * S, b);
+                    read_floats<S>(s_c + t * NP + me.q * S, cc);
 #pragma unroll
                     for (int c = 0; c < CH; ++c) {
                         const f32x2 v = dt[t * CW + me.d + 16 * c];
@@ -1069,16 +1072,20 @@ __global__ __launch_bounds__(Bwd<S>::WAVES * 64) __attribute__((amdgpu_waves_per
                 unpack(cy[i], yf);
                 unpack(cz[i], zf);
                 const int at = r * CW + X::col(me.lane);
-                lds_states<V>(bias, bf);
-                lds_states<V>(skip, sf);
+                read_floats<V>(bias, bf);
+                read_floats<V>(skip, sf);
                 step_sizes<V>(df, bf, in.softplus, true, vf);
                 if (in.z) {
                     float full[V];
-                    lds_states<V>(ldv + at, full);
+                    read_floats<V>(ldv + at, full);
+                    if (in.D) {
+#pragma unroll
+                        for (int j = 0; j < V; ++j) full[j] = fmaf(sf[j], xf[j], full[j]);
+                    }
 #pragma unroll
                     for (int j = 0; j < V; ++j) {
                         const float z = zf[j], sg = sigmoid(z);
-                        oz[j] = yf[j] * fmaf(sf[j], xf[j], full[j]) * sg * (1.0f + z * (1.0f - sg));
+                        oz[j] = yf[j] * full[j] * sg * (1.0f + z * (1.0f - sg));
                         yf[j] *= z * sg;  // dv
                     }
                 }
@@ -1386,7 +1393,8 @@ scan_status_t gradient(const selective_scan_grad_args_t& g, hipStream_t stream)
         if (p.per_seq > 1)
             hipLaunchKernelGGL((in.vec ? grad_totals_kernel<T, S, true> : grad_totals_kernel<T, S, false>), dim3((unsigned)wgs), block, 0, stream, p, in, gr, w.totals);
         if (wgs) {
-            hipLaunchKernelGGL((in.vec ? grad_kernel<T, S, true> : grad_kernel<T, S, false>), dim3((unsigned)wgs), dim3(Bwd<S>::WAVES * 64), 0, stream, p, in, gr, w.totals);
+            hipLaunchKernelGGL((in.vec ? grad_kernel<T, S, true> : grad_kernel<T, S, false>), dim3((unsigned)wgs),
+                               dim3(Bwd<S>::WAVES * 64), 0, stream, p, in, gr, w.totals);
             hipLaunchKernelGGL((join_bc_kernel<T>), dim3((unsigned)bc), dim3(256), 0, stream, p, (const float*)w.bc, np,
                                static_cast<T*>(g.dB), g.db_stride, static_cast<T*>(g.dC), g.dc_stride);
         }

@@ -371,7 +371,8 @@ def causal_conv1d_grad(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, 
     dx may be given to write into (a slice of a wider tensor, say)."""
     a, state = _conv_args(x, weight, bias, activation, seq_offsets, initial_state)
     d, k = weight.shape
-    g = _ConvGradArgs(a, *_like(dy, "dy", x.shape, x.dtype, x.get_device(), x.shape[-1]), _plain(dfinal_state, "dfinal_state", state, x.dtype, x.get_device()))
+    g = _ConvGradArgs(a, *_like(dy, "dy", x.shape, x.dtype, x.get_device(), x.shape[-1]),
+                      _plain(dfinal_state, "dfinal_state", state, x.dtype, x.get_device()))
 
     def call(handle):
         L = _lib()

@@ -67,9 +67,8 @@ scan_status_t embedding_lookup(seq_dtype_t dtype, const void* tokens, int token_
 
 /*
  * Gradient of embedding_lookup: dtable[v] = scale * the sum of dout[i] over
- * the positions i with tokens[i] == v, in ascending order of i for rows of up
- * to 64 positions and in a fixed order for every row; zero for rows without a
- * position.  accumulate != 0 adds to what dtable holds instead and leaves the
+ * the positions i with tokens[i] == v, added up in an order that depends on
+ * the tokens alone; zero for rows without a position.  accumulate != 0 adds to what dtable holds instead and leaves the
  * other rows untouched.  Tokens outside the table are left out.
  * dout: n x channels of dtype; dtable: n_rows x channels (contiguous) of
  * dtype or SEQ_F32.  n < 2^31, n_rows <= 2^24.
@@ -134,6 +133,7 @@ size_t causal_conv1d_grad_workspace(const causal_conv1d_args_t* args);
  * repeated slot's state and rows are then unspecified); rows whose slot lies
  * outside 0 .. n_slots - 1 are skipped: neither their output nor any state is
  * written.  state: n_slots x (width - 1) x channels, contiguous, of dtype.
+ * rows <= 65535.
  */
 typedef struct {
     int32_t dtype, weight_dtype, activation, width;

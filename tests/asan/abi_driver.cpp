@@ -18,6 +18,7 @@
 #include <vector>
 
 #include "dwpt_scan.h"
+#include "dwpt_seq.h"
 
 static int g_fail = 0;
 
@@ -28,6 +29,26 @@ static int g_fail = 0;
             ++g_fail;                                                         \
         }                                                                     \
     } while (0)
+
+// The sequence operators' argument checks and workspace sizes.
+static void seq_host_checks(uint32_t* buf)
+{
+    EXPECT(embedding_lookup(SEQ_F32, buf, 4, 0, buf, 4, 4, 4, 1.0f, buf, nullptr) == SCAN_OK);
+    EXPECT(embedding_lookup(SEQ_F32, buf, 4, 4, buf, 4, 4, 4, 1.0f, buf, nullptr) == SCAN_ERR_INVALID);  // out over table
+    EXPECT(embedding_grad(SEQ_F32, SEQ_F32, buf, 4, 4, buf, 4, 4, 4, 1.0f, 0, buf, nullptr, 0, nullptr) == SCAN_ERR_INVALID);
+    EXPECT(embedding_grad_workspace(1000, 1000, 8) > 1000 * 4);
+    EXPECT(causal_conv1d(nullptr, nullptr) == SCAN_ERR_INVALID);
+    causal_conv1d_args_t c{};
+    EXPECT(causal_conv1d(&c, nullptr) == SCAN_ERR_UNSUPPORTED);  // width 0
+    EXPECT(causal_conv1d_grad_workspace(&c) == 0);
+    selective_scan_args_t a{};
+    EXPECT(selective_scan(&a, nullptr) == SCAN_ERR_UNSUPPORTED);  // no states
+    a.states = 16;
+    EXPECT(selective_scan(&a, nullptr) == SCAN_ERR_INVALID);  // no channels
+    EXPECT(selective_scan_workspace(&a) == 0 && selective_scan_saved(&a) == 0);
+    EXPECT(selective_scan_grad(nullptr, nullptr) == SCAN_ERR_INVALID);
+    EXPECT(selective_scan_step(nullptr, nullptr) == SCAN_ERR_INVALID);
+}
 
 static void host_checks()
 {
@@ -50,6 +71,7 @@ static void host_checks()
     EXPECT(radix_split(buf, nullptr, 16, 0, buf + 8, nullptr, nullptr) == SCAN_ERR_INVALID);    // output overlaps keys
     EXPECT(csr_row_offsets(buf, 4, 3, nullptr, nullptr) == SCAN_ERR_INVALID);
     EXPECT(scan_noalloc(SCAN_OP_MAT3, SCAN_U32X9, buf, buf, (size_t)1 << 40, 0, nullptr) == SCAN_ERR_INVALID);
+    seq_host_checks(buf);
     // strings and knobs
     for (int s = -1; s <= 7; ++s) EXPECT(std::strlen(scan_status_string((scan_status_t)s)) > 0);
     const size_t old = scan_set_small_n_max(123);
@@ -67,6 +89,87 @@ static void host_checks()
             std::exit(3);                                                                 \
         }                                                                                 \
     } while (0)
+
+// One training pass of the sequence operators on a stream: tokens, table, convolution, scan and back.
+static void seq_device_checks(hipStream_t st)
+{
+    const uint64_t b = 3, l = 150, rows = b * l;
+    const uint32_t d = 72, n = 16, v = 100;
+    std::vector<int32_t> tok(rows);
+    for (uint64_t i = 0; i < rows; ++i) tok[i] = (int32_t)(i * 37 % 103) - 1;  // some outside the table
+    std::vector<float> table(v * d, 0.25f), weight(d * 4, 0.5f), A(d * n, -1.0f), bc(rows * 2 * n, 0.5f);
+    std::vector<void*> mem;
+    const auto dev = [&](const void* src, size_t bytes) {
+        void* p = nullptr;
+        HIPCHECK(hipMalloc(&p, bytes));
+        mem.push_back(p);
+        if (src)
+            HIPCHECK(hipMemcpy(p, src, bytes, hipMemcpyHostToDevice));
+        else
+            HIPCHECK(hipMemset(p, 0, bytes));
+        return p;
+    };
+    const size_t big = rows * d * 4;
+    void *dtok = dev(tok.data(), rows * 4), *dtab = dev(table.data(), v * d * 4), *e = dev(nullptr, big), *u = dev(nullptr, big);
+    void *y = dev(nullptr, big), *dbc = dev(bc.data(), bc.size() * 4), *dw = dev(weight.data(), weight.size() * 4);
+    EXPECT(embedding_lookup(SEQ_F32, dtok, 4, rows, dtab, d, v, d, 2.0f, e, st) == SCAN_OK);
+    causal_conv1d_grad_args_t cg{};
+    causal_conv1d_args_t& c = cg.args;
+    c.width = 4;
+    c.activation = SEQ_ACT_SILU;
+    c.rows = rows;
+    c.seqs = b;
+    c.channels = d;
+    c.x = e;
+    c.x_stride = c.y_stride = d;
+    c.weight = dw;
+    c.y = u;
+    EXPECT(causal_conv1d(&c, st) == SCAN_OK);
+    selective_scan_grad_args_t sg{};
+    selective_scan_args_t& a = sg.args;
+    a.rows = rows;
+    a.seqs = b;
+    a.channels = d;
+    a.states = n;
+    a.groups = 1;
+    a.delta_softplus = 1;
+    a.x = a.delta = u;
+    a.x_stride = a.delta_stride = a.y_stride = d;
+    a.A = (const float*)dev(A.data(), A.size() * 4);
+    a.B = dbc;
+    a.C = (const float*)dbc + n;
+    a.b_stride = a.c_stride = 2 * n;
+    a.y = y;
+    a.saved = (float*)dev(nullptr, selective_scan_saved(&a) * 4);
+    a.workspace_bytes = selective_scan_workspace(&a);
+    a.workspace = dev(nullptr, a.workspace_bytes);
+    EXPECT(selective_scan(&a, st) == SCAN_OK);
+    sg.dy = y;
+    sg.dx = dev(nullptr, big);
+    sg.ddelta = dev(nullptr, big);
+    sg.dB = dev(nullptr, rows * n * 4);
+    sg.dC = dev(nullptr, rows * n * 4);
+    sg.dy_stride = sg.dx_stride = sg.ddelta_stride = d;
+    sg.db_stride = sg.dc_stride = n;
+    sg.dA = (float*)dev(nullptr, A.size() * 4);
+    a.workspace_bytes = selective_scan_grad_workspace(&sg);
+    a.workspace = dev(nullptr, a.workspace_bytes);
+    EXPECT(selective_scan_grad(&sg, st) == SCAN_OK);
+    cg.dy = sg.dx;
+    cg.dx = dev(nullptr, big);
+    cg.dy_stride = cg.dx_stride = d;
+    cg.dweight = (float*)dev(nullptr, weight.size() * 4);
+    cg.workspace_bytes = causal_conv1d_grad_workspace(&c);
+    cg.workspace = dev(nullptr, cg.workspace_bytes);
+    EXPECT(causal_conv1d_grad(&cg, st) == SCAN_OK);
+    const size_t need = embedding_grad_workspace(rows, v, d);
+    EXPECT(embedding_grad(SEQ_F32, SEQ_F32, dtok, 4, rows, cg.dx, d, v, d, 2.0f, 0, dtab, dev(nullptr, need), need, st) == SCAN_OK);
+    HIPCHECK(hipStreamSynchronize(st));
+    float first = -1.0f;  // u[0] = silu(e[0] * 0.5): token -1 is a row of zeros
+    HIPCHECK(hipMemcpy(&first, u, 4, hipMemcpyDeviceToHost));
+    EXPECT(first == 0.0f);
+    for (void* p : mem) HIPCHECK(hipFree(p));
+}
 
 static void device_checks()
 {
@@ -125,6 +228,7 @@ static void device_checks()
         }
         EXPECT(scan_release_workspace() == SCAN_OK);
     }
+    for (int i = 0; i < 2; ++i) seq_device_checks(s[i]);
     HIPCHECK(hipFree(x));
     HIPCHECK(hipFree(y));
     HIPCHECK(hipFree(cnt));

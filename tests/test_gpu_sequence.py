@@ -439,6 +439,114 @@ def test_linear_gradients_match_differences():
         assert abs(got - (f64(grad) * exact_step).sum()) <= bound, name
 
 
+# ---------------------------------------------------------------------- sizes that take the other shapes
+@pytest.mark.parametrize("t,n", [("bf16", 16), ("f32", 5)])
+def test_scan_step_many_rows(t, n):
+    """Enough rows that a wavefront takes four of them, with slots that end inside such a four."""
+    rng = np.random.default_rng(30 + n)
+    rows, d, t = 2051, 130, T[t]
+    v = scan_inputs(rng, (1, rows), d, n, 1, t, strided=True)
+    state = randn(rng, rows, d, n)
+    start = state.clone()
+    slots = torch.from_numpy(rng.permutation(rows).astype(np.int32)).cuda()
+    slots[::97] = -1
+    y = torch.full((rows, d), 9.0, dtype=t, device="cuda")
+    dw.selective_scan_step(v["x"][0], v["delta"][0], v["A"], v["B"][0], v["C"][0], state, D=v["D"], z=v["z"][0],
+                           delta_bias=v["delta_bias"], delta_softplus=True, slots=slots, out=y)
+    live = (slots >= 0).nonzero()[:, 0]
+    w = {k: (q[:, live] if q.dim() > 2 else q) for k, q in v.items()}
+    at = slots[live].long()
+    want = scan_reference(w, [(i, i + 1) for i in range(live.numel())], start[at])
+    close(y[live], *want["y"], "y")
+    close(state[at], *want["final"], "state")
+    assert (y[slots < 0] == 9.0).all()
+    rest = torch.ones(rows, dtype=torch.bool, device="cuda")
+    rest[at] = False
+    same(state[rest], start[rest], "other slots")
+
+
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+def test_conv_long_blocks_match_short_ones(t):
+    """64 sequences at once take the longest row blocks, one at a time shorter ones: the same bits per
+    row; the weights' sums within their bound."""
+    rng = np.random.default_rng(31)
+    b, l, d, t = 64, 700, 1024, T[t]
+    x, dy = randn(rng, b, l, d, t=t), randn(rng, b, l, d, t=t)
+    w, bias = randn(rng, d, 4, t=t), randn(rng, d, t=t)
+    y = dw.causal_conv1d(x, w, bias, activation="silu")
+    g = dw.causal_conv1d_grad(dy, x, w, bias, activation="silu")
+    dweight, dbias, mag = torch.zeros(d, 4, dtype=torch.float64), torch.zeros(d, dtype=torch.float64), 0.0
+    for i in range(b):
+        yi = dw.causal_conv1d(x[i:i + 1], w, bias, activation="silu")
+        gi = dw.causal_conv1d_grad(dy[i:i + 1], x[i:i + 1], w, bias, activation="silu")
+        assert torch.equal(yi[0], y[i]) and torch.equal(gi.dx[0], g.dx[i])
+        dweight += gi.dweight.double().cpu()
+        dbias += gi.dbias.double().cpu()
+    # |act'| <= 1.1: the terms of a sum over rows are at most 1.1 |dy| |x|; two sums of b l terms each
+    largest = 1.1 * float((dy.abs().amax() * torch.clamp(x.abs().amax(), min=1.0)).float())
+    bound = 2 * b * l * 2 ** -24 * b * l * largest
+    assert (g.dweight.double().cpu() - dweight).abs().max() <= bound and (g.dbias.double().cpu() - dbias).abs().max() <= bound
+
+
+def test_offsets_past_32_bits():
+    """Rows, slots and table rows whose element offsets pass 2^31."""
+    rng = np.random.default_rng(32)
+    rows, tail, d, n = 540001, 150, 64, 16
+    big = torch.zeros(rows, 4096, dtype=torch.bfloat16, device="cuda")  # 2.2e9 elements
+    assert rows * 4096 > 2 ** 31
+    v = scan_inputs(rng, (tail,), d, n, 1, torch.bfloat16, strided=False)
+    x = big[:, 64:64 + d]
+    x[-tail:] = v["x"]
+    off = torch.tensor([0, rows - tail, rows], dtype=torch.int32, device="cuda")
+    w, b = randn(rng, d, 4, t=torch.bfloat16), randn(rng, d, t=torch.bfloat16)
+    want = ref.conv(f64(v["x"]), f64(w), f64(b), True, [(0, tail)], None, f64(v["x"]))
+    close(dw.causal_conv1d(x, w, b, activation="silu", seq_offsets=off)[-tail:], *want["y"], "conv y")
+    close(dw.causal_conv1d_grad(x, x, w, b, activation="silu", seq_offsets=off).dx[-tail:], *want["dx"], "conv dx")
+    z = big[:, 256:256 + d]
+    z[-tail:] = v["z"]
+    bc = big[:, 512:512 + 2 * n]
+    bc[-tail:, :n], bc[-tail:, n:] = v["B"].flatten(-2), v["C"].flatten(-2)
+    B, C = bc[:, :n].unflatten(-1, (1, n)), bc[:, n:].unflatten(-1, (1, n))
+    v["delta"] = v["x"]
+    want = scan_reference(v, [(0, tail)], None, v["z"])
+    kw = dict(D=v["D"], z=z, delta_bias=v["delta_bias"], delta_softplus=True, seq_offsets=off)
+    y, saved = dw.selective_scan(x, x, v["A"], B, C, save_for_grad=True, **kw)
+    close(y[-tail:], *want["y"], "scan y")
+    g = dw.selective_scan_grad(z, x, x, v["A"], B, C, saved=saved, **kw)
+    scan_check(dict(dx=g.dx[-tail:], dz=g.dz[-tail:], dB=g.dB[-tail:], dC=g.dC[-tail:]), want, "past 32 bits")
+    # tables and states
+    tok = torch.tensor([rows - 1, 7, rows - 2], dtype=torch.int32, device="cuda")
+    same(dw.embedding_lookup(tok, big), big[tok.long()], "lookup")
+    gt = dw.embedding_grad(tok, big[-3:], rows)
+    same(gt[tok.long()], big[-3:], "table gradient")
+    del big, gt, x, z, bc, B, C, g, y
+    slots = 33000
+    state = torch.zeros(slots, 4096, n, device="cuda")  # 2.2e9 elements
+    one = scan_inputs(rng, (1, 2), 4096, n, 1, torch.float32, strided=False)
+    at = torch.tensor([slots - 1, 5], dtype=torch.int32, device="cuda")
+    state[at.long()] = randn(rng, 2, 4096, n)
+    start = state[at.long()]
+    y = dw.selective_scan_step(one["x"][0], one["delta"][0], one["A"], one["B"][0], one["C"][0], state, D=one["D"], z=one["z"][0],
+                               delta_bias=one["delta_bias"], delta_softplus=True, slots=at)
+    want = scan_reference(one, [(0, 1), (1, 2)], start)
+    close(y, *want["y"], "step y")
+    close(state[at.long()], *want["final"], "step state")
+
+
+def test_scan_infinite_input_without_skip():
+    """Without D there is no term of it: an infinite x reaches y through the state alone."""
+    d, n = 16, 16
+    one = lambda *s: torch.ones(*s, device="cuda")  # noqa: E731
+    x = one(1, 3, d)
+    x[0, 1, 4] = float("inf")
+    args = (x, one(1, 3, d), -one(d, n), one(1, 3, 1, n), one(1, 3, 1, n))
+    y = dw.selective_scan(*args)
+    state = torch.zeros(1, d, n, device="cuda")
+    steps = [dw.selective_scan_step(x[:, i], args[1][:, i], args[2], args[3][:, i], args[4][:, i], state) for i in range(3)]
+    for v in (y[0], torch.cat(steps)):
+        assert (v[1:, 4] == float("inf")).all() and torch.isfinite(v[:, :4]).all() and torch.isfinite(v[0]).all()
+
+
 # ---------------------------------------------------------------------- together, graphs, streams
 def block(p, tokens, off=None, conv_state=None, scan_state=None):
     """Embedding, convolution, scan: a prompt."""

@@ -189,8 +189,8 @@ def test_workspace_queries_follow_the_plan(L):
     one = scan_args(rows=64 * 256, seqs=1, channels=256, **wide)
     assert L.selective_scan_workspace(ctypes.byref(many)) == 256
     assert L.selective_scan_workspace(ctypes.byref(one)) > 256 * 16 * 4
-    # the saved states: one per 32 rows, channel and (padded) state
-    assert L.selective_scan_saved(ctypes.byref(many)) == 64 * 8 * 4096 * 16
+    # the saved states: one per 16 rows, channel and (padded) state
+    assert L.selective_scan_saved(ctypes.byref(many)) == 64 * 16 * 4096 * 16
     assert L.selective_scan_saved(ctypes.byref(scan_args(rows=0, seqs=0, x=None, delta=None, B=None, C=None, z=None, y=None))) == 0
     assert L.selective_scan_workspace(ctypes.byref(scan_args(groups=3))) == 0
 
