@@ -5,20 +5,17 @@
 //
 // The recurrence is a scan of real affine maps h -> a h + b, as many as
 // rows x channels x states, that are made from far fewer inputs and never
-// leave the registers.  Per map: one exponential (a quarter-rate
-// instruction) and four multiplies or fused multiply-adds, against 1/16 of
-// the bytes of a row: the kernels are bound by the vector units, not by
-// memory.
+// leave the registers.  Per map: one exponential and three or four multiplies
+// or fused multiply-adds, against 1/16 of the bytes of a row: the kernels are
+// bound by the issue of vector instructions, not by memory.
 //
-// Layout.  A wavefront owns 16 channels; lane = 4 * channel + quarter, and a
-// lane holds S = ceil(states / 4) rounded up to 4, 8 or 16 neighbouring states
-// of its channel.  The sum over a channel's states is then S - 1 adds in the
-// lane and two DPP adds in its quad.  Rows are taken in tiles: the lanes load
-// 16-byte pieces of the tile's rows (the next tile's while this one is worked
-// on), turn them into (dt, dt x) pairs in LDS, B and C into 32-bit rows, and
-// walk the rows; results go back through LDS to the lanes that loaded the
-// inputs, which finish and store them as 16-byte pieces.  No wavefront waits
-// for another.
+// Layout.  A wavefront owns 16 channels (32 in the gradient); four lanes share a channel's states, S =
+// states / 4 rounded up to 4, 8 or 16 each (Place).  The sum over a channel's states is then S - 1 adds
+// in the lane and a sum over four lanes, four rows at a time.  Rows are taken in tiles: the lanes load
+// 16-byte pieces of the tile's rows (the next tile's while this one is worked on), turn them into dt
+// and dt x in LDS, B and C into 32-bit rows, and walk the rows; results go back through LDS to the
+// lanes that loaded the inputs, which finish and store them as 16-byte pieces.  Forwards no wavefront
+// waits for another; in the gradient a workgroup's wavefronts share B and C and add up dB and dC.
 //
 // Spans.  Where sequences and channels are too few to fill the chip, the rows
 // are cut into spans that are scanned at the same time: a first launch takes
@@ -36,9 +33,9 @@
 namespace dwpt_seq {
 namespace {
 
-constexpr int kWgChannels = 64;       // channels per workgroup
+constexpr int kWgChannels = 64;      // channels per workgroup
 constexpr uint32_t kMaxChannels = 1u << 20;
-constexpr uint32_t kEmptyStep = 32;   // workgroups per channel block that look for empty sequences
+constexpr uint32_t kEmptyStep = 32;  // workgroups per channel block that look for empty sequences
 
 constexpr int kSaveRows = 16;         // rows between the states that the gradient starts from; rows of its tiles
 constexpr int kSub = 4;               // rows whose factors and states the gradient keeps in registers
@@ -716,7 +713,7 @@ struct Grads {
 
 // Backwards, g = a[t+1] dh[t+1] is what the later rows pass on to row t's state:
 //   dh = dv C + g;  g' = a dh         (dv = dy silu(z))
-// Totals of a span for the spans before it: g at its first row from g = 0 behind its last (or from
+// Totals of a span for the spans before it (110 us for 8192 x 4096 channels, bound as the forward pass): g at its first row from g = 0 behind its last (or from
 // dfinal where the sequence ends in it), and the sum of dt.
 template <typename T, int S, bool VEC>
 __global__ __launch_bounds__(kGradWaves * 64) void grad_totals_kernel(Plan pl, Inputs in, Grads gr, SpanTotals totals)
@@ -806,7 +803,13 @@ __global__ __launch_bounds__(kGradWaves * 64) void grad_totals_kernel(Plan pl, I
     if (me.q == 0 && me.d < me.nch) totals.dt_sum[(size_t)span * pl.channels + me.c0 + me.d] = sum;
 }
 
-// Every gradient of a span's rows.  Tiles are taken from the last to the first.  A tile's states
+// Every gradient of a span's rows.  Measured: 727 of the 1117 us of a training step (4 x 2048 x 4096
+// channels, 16 states, bfloat16); 107 vector instructions per row and 16 channels for 4 states per
+// lane keep the vector units busy 58% of the time, the matrix unit is busy 16% of it; two wavefronts
+// per SIMD (256 registers).  With one channel per lane, eight rows' factors in registers and twice
+// the matrix instructions it took 870.
+//
+// Tiles are taken from the last to the first.  A tile's states
 // are recomputed from its saved one: once forwards, keeping the state in front of every kSub rows,
 // then kSub rows at a time with their factors a and states h in registers, which the walk back over
 // those rows uses:
@@ -1198,9 +1201,9 @@ __global__ __launch_bounds__(kGradWaves * 64) void grad_empty_kernel(Plan pl, co
 }
 
 // ------------------------------------------------------------ host side
-// Workgroups (of four wavefronts) that the rows are cut for.
-// Measured (16384 x 2048 channels / ragged 6001 x 4096 / training 4 x 2048 x 4096): 512 workgroups
-// 475 / 349 / 1478 us, 1024 259 / 212 / 1239, 2048 316 / 215 / 1250.
+// Workgroups that the rows are cut for.  Measured (one prompt of 16384 x 2048 channels / ragged 6001 x
+// 4096 / training 4 x 2048 x 4096, us): 512 workgroups 278 / 215 / 1703, 768 264 / 198 / 1245, 1024 256 /
+// 194 / 1117, 2048 260 / 194 / 1107.
 constexpr uint32_t kTargetWorkgroups = 1024;
 constexpr uint32_t kMinSpanRows = 128;
 
