@@ -28,6 +28,8 @@
 //
 // Packed sequences are segments: a wavefront walks them one after another,
 // starting each from its initial state.
+#include <cmath>
+
 #include "seq_common.hpp"
 
 namespace dwpt_seq {
@@ -1205,7 +1207,14 @@ __global__ __launch_bounds__(kGradWaves * 64) void grad_empty_kernel(Plan pl, co
 // 4096 / training 4 x 2048 x 4096, us): 512 workgroups 278 / 215 / 1703, 768 264 / 198 / 1245, 1024 256 /
 // 194 / 1117, 2048 260 / 194 / 1107.
 constexpr uint32_t kTargetWorkgroups = 1024;
-constexpr uint32_t kMinSpanRows = 128;
+// Shortest span, and the most workgroups for the sake of many short sequences (which bounds the
+// workspace).  A span's rows are walked twice and its start joins the spans before it one by one, so
+// a sequence of L rows is cut into about sqrt(L) spans at most.  Spans of at least 128 / 64 / 32 rows:
+// forward 512 rows x 2048 channels 30 / 23 / 23 us, 2048 x 1024 34 / 31 / 40 (64 spans: the joins);
+// forward and gradients 1 x 256 x 2048 150 / 91 / 71, 1 x 1024 x 2048 166 / 135 / 109; 128 rows x 2048
+// forward 20 (one launch) / 23 / 23.
+constexpr uint32_t kMinSpanRows = 32;
+constexpr uint32_t kMostWorkgroups = 8192;
 
 Plan make_plan(uint32_t channels, uint32_t states, uint32_t groups, uint64_t rows, uint64_t seqs, const int32_t* offsets)
 {
@@ -1223,7 +1232,16 @@ Plan make_plan(uint32_t channels, uint32_t states, uint32_t groups, uint64_t row
     uint64_t cuts = 1;
     if (run) {
         cuts = (kTargetWorkgroups + runs * p.blocks - 1) / (runs * p.blocks);
-        cuts = std::max<uint64_t>(1, std::min<uint64_t>(cuts, run / kMinSpanRows));
+        uint64_t most = run / kMinSpanRows;
+        if (offsets) {
+            // a wavefront walks its span's sequences one after another: a few for each
+            cuts = std::max<uint64_t>(cuts, std::min<uint64_t>(seqs / 4, kMostWorkgroups / p.blocks));
+            most = std::min<uint64_t>(most, (uint64_t)std::sqrt((double)rows * (double)seqs));
+        } else {
+            most = std::min<uint64_t>(most, (uint64_t)std::sqrt((double)run));
+        }
+        if (run <= 2 * kMinSpanRows) most = 1;
+        cuts = std::max<uint64_t>(1, std::min<uint64_t>(cuts, most));
     }
     p.span_rows = (uint32_t)std::max<uint64_t>(tt, round_up((run + cuts - 1) / cuts, tt));
     p.per_seq = (uint32_t)((run + p.span_rows - 1) / p.span_rows);

@@ -324,6 +324,24 @@ def test_scan_batch(t, b, l, d, n, g):
     scan_check(grads_dict(grads), want, "batch")
 
 
+@pytest.mark.parametrize("d", [16, 200])
+def test_scan_many_short_sequences(d):
+    """Hundreds of sequences of no row to a few (a batch of drafts, say): several in every span, spans that
+    begin and end inside them."""
+    rng = np.random.default_rng(40 + d)
+    lengths = [int(v) for v in rng.integers(0, 6, 300)] + [70] + [0, 0, 1]
+    rows, n = sum(lengths), 16
+    v = scan_inputs(rng, (rows,), d, n, 1, torch.float32, strided=False)
+    off = offsets(lengths)
+    init, dfin, dy = randn(rng, len(lengths), d, n), randn(rng, len(lengths), d, n), randn(rng, rows, d)
+    want = scan_reference(v, ref.ranges(None, off.tolist()), init, dy, dfin)
+    a, kw = call_args(v)
+    kw.update(delta_softplus=True, seq_offsets=off, initial_state=init)
+    y, fin, saved = dw.selective_scan(*a, final_state=True, save_for_grad=True, **kw)
+    scan_check(dict(y=y, final=fin), want, "many")
+    scan_check(grads_dict(dw.selective_scan_grad(dy, *a, saved=saved, dfinal_state=dfin, **kw)), want, "many")
+
+
 @pytest.mark.parametrize("t", list(T))
 @pytest.mark.parametrize("rows,d,n,g", [(1, 1, 1, 1), (3, 64, 16, 2), (9, 40, 64, 1), (17, 70, 9, 2), (5, 24, 32, 3)])
 def test_scan_step(t, rows, d, n, g):
