@@ -44,7 +44,7 @@ def lookup_reference(tokens, table, scale):
 
 
 @pytest.mark.parametrize("t", list(T))
-@pytest.mark.parametrize("n,v,d", [(0, 5, 8), (1, 1, 1), (3, 7, 5), (65, 300, 64), (130, 1000, 515), (77, 50, 2056), (1000, 40000, 96)])
+@pytest.mark.parametrize("n,v,d", [(0, 5, 8), (1, 1, 1), (3, 7, 5), (65, 300, 64), (130, 1000, 515), (66, 90, 590), (77, 50, 2056), (1000, 40000, 96)])
 def test_lookup(t, n, v, d):
     rng = np.random.default_rng(n + d)
     for dtype in (torch.int32, torch.int64):
@@ -94,7 +94,8 @@ def tokens_of(kind, rng, n, v):
 
 @pytest.mark.parametrize("t", list(T))
 @pytest.mark.parametrize("kind", ["uniform", "one", "few", "none", "skewed"])
-@pytest.mark.parametrize("n,v,d", [(0, 3, 8), (1, 1, 1), (5, 9, 3), (64, 20, 64), (65, 257, 40), (1000, 700, 72), (4097, 3000, 17)])
+@pytest.mark.parametrize("n,v,d", [(0, 3, 8), (1, 1, 1), (5, 9, 3), (64, 20, 64), (65, 257, 40), (90, 300, 590),
+                                   (1000, 700, 72), (4097, 3000, 17)])
 def test_grad(t, kind, n, v, d):
     rng = np.random.default_rng(n + v)
     tok = tokens_of(kind, rng, n, v).int().cuda()
