@@ -28,18 +28,14 @@
 //
 // Packed sequences are segments: a wavefront walks them one after another,
 // starting each from its initial state.
-#include <cmath>
-
 #include "seq_common.hpp"
 
 namespace dwpt_seq {
 namespace {
 
-constexpr int kWgChannels = 64;      // channels per workgroup
 constexpr uint32_t kMaxChannels = 1u << 20;
 constexpr uint32_t kEmptyStep = 32;  // workgroups per channel block that look for empty sequences
 
-constexpr int kSaveRows = 16;         // rows between the states that the gradient starts from; rows of its tiles
 constexpr int kSub = 4;               // rows whose factors and states the gradient keeps in registers
 
 // S states per lane: TT rows per tile of the forward kernels.
@@ -50,34 +46,6 @@ struct Cfg {
 };
 
 int states_per_lane(uint32_t states) { return states <= 16 ? 4 : states <= 32 ? 8 : 16; }
-
-// Rows cut into spans.  Sequences of one length: `per_seq` spans of `span_rows` rows for each (the
-// last one shorter); packed sequences: every span_rows rows, wherever sequences begin.
-struct Plan {
-    Sequences seqs;
-    uint32_t channels, states, groups, group_channels;
-    uint32_t blocks_per_group, blocks;  // workgroups along a group's channels, along all
-    uint32_t span_rows, per_seq, spans, tiles_per_span;
-
-    __device__ __forceinline__ void rows_of(uint32_t span, uint32_t& r0, uint32_t& r1) const
-    {
-        if (seqs.offsets) {
-            r0 = span * span_rows;
-            r1 = min(r0 + span_rows, seqs.rows);
-        } else {
-            const uint32_t s = span / per_seq, first = (span % per_seq) * span_rows;
-            r0 = s * seqs.len + first;
-            r1 = s * seqs.len + min(first + span_rows, seqs.len);
-        }
-    }
-    // The span that row r of the sequence that `span` meets lies in (r in a sequence of `span`).
-    __device__ __forceinline__ uint32_t span_of(uint32_t span, uint32_t r) const
-    {
-        if (seqs.offsets) return r / span_rows;
-        const uint32_t s = span / per_seq;
-        return s * per_seq + (r - s * seqs.len) / span_rows;
-    }
-};
 
 struct Inputs {
     const void *x, *delta, *B, *C, *z;
@@ -336,15 +304,16 @@ struct SpanTotals {
     float* states;  // [span][channels][NP]
     float* dt_sum;  // [span][channels]
 };
-// h = the state behind spans [first, last], joined in order (`step` 1) or in reverse (-1).
+// h = the state behind spans first .. last, joined in that order, up or down.
 template <int S, int CH, bool QUADS>
 __device__ __forceinline__ void join_spans(const SpanTotals& t, const Plan& pl, const Place<16 * CH, QUADS>& me,
-                                           uint32_t first, uint32_t last, int step, const LaneStates<S, CH, QUADS>& A2,
+                                           uint32_t first, uint32_t last, const LaneStates<S, CH, QUADS>& A2,
                                            LaneStates<S, CH, QUADS>& h)
 {
     h.load_padded(t.states, pl, me, first);
+    const uint32_t step = first <= last ? 1u : ~0u;
 #pragma unroll 4
-    while (first != last) {
+    for (uint32_t left = first <= last ? last - first : first - last; left; --left) {
         first += step;
         LaneStates<S, CH, QUADS> e;
         e.load_padded(t.states, pl, me, first);
@@ -448,12 +417,13 @@ __global__ __launch_bounds__(kFwdWaves * 64) __attribute__((amdgpu_waves_per_eu(
             pos = e;
             continue;
         }
-        if (pos == st)
+        uint32_t from, to;
+        if (!pl.spans_before(span, r0, pos, st, from, to))
             h.start(in.initial, pl, me, (uint32_t)s);
         else if (TOTALS)
             h.zero();
         else
-            join_spans<S, CH, false>(totals, pl, me, pl.span_of(span, st), span - 1, 1, A2, h);
+            join_spans<S, CH, false>(totals, pl, me, from, to, A2, h);
         float sum[CH] = {};
         typename X::P px[X::PIECES], pd[X::PIECES], pz[X::PIECES];
         typename BC::P pb[BC::PIECES], pc[BC::PIECES];
@@ -879,10 +849,11 @@ __global__ __launch_bounds__(Bwd<S>::WAVES * 64) __attribute__((amdgpu_waves_per
         s = uniform(s);
         const uint32_t st = pl.seqs.start((uint32_t)s), en = max(pl.seqs.end((uint32_t)s), hi);
         const uint32_t first = (uint32_t)uniform((int)max(st, r0));
-        if (hi == en)
-            g.start(gr.dfinal, pl, me, (uint32_t)s);
+        uint32_t from, to;
+        if (pl.spans_behind(span, r1, hi, en, from, to))
+            join_spans<S, CH, true>(totals, pl, me, from, to, A2, g);
         else
-            join_spans<S, CH, true>(totals, pl, me, pl.span_of(span, en - 1), span + 1, -1, A2, g);
+            g.start(gr.dfinal, pl, me, (uint32_t)s);
         typename X::P px[X::PIECES], pd[X::PIECES], pz[X::PIECES], py[X::PIECES];
         typename BC::P pb[BC::PIECES], pc[BC::PIECES];
         const auto fetch = [&](uint32_t at, int len) {
@@ -1203,55 +1174,9 @@ __global__ __launch_bounds__(kGradWaves * 64) void grad_empty_kernel(Plan pl, co
 }
 
 // ------------------------------------------------------------ host side
-// Workgroups that the rows are cut for.  Measured (one prompt of 16384 x 2048 channels / ragged 6001 x
-// 4096 / training 4 x 2048 x 4096, us): 512 workgroups 278 / 215 / 1703, 768 264 / 198 / 1245, 1024 256 /
-// 194 / 1117, 2048 260 / 194 / 1107.
-constexpr uint32_t kTargetWorkgroups = 1024;
-// Shortest span, and the most workgroups for the sake of many short sequences (which bounds the
-// workspace).  A span's rows are walked twice and its start joins the spans before it one by one, so
-// a sequence of L rows is cut into about sqrt(L) spans at most.  Spans of at least 128 / 64 / 32 rows:
-// forward 512 rows x 2048 channels 30 / 23 / 23 us, 2048 x 1024 34 / 31 / 40 (64 spans: the joins);
-// forward and gradients 1 x 256 x 2048 150 / 91 / 71, 1 x 1024 x 2048 166 / 135 / 109; 128 rows x 2048
-// forward 20 (one launch) / 23 / 23.
-constexpr uint32_t kMinSpanRows = 32;
-constexpr uint32_t kMostWorkgroups = 8192;
-
-Plan make_plan(uint32_t channels, uint32_t states, uint32_t groups, uint64_t rows, uint64_t seqs, const int32_t* offsets)
-{
-    Plan p{};
-    p.seqs = Sequences{offsets, (uint32_t)rows, (uint32_t)seqs, seqs ? (uint32_t)(rows / seqs) : 0u};
-    p.channels = channels;
-    p.states = states;
-    p.groups = groups;
-    p.group_channels = channels / groups;
-    p.blocks_per_group = (p.group_channels + kWgChannels - 1) / kWgChannels;
-    p.blocks = groups * p.blocks_per_group;
-    constexpr uint32_t tt = 32;  // spans are whole tiles
-    // rows of one sequence, or of all packed ones; and how many spans they may be cut into
-    const uint64_t run = offsets ? rows : p.seqs.len, runs = offsets ? 1 : seqs;
-    uint64_t cuts = 1;
-    if (run) {
-        cuts = (kTargetWorkgroups + runs * p.blocks - 1) / (runs * p.blocks);
-        uint64_t most = run / kMinSpanRows;
-        if (offsets) {
-            // a wavefront walks its span's sequences one after another: a few for each
-            cuts = std::max<uint64_t>(cuts, std::min<uint64_t>(seqs / 4, kMostWorkgroups / p.blocks));
-            most = std::min<uint64_t>(most, (uint64_t)std::sqrt((double)rows * (double)seqs));
-        } else {
-            most = std::min<uint64_t>(most, (uint64_t)std::sqrt((double)run));
-        }
-        if (run <= 2 * kMinSpanRows) most = 1;
-        cuts = std::max<uint64_t>(1, std::min<uint64_t>(cuts, most));
-    }
-    p.span_rows = (uint32_t)std::max<uint64_t>(tt, round_up((run + cuts - 1) / cuts, tt));
-    p.per_seq = (uint32_t)((run + p.span_rows - 1) / p.span_rows);
-    p.spans = offsets ? p.per_seq : (uint32_t)(p.per_seq * seqs);
-    p.tiles_per_span = p.span_rows / kSaveRows;
-    return p;
-}
 Plan make_plan(const selective_scan_args_t& a)
 {
-    return make_plan(a.channels, a.states, a.groups, a.rows, a.seqs, a.seq_offsets);
+    return make_scan_plan(a.channels, a.states, a.groups, a.rows, a.seqs, a.seq_offsets);
 }
 
 size_t padded_states(uint32_t states) { return 4 * (size_t)states_per_lane(states); }
@@ -1561,7 +1486,7 @@ scan_status_t selective_scan_step(const selective_scan_step_args_t* args, void* 
                          range(a.delta_bias, (uint64_t)a.channels * 4),
                          range(a.slots, a.rows * 4)};
     if (any_overlap(outs, ins)) return SCAN_ERR_INVALID;
-    const Plan p = make_plan(a.channels, a.states, a.groups, a.rows, 1, nullptr);
+    const Plan p = make_scan_plan(a.channels, a.states, a.groups, a.rows, 1, nullptr);
     const uint64_t all = a.rows * (uint64_t)p.blocks;
     const bool four = all >= 4 * (uint64_t)kTargetWorkgroups;
     const uint64_t wgs = four ? (a.rows + 3) / 4 * p.blocks : all;

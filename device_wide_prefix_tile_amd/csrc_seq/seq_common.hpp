@@ -1,5 +1,5 @@
 // Shared pieces of the sequence operators: element types, 16-byte vectors of
-// them, activations, the sequences' row ranges, and host-side checks.
+// them, activations, and host-side checks.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -9,6 +9,7 @@
 #include <type_traits>
 
 #include "dwpt_seq.h"
+#include "seq_plan.hpp"
 
 namespace dwpt_seq {
 
@@ -117,56 +118,6 @@ __device__ __forceinline__ void wave_sync()
 }
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-
-// The sequences of a call: `len` rows each (offsets == nullptr), or the ranges between consecutive
-// offsets.  Offsets are clamped to 0 .. rows, so that no value of them leads outside the arrays.
-struct Sequences {
-    const int32_t* offsets;
-    uint32_t rows, count, len;
-
-    __device__ __forceinline__ uint32_t start(uint32_t s) const
-    {
-        if (!offsets) return s * len;
-        const int32_t o = offsets[s];
-        return o < 0 ? 0u : (uint32_t)o > rows ? rows : (uint32_t)o;
-    }
-    __device__ __forceinline__ uint32_t end(uint32_t s) const { return start(s + 1); }
-
-    // The sequence that row r belongs to: the last s with start(s) <= r; -1 if r lies before the
-    // first, count if behind the last.  (Of sequences that start at one row, all but the last are
-    // empty.)
-    __device__ __forceinline__ int find(uint32_t r) const
-    {
-        if (!offsets) return (int)(r / len);
-        uint32_t lo = 0, hi = count + 1;  // offsets [0, lo) are <= r, [hi, ..) are > r
-        while (lo < hi) {
-            const uint32_t mid = (lo + hi) >> 1;
-            if (start(mid) <= r)
-                lo = mid + 1;
-            else
-                hi = mid;
-        }
-        return (int)lo - 1;
-    }
-
-    // Moves (s, pos) to the first row at or behind pos that belongs to a sequence, whose range is
-    // then [st, en); false if there is none below `limit`.  s: find(pos), or an earlier sequence.
-    __device__ __forceinline__ bool seek(int& s, uint32_t& pos, uint32_t limit, uint32_t& st, uint32_t& en) const
-    {
-        if (s < 0) s = 0;
-        while (pos < limit && s < (int)count) {
-            st = start((uint32_t)s);
-            en = end((uint32_t)s);
-            if (en <= pos || en <= st) {
-                ++s;
-            } else {
-                if (pos < st) pos = st;
-                return pos < limit;
-            }
-        }
-        return false;
-    }
-};
 
 // ------------------------------------------------------------ host side
 inline bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }

@@ -1,0 +1,98 @@
+"""The sequence operators at their edges: offsets in any order, values that are not finite, rows and
+states that do not exist, sizes past a launch's limits.  Tolerances as in sequence_reference.py."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import device_wide_prefix_tile_amd as dw
+import sequence_reference as ref
+from device_wide_prefix_tile_amd import sequence as seq
+from sequence_reference import close, f64  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+T = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+
+
+def randn(rng, *shape, t=torch.float32, scale=1.0):
+    return (torch.from_numpy(rng.standard_normal(shape)) * scale).to(t).cuda()
+
+
+def offsets(lengths, first=0):
+    return torch.tensor(np.cumsum([first] + list(lengths)), dtype=torch.int32, device="cuda")
+
+
+def scan_inputs(rng, lead, d, n, g=1, t=torch.float32):
+    v = dict(x=randn(rng, *lead, d, t=t), delta=randn(rng, *lead, d, t=t), z=randn(rng, *lead, d, t=t),
+             B=randn(rng, *lead, g, n, t=t), C=randn(rng, *lead, g, n, t=t), D=randn(rng, d), delta_bias=randn(rng, d) - 2.0)
+    v["A"] = -torch.from_numpy(rng.uniform(0.2, 3.0, (d, n))).float().cuda()
+    return v
+
+
+def call_args(v):
+    return (v["x"], v["delta"], v["A"], v["B"], v["C"]), {k: v[k] for k in ("D", "z", "delta_bias") if v.get(k) is not None}
+
+
+class Bands:
+    """Memory with 64 KB of a known pattern on both sides of every piece."""
+    BAND = 1 << 16
+
+    def __init__(self):
+        self.all = []
+
+    def take(self, shape, dtype):
+        n = int(np.prod(shape)) * torch.empty(0, dtype=dtype).element_size()
+        size = (n + 255) // 256 * 256
+        raw = torch.full((size + 2 * self.BAND,), 0xA5, dtype=torch.uint8, device="cuda")
+        self.all.append((raw, n))
+        return raw[self.BAND:self.BAND + n].view(dtype).view(shape)
+
+    def check(self):
+        for raw, n in self.all:
+            assert (raw[:self.BAND] == 0xA5).all() and (raw[self.BAND + n:] == 0xA5).all()
+
+
+# ---------------------------------------------------------------------- offsets
+UNORDERED = [[0, 100, 50, 200], [0, 20, 10, 200], [200, 0, 200, 0, 130], [64, 32, 128, 0, 200], [-5, 90, 400, 30, 200],
+             [-(1 << 31), (1 << 31) - 1, 3, (1 << 31) - 1], [199, 199, 7, 7, 1000], [0, 200, 0, 200, 0]]
+
+
+@pytest.mark.parametrize("off", UNORDERED)
+@pytest.mark.parametrize("d", [16, 200])
+def test_offsets_in_any_order_stay_inside_the_arrays(off, d):
+    """Offsets that descend or lie outside the rows: results are unspecified, the bytes around every output,
+    saved state and workspace are not.  (tests/test_scan_walk_model.py has the same for the indices read.)"""
+    rng = np.random.default_rng(len(off) + d)
+    rows, n, k, seqs = 200, 16, 4, len(off) - 1
+    off = torch.tensor(off, dtype=torch.int32, device="cuda")
+    v = scan_inputs(rng, (rows,), d, n)
+    dy, init, dfin = randn(rng, rows, d), randn(rng, seqs, d, n), randn(rng, seqs, d, n)
+    good = offsets([70, 130])
+    args, kw = call_args(v)
+    before = dw.selective_scan(*args, delta_softplus=True, seq_offsets=good, **kw)
+    mem, L = Bands(), seq._lib()
+
+    def call(*shape, dtype=torch.float32):
+        return mem.take(shape, dtype).data_ptr()
+    a, _ = seq._scan_args(*args, v["D"], v["z"], v["delta_bias"], True, off, init)
+    a.y, a.y_stride, a.final_state = call(rows, d), d, call(seqs, d, n)
+    a.saved = call(L.selective_scan_saved(ctypes.byref(a)))
+    a.workspace_bytes = L.selective_scan_workspace(ctypes.byref(a))
+    a.workspace = call(a.workspace_bytes, dtype=torch.uint8)
+    stream = torch.cuda.current_stream().cuda_stream
+    assert L.selective_scan(ctypes.byref(a), stream) == 0
+    g = seq._ScanGradArgs(a, dy.data_ptr(), d, dfin.data_ptr(), call(rows, d), d, call(rows, d), d, call(rows, d), d,
+                          call(rows, n), n, call(rows, n), n, call(d, n), call(d), call(d), call(seqs, d, n))
+    g.args.workspace_bytes = L.selective_scan_grad_workspace(ctypes.byref(g))
+    g.args.workspace = call(g.args.workspace_bytes, dtype=torch.uint8)
+    assert L.selective_scan_grad(ctypes.byref(g), stream) == 0
+    w, b, cinit, cfin = randn(rng, d, k), randn(rng, d), randn(rng, seqs, k - 1, d), randn(rng, seqs, k - 1, d)
+    dw.causal_conv1d(v["x"], w, b, activation="silu", seq_offsets=off, initial_state=cinit,
+                     final_state=mem.take((seqs, k - 1, d), torch.float32), out=mem.take((rows, d), torch.float32))
+    dw.causal_conv1d_grad(dy, v["x"], w, b, activation="silu", seq_offsets=off, initial_state=cinit, dfinal_state=cfin,
+                          dx=mem.take((rows, d), torch.float32))
+    torch.cuda.synchronize()
+    mem.check()
+    assert torch.equal(dw.selective_scan(*args, delta_softplus=True, seq_offsets=good, **kw), before)
