@@ -789,12 +789,13 @@ __global__ __launch_bounds__(kGradWaves * 64) void grad_totals_kernel(Plan pl, I
 //
 // dB and dC are sums over channels, which lie across the lanes: the matrix unit adds them up.
 // v_mfma_f32_16x16x4_f32 multiplies a 16 x 4 matrix by a 4 x 16 one whose element (k, j) is in
-// lane 16 k + j; with a first matrix that is 1 in row t mod 16 and 0 elsewhere it adds, into row
-// t mod 16 of the accumulator, the four 16-lane rows of any register.  So the 16 rows of the tile
-// collect in one accumulator per state, at one instruction per row and state (a lane's channels
-// are added up before) and none on the vector units; what is left is a sum over the 4 channels of a
-// lane row, once a tile.  The wavefronts of a workgroup add theirs in LDS, the workgroups theirs in
-// a second launch, always in the same order.
+// lane 16 k + j; with a first matrix of ones it leaves the sum of any register's four 16-lane rows in
+// every row of the result, and the lane row that keeps tile row t takes it.  That is one matrix
+// instruction and one selection per row and state (a lane's channels are added up before); what is
+// left is a sum over the 4 channels of a lane row, once a tile.  (A first matrix that is 1 in one row
+// and 0 elsewhere would need no selection, but 0 times a value that is not finite would reach the
+// tile's other rows; 1114 against 1126 us.)  The wavefronts of a workgroup add theirs in LDS, the
+// workgroups theirs in a second launch, always in the same order.
 template <int S>
 struct Bwd {
     static constexpr int CW = S == 4 ? 32 : 16, WAVES = kWgChannels / CW;
@@ -951,6 +952,7 @@ __global__ __launch_bounds__(Bwd<S>::WAVES * 64) __attribute__((amdgpu_waves_per
                     }
                 }
                 float ch[CH][kSub], sd[CH][kSub], sx[CH][kSub];  // the lane's sums of C h, A g h, dh B
+                const bool mine = (me.lane >> 4) == k;           // the lane row that keeps these kSub rows' dB and dC
 #pragma unroll
                 for (int u = kSub - 1; u >= 0; --u) {
                     const int t = k * kSub + u;
@@ -976,11 +978,12 @@ __global__ __launch_bounds__(Bwd<S>::WAVES * 64) __attribute__((amdgpu_waves_per
                             sd[c][u] = i ? fmaf(A2.v[c][i], through, sd[c][u]) : A2.v[c][i] * through;
                         }
                     }
-                    const float select = (me.lane & 15) == (t & 15) ? 1.0f : 0.0f;
 #pragma unroll
                     for (int i = 0; i < S; ++i) {
-                        accC[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(select, pc_[i], accC[i], 0, 0, 0);
-                        accB[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(select, pb_[i], accB[i], 0, 0, 0);
+                        const f32x4 c4 = __builtin_amdgcn_mfma_f32_16x16x4f32(1.0f, pc_[i], f32x4{}, 0, 0, 0);
+                        const f32x4 b4 = __builtin_amdgcn_mfma_f32_16x16x4f32(1.0f, pb_[i], f32x4{}, 0, 0, 0);
+                        accC[i][u] = mine ? c4[0] : accC[i][u];
+                        accB[i][u] = mine ? b4[0] : accB[i][u];
                     }
                 }
                 // every lane of the quad has read the rows' values: lane q writes row q's sums over them

@@ -96,3 +96,54 @@ def test_offsets_in_any_order_stay_inside_the_arrays(off, d):
     torch.cuda.synchronize()
     mem.check()
     assert torch.equal(dw.selective_scan(*args, delta_softplus=True, seq_offsets=good, **kw), before)
+
+
+# ---------------------------------------------------------------------- values that are not finite
+def scan_values(v, lengths, dy=None, initial=None, dfinal=None, sp=True):
+    """{name: value} of the formulas in 64 bits, infinities and NaN included."""
+    d, (g, n) = v["x"].shape[-1], v["B"].shape[-2:]
+    ends = np.cumsum([0] + list(lengths))
+    with np.errstate(all="ignore"):
+        r = ref.scan(f64(v["x"]), f64(v["delta"]), f64(v["A"]), f64(v["B"]), f64(v["C"]), f64(v.get("D")), f64(v.get("z")),
+                     f64(v.get("delta_bias")), sp, list(zip(ends[:-1], ends[1:])), f64(initial), None if dy is None else f64(dy), f64(dfinal))
+    return {k: q[0] for k, q in r.items()}
+
+
+def run_scan(v, lengths, dy, sp=True, **kw):
+    a, more = call_args(v)
+    kw.update(more, delta_softplus=sp, seq_offsets=offsets(lengths))
+    y, fin = dw.selective_scan(*a, final_state=True, **kw)
+    g = dw.selective_scan_grad(dy, *a, **kw)
+    out = {k: q for k, q in g._asdict().items() if q is not None}
+    if "dinitial_state" in out:
+        out["dinitial"] = out.pop("dinitial_state")
+    return dict(out, y=y, final=fin)
+
+
+def same_where_finite(got, clean, want, want_clean, what):
+    """Finite exactly where the formulas are, and the same bits as without the value wherever the formulas
+    give the same (an infinite step forgets the state: what was passed back to it changes, and is finite)."""
+    for name, q in got.items():
+        finite = torch.from_numpy(np.isfinite(want[name])).view(q.shape)
+        assert torch.equal(torch.isfinite(q).cpu(), finite), "%s %s: finite elsewhere" % (what, name)
+        still = torch.from_numpy(want[name] == want_clean[name]).view(q.shape)
+        assert torch.equal(q.cpu()[still], clean[name].cpu()[still]), "%s %s: other values changed" % (what, name)
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("where", ["x", "delta", "z", "dy"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("n", [16, 32, 64])
+def test_scan_gradients_keep_a_row_to_itself(t, where, value, n):
+    """One value that is not finite reaches what the formulas let it reach: of dB and dC, the rows of
+    its own term alone, not their neighbours."""
+    rng = np.random.default_rng(60 + n)
+    lengths, d, t0, c0 = [40, 20], 48, 21, 37
+    v = scan_inputs(rng, (60,), d, n, 1, T[t])
+    dy = randn(rng, 60, d, t=T[t])
+    clean, want_clean = run_scan(v, lengths, dy), scan_values(v, lengths, dy)
+    (dy if where == "dy" else v[where])[t0, c0] = value
+    want = scan_values(v, lengths, dy)
+    if where in ("x", "dy"):
+        assert np.isfinite(want["dB" if where == "x" else "dC"]).all((1, 2)).sum() == 59  # one row of 60
+    same_where_finite(run_scan(v, lengths, dy), clean, want, want_clean, "%s %s" % (where, value))
