@@ -204,6 +204,13 @@ struct Place {
     {
         return QUADS ? q * S + i : (i / 4) * 16 + 4 * q + i % 4;
     }
+    // Whether the lane's state i exists.  A state of the padding has A = B = C = 0, but 0 times an
+    // infinite dt x is NaN: sums over the states leave it out.
+    template <int S>
+    __device__ __forceinline__ bool real(int i, uint32_t states) const
+    {
+        return state<S>(i) < states;
+    }
     int lane, w, d, q;                  // channel and quarter of the lane
     uint32_t group, c0;                 // first channel of the wavefront
     int nch;                            // channels of the wavefront (0: none)
@@ -519,7 +526,8 @@ __global__ __launch_bounds__(kFwdWaves * 64) __attribute__((amdgpu_waves_per_eu(
                         for (int i = 0; i < S; ++i) {
                             float& hi = h.v[c][i];
                             hi = fmaf(exp2_fast(v * A2.v[c][i]), hi, p[c][i / 4][4 * u + i % 4]);
-                            if (!TOTALS) y_ = i ? fmaf(w.c[u][i / 4][i % 4], hi, y_) : w.c[u][0][0] * hi;
+                            const float ht = VEC || me.template real<S>(i, pl.states) ? hi : 0.0f;
+                            if (!TOTALS) y_ = i ? fmaf(w.c[u][i / 4][i % 4], ht, y_) : w.c[u][0][0] * ht;
                         }
                         part[c][u] = y_;
                     }
@@ -649,7 +657,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void scan_step_kernel(Plan pl, Inp
 #pragma unroll
         for (int i = 0; i < S; ++i) {
             h[u][i] = fmaf(exp2_fast(dt * (a[i] * kLog2e)), h[u][i], dx * (float)b[u].v[i]);
-            sum = fmaf((float)cc[u].v[i], h[u][i], sum);
+            if (VEC || first + i < pl.states) sum = fmaf((float)cc[u].v[i], h[u][i], sum);
         }
         if (VEC) {
 #pragma unroll
@@ -973,9 +981,11 @@ __global__ __launch_bounds__(Bwd<S>::WAVES * 64) __attribute__((amdgpu_waves_per
                             g.v[c][i] = a[u][c][i] * dh;
                             const float through = g.v[c][i] * hs[u][c][i];
                             dA.v[c][i] = fmaf(v[0], through, dA.v[c][i]);
-                            ch[c][u] = i ? fmaf(cc[i], ht, ch[c][u]) : cc[i] * ht;
-                            sx[c][u] = i ? fmaf(dh, b[i], sx[c][u]) : dh * b[i];
-                            sd[c][u] = i ? fmaf(A2.v[c][i], through, sd[c][u]) : A2.v[c][i] * through;
+                            const bool real = VEC || me.template real<S>(i, pl.states);
+                            const float hr = real ? ht : 0.0f, dr = real ? dh : 0.0f, tr = real ? through : 0.0f;
+                            ch[c][u] = i ? fmaf(cc[i], hr, ch[c][u]) : cc[i] * hr;
+                            sx[c][u] = i ? fmaf(dr, b[i], sx[c][u]) : dr * b[i];
+                            sd[c][u] = i ? fmaf(A2.v[c][i], tr, sd[c][u]) : A2.v[c][i] * tr;
                         }
                     }
 #pragma unroll

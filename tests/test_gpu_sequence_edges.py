@@ -147,3 +147,44 @@ def test_scan_gradients_keep_a_row_to_itself(t, where, value, n):
     if where in ("x", "dy"):
         assert np.isfinite(want["dB" if where == "x" else "dC"]).all((1, 2)).sum() == 59  # one row of 60
     same_where_finite(run_scan(v, lengths, dy), clean, want, want_clean, "%s %s" % (where, value))
+
+
+def positive(v):
+    """Every term of one sign, so that an infinity stays one: no difference of infinities but the formulas' own."""
+    return {k: (q if k == "A" or q is None else q.abs()) for k, q in v.items()}
+
+
+def same_kind(got, want, what):
+    """Infinite, not a number or finite exactly where the formulas are."""
+    for name, q in got.items():
+        w = torch.from_numpy(np.asarray(want[name])).view(q.shape)
+        q = q.double().cpu()
+        for kind in (torch.isnan, torch.isposinf, torch.isneginf):
+            assert torch.equal(kind(q), kind(w)), "%s %s %s" % (what, name, kind.__name__)
+
+
+@pytest.mark.parametrize("n", [1, 5, 13, 16, 24, 40, 64])
+@pytest.mark.parametrize("where", ["x", "delta", "dy"])
+def test_infinities_do_not_meet_the_padding_of_the_states(where, n):
+    """An infinite input gives the same with 13 states as with 16: states are padded to 16, 32 or 64 with
+    zeros, and zero times infinity is no zero."""
+    rng = np.random.default_rng(70 + n)
+    lengths, d, t0, c0 = [40, 20], 24, 21, 11
+    v = positive(scan_inputs(rng, (60,), d, n))
+    dy = randn(rng, 60, d).abs()
+    (dy if where == "dy" else v[where])[t0, c0] = float("inf")
+    same_kind(run_scan(v, lengths, dy), scan_values(v, lengths, dy), where)
+
+
+@pytest.mark.parametrize("n", [1, 5, 16, 24, 40])
+@pytest.mark.parametrize("rows", [3, 2051])
+def test_step_infinities_do_not_meet_the_padding_of_the_states(rows, n):
+    rng = np.random.default_rng(80 + n)
+    d = 130
+    v = positive(scan_inputs(rng, (rows,), d, n))
+    v["x"][1, 7] = float("inf")
+    state = torch.zeros(rows, d, n, device="cuda")
+    a, kw = call_args(v)
+    y = dw.selective_scan_step(*a, state, delta_softplus=True, **kw)
+    want = scan_values(v, [1] * rows)
+    same_kind(dict(y=y, final=state), want, "step")
