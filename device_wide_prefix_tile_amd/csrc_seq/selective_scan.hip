@@ -1081,7 +1081,8 @@ __global__ __launch_bounds__(Bwd<S>::WAVES * 64) __attribute__((amdgpu_waves_per
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     const f32x2 q = dt[at + j];
-                    ox[j] = fmaf(yf[j], sf[j], vf[j] * q[1]);
+                    ox[j] = vf[j] * q[1];
+                    if (in.D) ox[j] = fmaf(yf[j], sf[j], ox[j]);  // as in the forward pass: without D no term
                     od[j] = fmaf(xf[j], q[1], q[0]);
                     dskip[j] = fmaf(yf[j], xf[j], dskip[j]);
                 }

@@ -188,3 +188,20 @@ def test_step_infinities_do_not_meet_the_padding_of_the_states(rows, n):
     y = dw.selective_scan_step(*a, state, delta_softplus=True, **kw)
     want = scan_values(v, [1] * rows)
     same_kind(dict(y=y, final=state), want, "step")
+
+
+@pytest.mark.parametrize("n", [1, 16])
+@pytest.mark.parametrize("with_z", [True, False])
+def test_infinite_gradient_without_skip(n, with_z):
+    """Without D dx has no term of it, as y has none: 0 times an infinite dy is not zero."""
+    rng = np.random.default_rng(90 + n)
+    lengths, d = [40, 20], 40
+    v = positive(scan_inputs(rng, (60,), d, n))
+    v["D"] = None
+    if not with_z:
+        v["z"] = None
+    dy = randn(rng, 60, d).abs()
+    dy[21, 5] = float("inf")
+    got, want = run_scan(v, lengths, dy), scan_values(v, lengths, dy)
+    assert np.isposinf(want["dx"][21, 5])
+    same_kind(got, {k: want[k] for k in got}, "no D")
