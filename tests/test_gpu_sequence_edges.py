@@ -100,12 +100,14 @@ def test_offsets_in_any_order_stay_inside_the_arrays(off, d):
 
 # ---------------------------------------------------------------------- values that are not finite
 def scan_values(v, lengths, dy=None, initial=None, dfinal=None, sp=True):
-    """{name: value} of the formulas in 64 bits, infinities and NaN included."""
+    """{name: value} of the formulas in 64 bits, infinities and NaN included.  The reference multiplies by a
+    zero D where there is none; 2^-1000 changes no finite value and keeps infinities what they are."""
     d, (g, n) = v["x"].shape[-1], v["B"].shape[-2:]
     ends = np.cumsum([0] + list(lengths))
     with np.errstate(all="ignore"):
-        r = ref.scan(f64(v["x"]), f64(v["delta"]), f64(v["A"]), f64(v["B"]), f64(v["C"]), f64(v.get("D")), f64(v.get("z")),
-                     f64(v.get("delta_bias")), sp, list(zip(ends[:-1], ends[1:])), f64(initial), None if dy is None else f64(dy), f64(dfinal))
+        r = ref.scan(f64(v["x"]), f64(v["delta"]), f64(v["A"]), f64(v["B"]), f64(v["C"]),
+                     np.full(d, 2.0 ** -1000) if v.get("D") is None else f64(v["D"]), f64(v.get("z")), f64(v.get("delta_bias")), sp,
+                     list(zip(ends[:-1], ends[1:])), f64(initial), None if dy is None else f64(dy), f64(dfinal))
     return {k: q[0] for k, q in r.items()}
 
 
