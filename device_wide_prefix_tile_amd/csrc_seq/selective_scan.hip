@@ -964,6 +964,9 @@ __global__ __launch_bounds__(Bwd<S>::WAVES * 64) __attribute__((amdgpu_waves_per
 #pragma unroll
                 for (int u = kSub - 1; u >= 0; --u) {
                     const int t = k * kSub + u;
+#pragma unroll
+                    for (int c = 0; c < CH; ++c) ch[c][u] = sd[c][u] = sx[c][u] = 0.0f;
+                    if (u && t >= len) continue;  // a row behind the tile: 0 times an infinite state is no zero
                     float b[S], cc[S], pb_[S], pc_[S];
                     read_floats<S>(s_b + t * NP + me.q * S, b);
                     read_floats<S>(s_c + t * NP + me.q * S, cc);
@@ -971,7 +974,6 @@ __global__ __launch_bounds__(Bwd<S>::WAVES * 64) __attribute__((amdgpu_waves_per
                     for (int c = 0; c < CH; ++c) {
                         const f32x2 v = dt[t * CW + me.d + 16 * c];
                         const float dv = ldv[t * CW + me.d + 16 * c];
-                        ch[c][u] = sd[c][u] = sx[c][u] = 0.0f;
 #pragma unroll
                         for (int i = 0; i < S; ++i) {
                             const float ht = hs[u + 1][c][i];

@@ -207,3 +207,25 @@ def test_infinite_gradient_without_skip(n, with_z):
     got, want = run_scan(v, lengths, dy), scan_values(v, lengths, dy)
     assert np.isposinf(want["dx"][21, 5])
     same_kind(got, {k: want[k] for k in got}, "no D")
+
+
+@pytest.mark.parametrize("n", [1, 16, 24, 64])
+@pytest.mark.parametrize("where", ["x", "dfinal"])
+def test_infinities_do_not_meet_the_rows_behind_a_sequence(where, n):
+    """A sequence that ends inside four rows: the rows behind it take no part, so an infinite state at its
+    last row does not reach dA, which has no term of that state."""
+    rng = np.random.default_rng(100 + n)
+    lengths, d = [22, 5, 35], 40
+    v = positive(scan_inputs(rng, (62,), d, n))
+    dy, dfin = randn(rng, 62, d).abs(), randn(rng, 3, d, n).abs()
+    if where == "x":
+        v["x"][21, 5] = v["x"][26, 30] = float("inf")
+    else:
+        dfin[0, 5], dfin[1, 30] = float("inf"), float("inf")
+    a, kw = call_args(v)
+    kw.update(delta_softplus=True, seq_offsets=offsets(lengths))
+    g = {k: q for k, q in dw.selective_scan_grad(dy, *a, dfinal_state=dfin, **kw)._asdict().items() if q is not None}
+    want = scan_values(v, lengths, dy, dfinal=dfin)
+    if where == "x":
+        assert np.isfinite(want["dA"]).all()
+    same_kind(g, {k: want[k] for k in g}, where)
