@@ -28,6 +28,8 @@
 //
 // Packed sequences are segments: a wavefront walks them one after another,
 // starting each from its initial state.
+#include <cfloat>
+
 #include "seq_common.hpp"
 
 namespace dwpt_seq {
@@ -241,7 +243,7 @@ struct LaneStates {
             for (int i = 0; i < S; ++i) v[c][i] = 0.0f;
     }
     // from and to an array (channels x states); zeros where padded
-    __device__ __forceinline__ void load(const float* __restrict__ p, const Plan& pl, const Me& me, float scale = 1.0f)
+    __device__ __forceinline__ void load(const float* __restrict__ p, const Plan& pl, const Me& me)
     {
 #pragma unroll
         for (int c = 0; c < CH; ++c)
@@ -249,7 +251,20 @@ struct LaneStates {
             for (int i = 0; i < S; ++i) {
                 const uint32_t n = me.template state<S>(i);
                 const int ch = me.d + 16 * c;
-                v[c][i] = ch < me.nch && n < pl.states ? p[(size_t)(me.c0 + ch) * pl.states + n] * scale : 0.0f;
+                v[c][i] = ch < me.nch && n < pl.states ? p[(size_t)(me.c0 + ch) * pl.states + n] : 0.0f;
+            }
+    }
+    // A / ln 2, whose product with dt is the power of two.  A rate of minus infinity forgets at once, as
+    // the lowest finite one does, which times the zero step of a row behind a tile is zero and not NaN.
+    __device__ __forceinline__ void load_rates(const float* __restrict__ A, const Plan& pl, const Me& me)
+    {
+        load(A, pl, me);
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int i = 0; i < S; ++i) {
+                const float r = v[c][i] * kLog2e;
+                v[c][i] = r < -FLT_MAX ? -FLT_MAX : r > FLT_MAX ? FLT_MAX : r;
             }
     }
     __device__ __forceinline__ void store(float* __restrict__ p, const Plan& pl, const Me& me) const
@@ -412,7 +427,7 @@ __global__ __launch_bounds__(kFwdWaves * 64) __attribute__((amdgpu_waves_per_eu(
         s_par[me.w][me.lane] = p && c < me.nch ? p[me.c0 + c] : 0.0f;
     }
     LaneStates<S, CH, false> A2, h;
-    A2.load(in.A, pl, me, kLog2e);
+    A2.load_rates(in.A, pl, me);
     const uint32_t bc_at = me.group * pl.states;
 
     uint32_t pos = r0, st, en;
@@ -718,7 +733,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void grad_totals_kernel(Plan pl, I
     f32x2* const dt = s_dt[me.w];
     float* const lc = s_c[me.w];
     LaneStates<S, 1, true> A2, g;
-    A2.load(in.A, pl, me, kLog2e);
+    A2.load_rates(in.A, pl, me);
     float bias[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -840,7 +855,7 @@ __global__ __launch_bounds__(Bwd<S>::WAVES * 64) __attribute__((amdgpu_waves_per
         s_par[me.w][me.lane] = p && c < me.nch ? p[me.c0 + c] : 0.0f;
     }
     LaneStates<S, CH, true> A2, g, h, dA;
-    A2.load(in.A, pl, me, kLog2e);
+    A2.load_rates(in.A, pl, me);
     dA.zero();
     float dskip[V] = {}, dbias[V] = {};
     const uint32_t bc_at = me.group * pl.states;

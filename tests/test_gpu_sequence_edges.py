@@ -229,3 +229,25 @@ def test_infinities_do_not_meet_the_rows_behind_a_sequence(where, n):
     if where == "x":
         assert np.isfinite(want["dA"]).all()
     same_kind(g, {k: want[k] for k in g}, where)
+
+
+@pytest.mark.parametrize("n", [3, 16, 40])
+def test_rate_of_minus_infinity_forgets(n):
+    """A = -inf gives the factor 0, as any rate does whose exponential underflows: also where a tile ends
+    inside a sequence, whose remaining rows have a step of zero."""
+    rng = np.random.default_rng(110 + n)
+    lengths, d = [22, 5, 135], 40
+    v = scan_inputs(rng, (162,), d, n)
+    init = randn(rng, 3, d, n)
+    got = []
+    for rate in (-float("inf"), -1e30):
+        v["A"][7, 0] = v["A"][33, n - 1] = rate
+        a, kw = call_args(v)
+        kw.update(delta_softplus=True, seq_offsets=offsets(lengths), initial_state=init)
+        y, fin = dw.selective_scan(*a, final_state=True, **kw)
+        state = init.clone()
+        step = dw.selective_scan_step(*[q[:3] if q.shape[0] == 162 else q for q in a], state, D=v["D"], z=v["z"][:3],
+                                      delta_bias=v["delta_bias"], delta_softplus=True)
+        got.append((y, fin, step, state))
+    for p, q in zip(*got):
+        assert torch.isfinite(p).all() and torch.equal(p, q)
