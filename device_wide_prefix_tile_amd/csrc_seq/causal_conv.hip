@@ -35,7 +35,8 @@ uint32_t channel_lanes(uint32_t nvec)
 struct Shape {
     Sequences seqs;
     uint32_t channels, nvec, cl, row_blocks, rows_per_block, groups;  // groups: row blocks per workgroup
-    uint32_t nx, ny;  // workgroups along the channels (neighbours in the launch) and along the rows
+    uint32_t nx, ny;      // workgroups along the channels (neighbours in the launch) and along the rows
+    uint32_t workgroups;  // of the launch, those of the states included
 };
 
 template <typename T>
@@ -109,7 +110,9 @@ template <typename T, typename W, int K, int V, int ACT>
 __global__ __launch_bounds__(kBlock) void conv_kernel(Shape sh, Conv<T> a, const W* __restrict__ weight,
                                                       const W* __restrict__ bias)
 {
-    const uint32_t bx = blockIdx.x % sh.nx, by = blockIdx.x / sh.nx;
+    const uint32_t wg = workgroup();
+    if (wg >= sh.workgroups) return;
+    const uint32_t bx = wg % sh.nx, by = wg / sh.nx;
     const uint32_t cv = bx * sh.cl + threadIdx.x % sh.cl;
     const uint32_t rb = by * sh.groups + threadIdx.x / sh.cl;
     if (cv >= sh.nvec) return;
@@ -186,8 +189,10 @@ __global__ __launch_bounds__(kBlock) void conv_grad_kernel(Shape sh, Conv<T> a, 
                                                            const W* __restrict__ weight, const W* __restrict__ bias)
 {
     extern __shared__ float s_sum[];  // [groups][K + 1][cl * V]
+    const uint32_t wg = workgroup();
+    if (wg >= sh.workgroups) return;
     const uint32_t lane_c = threadIdx.x % sh.cl, group = threadIdx.x / sh.cl;
-    const uint32_t bx = blockIdx.x % sh.nx, by = blockIdx.x / sh.nx;
+    const uint32_t bx = wg % sh.nx, by = wg / sh.nx;
     const uint32_t cv = bx * sh.cl + lane_c;
     const uint32_t c = cv * V;
     const bool active = cv < sh.nvec;
@@ -492,14 +497,15 @@ scan_status_t forward(const causal_conv1d_args_t& a, hipStream_t s)
         using T = decltype(te);
         using W = decltype(we);
         constexpr int K = decltype(ke)::value, V = kPack;
-        const Shape sh = make_shape(a, vec ? V : 1, false);
+        Shape sh = make_shape(a, vec ? V : 1, false);
         const Conv<T> p{static_cast<const T*>(a.x), a.x_stride, static_cast<const T*>(a.initial_state), static_cast<T*>(a.y),
                         a.y_stride, static_cast<T*>(a.final_state)};
         const W *w = static_cast<const W*>(a.weight), *b = static_cast<const W*>(a.bias);
         const uint64_t wgs = sh.nx * ((uint64_t)sh.ny + (a.final_state ? (sh.seqs.count + sh.groups - 1) / sh.groups : 0u));
         if (wgs == 0) return SCAN_OK;
-        if (wgs > 0x7FFFFFFFu) return SCAN_ERR_INVALID;
-        const dim3 grid((unsigned)wgs);
+        if (wgs > kMostInGrid) return SCAN_ERR_INVALID;
+        sh.workgroups = (uint32_t)wgs;
+        const dim3 grid = grid_of(wgs);
         const bool act = a.activation == SEQ_ACT_SILU;
         auto k = vec ? (act ? conv_kernel<T, W, K, V, SEQ_ACT_SILU> : conv_kernel<T, W, K, V, SEQ_ACT_NONE>)
                      : (act ? conv_kernel<T, W, K, 1, SEQ_ACT_SILU> : conv_kernel<T, W, K, 1, SEQ_ACT_NONE>);
@@ -517,16 +523,17 @@ scan_status_t gradient(const causal_conv1d_grad_args_t& g, hipStream_t s)
         using W = decltype(we);
         constexpr int K = decltype(ke)::value, V = kPack;
         const int v = vec ? V : 1;
-        const Shape sh = make_shape(a, v, true);
+        Shape sh = make_shape(a, v, true);
         const Conv<T> p{static_cast<const T*>(a.x), a.x_stride, static_cast<const T*>(a.initial_state), nullptr, 0, nullptr};
         const ConvGrad<T> q{static_cast<const T*>(g.dy), g.dy_stride,   static_cast<const T*>(g.dfinal_state),
                             static_cast<T*>(g.dx),       g.dx_stride,   static_cast<T*>(g.dinitial_state),
                             static_cast<float*>(g.workspace)};
         const W *w = static_cast<const W*>(a.weight), *b = static_cast<const W*>(a.bias);
         const uint64_t wgs = sh.nx * ((uint64_t)sh.ny + (g.dinitial_state ? (sh.seqs.count + sh.groups - 1) / sh.groups : 0u));
-        if (wgs > 0x7FFFFFFFu) return SCAN_ERR_INVALID;
+        if (wgs > kMostInGrid) return SCAN_ERR_INVALID;
         if (wgs) {
-            const dim3 grid((unsigned)wgs);
+            sh.workgroups = (uint32_t)wgs;
+            const dim3 grid = grid_of(wgs);
             const bool act = a.activation == SEQ_ACT_SILU;
             auto k = vec ? (act ? conv_grad_kernel<T, W, K, V, SEQ_ACT_SILU> : conv_grad_kernel<T, W, K, V, SEQ_ACT_NONE>)
                          : (act ? conv_grad_kernel<T, W, K, 1, SEQ_ACT_SILU> : conv_grad_kernel<T, W, K, 1, SEQ_ACT_NONE>);

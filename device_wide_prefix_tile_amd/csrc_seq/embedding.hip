@@ -373,6 +373,7 @@ __device__ __forceinline__ void store_row(O* __restrict__ dtable, uint32_t chann
 struct Sums {
     GroupPlan plan;
     uint32_t channels, columns, windows;  // columns: workgroups (of 256 * V columns) per window
+    uint32_t workgroups;                  // of sums_kernel
     int64_t stride;
     const uint32_t *order, *start, *count, *grouped;
     float* pieces;
@@ -384,9 +385,11 @@ template <typename T, typename O, typename I, int V>
 __global__ __launch_bounds__(256) void sums_kernel(Sums a, const I* __restrict__ tokens, const T* __restrict__ dout,
                                                    O* __restrict__ dtable)
 {
-    if (blockIdx.x < a.windows * a.columns) {
-        const uint32_t x = blockIdx.x / a.columns;
-        const uint32_t c = (blockIdx.x % a.columns * 256 + threadIdx.x) * V;
+    const uint32_t wg = workgroup();
+    if (wg >= a.workgroups) return;
+    if (wg < a.windows * a.columns) {
+        const uint32_t x = wg / a.columns;
+        const uint32_t c = (wg % a.columns * 256 + threadIdx.x) * V;
         // places behind the last grouped position (tokens outside the table have none) hold nothing
         const uint32_t lo = x * kPiece;
         const uint32_t grouped = *a.grouped;
@@ -406,7 +409,7 @@ __global__ __launch_bounds__(256) void sums_kernel(Sums a, const I* __restrict__
         return;
     }
     const uint32_t chunks = (a.channels + 64 * V - 1) / (64 * V);
-    const uint32_t unit = (blockIdx.x - a.windows * a.columns) * 4 + (uint32_t)uniform((int)(threadIdx.x >> 6));
+    const uint32_t unit = (wg - a.windows * a.columns) * 4 + (uint32_t)uniform((int)(threadIdx.x >> 6));
     const uint32_t first = unit / chunks * kRows;
     const uint32_t c = (unit % chunks * 64 + (threadIdx.x & 63)) * V;
     const uint32_t slots = a.plan.buckets * a.plan.per;  // rows in the order of start and count
@@ -437,8 +440,10 @@ __global__ __launch_bounds__(256) void sums_kernel(Sums a, const I* __restrict__
 template <typename T, typename O, typename I, int V>
 __global__ __launch_bounds__(256) void join_kernel(Sums a, const I* __restrict__ tokens, O* __restrict__ dtable)
 {
-    const uint32_t x = blockIdx.x / a.columns;
-    const uint32_t c = (blockIdx.x % a.columns * 256 + threadIdx.x) * V;
+    const uint32_t wg = workgroup();
+    if (wg >= a.windows * a.columns) return;
+    const uint32_t x = wg / a.columns;
+    const uint32_t c = (wg % a.columns * 256 + threadIdx.x) * V;
     const uint32_t lo = x * kPiece, grouped = *a.grouped;
     if (lo >= grouped || c >= a.channels) return;
     // it reaches the end of the window, for it is longer than one
@@ -475,7 +480,7 @@ __global__ __launch_bounds__(256) void lookup_kernel(const I* __restrict__ token
                                                      const T* __restrict__ table, int64_t stride, uint32_t v,
                                                      uint32_t channels, float scale, T* __restrict__ out)
 {
-    const uint32_t i = blockIdx.x * 4 + (threadIdx.x >> 6);
+    const uint32_t i = (blockIdx.z * kGridWidth + blockIdx.x) * 4 + (threadIdx.x >> 6);
     if (i >= n) return;
     const uint32_t r = (uint32_t)uniform((int)table_row(tokens, i, v));
     const uint32_t c0 = (blockIdx.y * 256 + (threadIdx.x & 63)) * V;
@@ -529,7 +534,7 @@ scan_status_t run_lookup(const I* tokens, size_t n, const T* table, int64_t stri
 {
     with_pack<T>(channels, stride, {{table, sizeof(T)}, {out, sizeof(T)}}, [&](auto pack) {
         constexpr int V = decltype(pack)::value;
-        const dim3 grid((unsigned)((n + 3) / 4), (channels + 256 * V - 1) / (256 * V));
+        const dim3 rows = grid_of((n + 3) / 4), grid(rows.x, (channels + 256 * V - 1) / (256 * V), rows.y);
         hipLaunchKernelGGL((lookup_kernel<T, I, V>), grid, dim3(256), 0, s, tokens, (uint32_t)n, table, stride, (uint32_t)v,
                            channels, scale, out);
     });
@@ -553,18 +558,23 @@ void run_group(const I* tokens, const GroupPlan& p, const GroupSpace& w, hipStre
                        w.start, w.count, w.grouped, w.seg_counts, w.totals);
 }
 
+// The grouping, the sums and the join.
 template <typename T, typename O, int V, typename I>
-void run_sums(const I* tokens, const GroupPlan& p, const GroupSpace& w, const T* dout, int64_t stride,
-              uint32_t channels, float scale, int accumulate, O* dtable, hipStream_t s)
+scan_status_t run_sums(const I* tokens, const GroupPlan& p, const GroupSpace& w, const T* dout, int64_t stride,
+                       uint32_t channels, float scale, int accumulate, O* dtable, hipStream_t s)
 {
     const uint32_t columns = (channels + 256 * V - 1) / (256 * V), chunks = (channels + 64 * V - 1) / (64 * V);
     const uint32_t windows = p.n > kPiece ? (p.n + kPiece - 1) / kPiece : 0;  // else no row is that long
-    const Sums a{p, channels, columns, windows, stride, w.order, w.start, w.count, w.grouped, w.pieces, scale, accumulate};
     const uint64_t units = ((uint64_t)p.buckets * p.per + kRows - 1) / kRows * chunks;
-    hipLaunchKernelGGL((sums_kernel<T, O, I, V>), dim3((unsigned)(windows * columns + (units + 3) / 4)), dim3(256), 0, s, a,
-                       tokens, dout, dtable);
+    const uint64_t workgroups = (uint64_t)windows * columns + (units + 3) / 4;
+    if (workgroups > kMostInGrid / 4) return SCAN_ERR_INVALID;  // the kernel counts wavefronts
+    run_group(tokens, p, w, s);
+    const Sums a{p,       channels, columns, windows,   (uint32_t)workgroups, stride, w.order,
+                 w.start, w.count,  w.grouped, w.pieces, scale,                accumulate};
+    hipLaunchKernelGGL((sums_kernel<T, O, I, V>), grid_of(workgroups), dim3(256), 0, s, a, tokens, dout, dtable);
     if (windows)
-        hipLaunchKernelGGL((join_kernel<T, O, I, V>), dim3(windows * columns), dim3(256), 0, s, a, tokens, dtable);
+        hipLaunchKernelGGL((join_kernel<T, O, I, V>), grid_of((uint64_t)windows * columns), dim3(256), 0, s, a, tokens, dtable);
+    return launched();
 }
 
 template <typename T, typename O, typename I>
@@ -573,11 +583,11 @@ scan_status_t run_grad(const I* tokens, size_t n, const T* dout, int64_t stride,
 {
     const GroupPlan p = make_plan(n, v);
     const GroupSpace w = lay_out(p, channels, workspace);
-    run_group(tokens, p, w, s);
+    scan_status_t st = SCAN_OK;
     with_pack<T>(channels, stride, {{dout, sizeof(T)}, {dtable, sizeof(O)}}, [&](auto pack) {
-        run_sums<T, O, decltype(pack)::value>(tokens, p, w, dout, stride, channels, scale, accumulate, dtable, s);
+        st = run_sums<T, O, decltype(pack)::value>(tokens, p, w, dout, stride, channels, scale, accumulate, dtable, s);
     });
-    return launched();
+    return st;
 }
 
 bool valid_tokens(const void* tokens, int token_bytes, size_t n)

@@ -399,11 +399,12 @@ __global__ __launch_bounds__(kFwdWaves * 64) __attribute__((amdgpu_waves_per_eu(
     __shared__ __align__(16) float s_y[TOTALS ? 1 : WAVES][TOTALS ? 4 : TT * CW];
     __shared__ __align__(16) float s_par[WAVES][2 * CW];  // delta_bias and D of the wavefront's channels
 
-    const uint32_t block = blockIdx.x % pl.blocks, span = blockIdx.x / pl.blocks;
+    const uint32_t wg = workgroup(), block = wg % pl.blocks, span = wg / pl.blocks;
     const Place<CW, false> me(pl, block);
     if (me.nch == 0) return;
     if (span >= pl.spans) {
         // behind the spans: the final states of empty sequences
+        if (TOTALS || !final_state || span - pl.spans >= kEmptyStep) return;
         for (uint32_t s = span - pl.spans; s < pl.seqs.count; s += kEmptyStep) {
             if (pl.seqs.end(s) > pl.seqs.start(s)) continue;
             LaneStates<S, CH, false> h;
@@ -616,7 +617,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void scan_step_kernel(Plan pl, Inp
                                                                     uint32_t n_slots, float* __restrict__ state,
                                                                     T* __restrict__ y, int64_t y_stride)
 {
-    const uint32_t block = blockIdx.x % pl.blocks, r0 = blockIdx.x / pl.blocks * R;
+    const uint32_t wg = workgroup(), block = wg % pl.blocks, r0 = wg / pl.blocks * R;
     const Place<16, true> me(pl, block);
     if (me.d >= me.nch) return;
     const uint32_t c = me.c0 + me.d, first = me.q * S;
@@ -721,9 +722,9 @@ __global__ __launch_bounds__(kGradWaves * 64) void grad_totals_kernel(Plan pl, I
     __shared__ __align__(16) f32x2 s_dt[kGradWaves][TT * 16];
     __shared__ __align__(16) float s_c[kGradWaves][TT * NP];
 
-    const uint32_t block = blockIdx.x % pl.blocks, span = blockIdx.x / pl.blocks;
+    const uint32_t wg = workgroup(), block = wg % pl.blocks, span = wg / pl.blocks;
     const Place<16, true> me(pl, block);
-    if (me.nch == 0) return;
+    if (me.nch == 0 || span >= pl.spans) return;
     uint32_t r0, r1, st, en;
     pl.rows_of(span, r0, r1);
     uint32_t pos = r0;
@@ -840,8 +841,9 @@ __global__ __launch_bounds__(Bwd<S>::WAVES * 64) __attribute__((amdgpu_waves_per
     // the wavefront's sums for dB and dC take the place of the states, which are used up by then
     static_assert(BLOCKS * 64 * S * CH >= TT * 2 * NP, "the sums fit");
 
-    const uint32_t block = blockIdx.x % pl.blocks, span = blockIdx.x / pl.blocks;
+    const uint32_t wg = workgroup(), block = wg % pl.blocks, span = wg / pl.blocks;
     const Place<CW, true> me(pl, block);
+    if (span >= pl.spans) return;
     uint32_t r0, r1;
     pl.rows_of(span, r0, r1);
     f32x2* const dt = s_dt[me.w];
@@ -1147,7 +1149,7 @@ __global__ __launch_bounds__(256) void join_bc_kernel(Plan pl, const float* __re
                                                       int64_t db_stride, T* __restrict__ dC, int64_t dc_stride)
 {
     const uint32_t quads = np / 2;  // 2 np columns
-    const uint64_t i = blockIdx.x * (uint64_t)256 + threadIdx.x;
+    const uint64_t i = workgroup() * (uint64_t)256 + threadIdx.x;
     const uint32_t col = (uint32_t)(i % quads) * 4;
     const uint64_t rg = i / quads;
     const uint32_t group = (uint32_t)(rg % pl.groups);
@@ -1170,7 +1172,7 @@ __global__ __launch_bounds__(256) void join_spans_kernel(Plan pl, const float* _
                                                          const float* __restrict__ dch, uint32_t np, float* __restrict__ dA,
                                                          float* __restrict__ dD, float* __restrict__ dbias)
 {
-    const uint64_t i = blockIdx.x * (uint64_t)256 + threadIdx.x, na = (uint64_t)pl.channels * np;
+    const uint64_t i = workgroup() * (uint64_t)256 + threadIdx.x, na = (uint64_t)pl.channels * np;
     float sum = 0.0f;
     if (i < na) {
 #pragma unroll 8
@@ -1194,9 +1196,10 @@ template <int S>
 __global__ __launch_bounds__(kGradWaves * 64) void grad_empty_kernel(Plan pl, const float* __restrict__ dfinal,
                                                                  float* __restrict__ dinitial)
 {
-    const uint32_t block = blockIdx.x % pl.blocks;
+    const uint32_t wg = workgroup(), block = wg % pl.blocks;
     const Place<16, true> me(pl, block);
-    for (uint32_t s = blockIdx.x / pl.blocks; s < pl.seqs.count; s += kEmptyStep) {
+    if (wg / pl.blocks >= kEmptyStep) return;
+    for (uint32_t s = wg / pl.blocks; s < pl.seqs.count; s += kEmptyStep) {
         if (pl.seqs.end(s) > pl.seqs.start(s)) continue;
         LaneStates<S, 1, true> g;
         g.start(dfinal, pl, me, s);
@@ -1334,14 +1337,14 @@ scan_status_t forward(const selective_scan_args_t& a, hipStream_t stream)
         constexpr int S = decltype(se)::value;
         const uint64_t wgs = (uint64_t)p.spans * p.blocks;
         const uint64_t extra = a.final_state ? (uint64_t)std::min<uint64_t>(p.seqs.count, kEmptyStep) * p.blocks : 0;
-        if (wgs + extra > 0x7FFFFFFFu) return SCAN_ERR_INVALID;
+        if (wgs + extra > kMostInGrid) return SCAN_ERR_INVALID;
         if (p.per_seq > 1)
-            hipLaunchKernelGGL((in.vec ? scan_kernel<T, S, true, true> : scan_kernel<T, S, false, true>), dim3((unsigned)wgs),
+            hipLaunchKernelGGL((in.vec ? scan_kernel<T, S, true, true> : scan_kernel<T, S, false, true>), grid_of(wgs),
                                dim3(kFwdWaves * 64), 0, stream, p, in, w.totals, (void*)nullptr, (int64_t)0, (float*)nullptr,
                                (float*)nullptr);
         if (wgs + extra)
             hipLaunchKernelGGL((in.vec ? scan_kernel<T, S, true, false> : scan_kernel<T, S, false, false>),
-                               dim3((unsigned)(wgs + extra)), dim3(kFwdWaves * 64), 0, stream, p, in, w.totals, a.y, a.y_stride,
+                               grid_of(wgs + extra), dim3(kFwdWaves * 64), 0, stream, p, in, w.totals, a.y, a.y_stride,
                                a.final_state, a.saved);
         return launched();
     });
@@ -1365,21 +1368,21 @@ scan_status_t gradient(const selective_scan_grad_args_t& g, hipStream_t stream)
         const uint32_t np = 4 * S;
         const uint64_t wgs = (uint64_t)p.spans * p.blocks;
         const uint64_t bc = ((uint64_t)a.rows * a.groups * (np / 2) + 255) / 256;
-        if (wgs > 0x7FFFFFFFu || bc > 0x7FFFFFFFu) return SCAN_ERR_INVALID;
+        if (wgs > kMostInGrid || bc > kMostInGrid) return SCAN_ERR_INVALID;
         const dim3 block(kGradWaves * 64);
         if (p.per_seq > 1)
-            hipLaunchKernelGGL((in.vec ? grad_totals_kernel<T, S, true> : grad_totals_kernel<T, S, false>), dim3((unsigned)wgs), block, 0, stream, p, in, gr, w.totals);
+            hipLaunchKernelGGL((in.vec ? grad_totals_kernel<T, S, true> : grad_totals_kernel<T, S, false>), grid_of(wgs), block, 0, stream, p, in, gr, w.totals);
         if (wgs) {
-            hipLaunchKernelGGL((in.vec ? grad_kernel<T, S, true> : grad_kernel<T, S, false>), dim3((unsigned)wgs),
+            hipLaunchKernelGGL((in.vec ? grad_kernel<T, S, true> : grad_kernel<T, S, false>), grid_of(wgs),
                                dim3(Bwd<S>::WAVES * 64), 0, stream, p, in, gr, w.totals);
-            hipLaunchKernelGGL((join_bc_kernel<T>), dim3((unsigned)bc), dim3(256), 0, stream, p, (const float*)w.bc, np,
+            hipLaunchKernelGGL((join_bc_kernel<T>), grid_of(bc), dim3(256), 0, stream, p, (const float*)w.bc, np,
                                static_cast<T*>(g.dB), g.db_stride, static_cast<T*>(g.dC), g.dc_stride);
         }
         const uint64_t sums = (uint64_t)a.channels * (np + 2);
-        hipLaunchKernelGGL(join_spans_kernel, dim3((unsigned)((sums + 255) / 256)), dim3(256), 0, stream, p,
+        hipLaunchKernelGGL(join_spans_kernel, grid_of((sums + 255) / 256), dim3(256), 0, stream, p,
                            (const float*)w.dA, (const float*)w.dch, np, g.dA, g.dD, g.ddelta_bias);
         if (g.dinitial_state && p.seqs.count && (a.seq_offsets || a.rows == 0))
-            hipLaunchKernelGGL((grad_empty_kernel<S>), dim3((unsigned)(std::min(p.seqs.count, kEmptyStep) * p.blocks)), block,
+            hipLaunchKernelGGL((grad_empty_kernel<S>), grid_of((uint64_t)std::min(p.seqs.count, kEmptyStep) * p.blocks), block,
                                0, stream, p, g.dfinal_state, g.dinitial_state);
         return launched();
     });
@@ -1521,7 +1524,7 @@ scan_status_t selective_scan_step(const selective_scan_step_args_t* args, void* 
     const uint64_t all = a.rows * (uint64_t)p.blocks;
     const bool four = all >= 4 * (uint64_t)kTargetWorkgroups;
     const uint64_t wgs = four ? (a.rows + 3) / 4 * p.blocks : all;
-    if (wgs > 0x7FFFFFFFu) return SCAN_ERR_INVALID;
+    if (wgs > kMostInGrid) return SCAN_ERR_INVALID;
     Inputs in = make_inputs(a, r);
     in.vec = a.states == padded_states(a.states) && aligned(a.state, 16) && aligned(a.A, 16) && r.vec(a.B, a.b_stride) &&
              r.vec(a.C, a.c_stride);
@@ -1530,7 +1533,7 @@ scan_status_t selective_scan_step(const selective_scan_step_args_t* args, void* 
         constexpr int S = decltype(se)::value;
         const auto k = four ? (in.vec ? scan_step_kernel<T, S, true, 4> : scan_step_kernel<T, S, false, 4>)
                             : (in.vec ? scan_step_kernel<T, S, true, 1> : scan_step_kernel<T, S, false, 1>);
-        hipLaunchKernelGGL(k, dim3((unsigned)wgs), dim3(kGradWaves * 64), 0, static_cast<hipStream_t>(stream), p, in, a.slots,
+        hipLaunchKernelGGL(k, grid_of(wgs), dim3(kGradWaves * 64), 0, static_cast<hipStream_t>(stream), p, in, a.slots,
                            (uint32_t)a.n_slots, a.state, static_cast<T*>(a.y), a.y_stride);
         return launched();
     });

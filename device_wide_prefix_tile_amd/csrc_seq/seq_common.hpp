@@ -117,6 +117,11 @@ __device__ __forceinline__ void wave_sync()
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// A launch's workgroups are numbered over two dimensions of the grid, kGridWidth in a row: HIP takes
+// less than 2^32 work items along one.  The last row may hold numbers behind the last workgroup.
+constexpr uint32_t kGridWidth = 1u << 22;
+__device__ __forceinline__ uint32_t workgroup() { return blockIdx.y * kGridWidth + blockIdx.x; }
+
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // ------------------------------------------------------------ host side
@@ -161,6 +166,14 @@ bool any_overlap(const Range (&out)[NO], const Range (&in)[NI])
             if (overlap(out[i], out[j])) return true;
     }
     return false;
+}
+
+// The grid of `workgroups` (of 256 lanes or fewer) for workgroup(); more of them than kMostInGrid
+// would need arrays larger than a card's memory.
+constexpr uint64_t kMostInGrid = 0x7FFFFFFF;
+inline dim3 grid_of(uint64_t workgroups)
+{
+    return dim3((unsigned)std::min<uint64_t>(workgroups, kGridWidth), (unsigned)((workgroups + kGridWidth - 1) / kGridWidth));
 }
 
 inline scan_status_t launched() { return hipGetLastError() == hipSuccess ? SCAN_OK : SCAN_ERR_HIP; }

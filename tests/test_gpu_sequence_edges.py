@@ -251,3 +251,46 @@ def test_rate_of_minus_infinity_forgets(n):
         got.append((y, fin, step, state))
     for p, q in zip(*got):
         assert torch.isfinite(p).all() and torch.equal(p, q)
+
+
+# ---------------------------------------------------------------------- more workgroups than one dimension of a grid holds
+def test_lookup_of_more_tokens_than_a_grid_row():
+    n = (1 << 26) + 5
+    table = torch.arange(1, 12, dtype=torch.float16, device="cuda")[:, None]
+    tok = (torch.arange(n, dtype=torch.int32, device="cuda") % 13) - 1  # -1 and 11 are outside the table
+    y = dw.embedding_lookup(tok, table, scale=2.0)
+    want = torch.where((tok >= 0) & (tok < 11), (tok + 1) * 2, 0).to(torch.float16)
+    assert torch.equal(y[:, 0], want)
+
+
+def test_table_gradient_of_more_rows_than_a_grid_row():
+    v, d = 1 << 24, 1023  # odd: one element per lane
+    tok = torch.tensor([0, v - 1, 12345678, v - 1, -1, v], dtype=torch.int32, device="cuda")
+    dout = torch.randint(-8, 9, (6, d), device="cuda").to(torch.bfloat16)
+    g = dw.embedding_grad(tok, dout, v)
+    for r, want in ((0, dout[0]), (12345678, dout[2]), (v - 1, dout[1] + dout[3])):
+        assert torch.equal(g[r], want)
+        g[r] = 0
+    assert not g.any()
+
+
+def test_convolution_of_more_sequences_than_a_grid_row():
+    b = (1 << 29) + 3
+    x = (torch.arange(b, dtype=torch.int32, device="cuda") % 251).to(torch.bfloat16).view(b, 1, 1)
+    w = torch.tensor([[3.0, 0.5]], dtype=torch.bfloat16, device="cuda")
+    y, fin = dw.causal_conv1d(x, w, final_state=True)
+    assert torch.equal(fin, x) and torch.equal(y, x * 0.5)
+
+
+def test_scan_of_more_sequences_than_a_grid_row():
+    b = (1 << 24) + 3
+    one = torch.ones(b, 1, 1, device="cuda")
+    x = (torch.arange(b, dtype=torch.int32, device="cuda") % 1021).float().view(b, 1, 1)
+    args = (x, one, -torch.ones(1, 1, device="cuda"), one[..., None], one[..., None])
+    y, fin, saved = dw.selective_scan(*args, final_state=True, save_for_grad=True)
+    assert torch.equal(y, x) and torch.equal(fin, x)  # dt x B = x
+    g = dw.selective_scan_grad(x, *args, saved=saved)
+    assert torch.equal(g.dx, x) and torch.equal(g.dC[..., 0], x * x) and torch.equal(g.dB[..., 0], x * x)
+    state = torch.zeros(b, 1, 1, device="cuda")
+    step = dw.selective_scan_step(x[:, 0], one[:, 0], args[2], one, one, state)
+    assert torch.equal(step, x[:, 0]) and torch.equal(state, x)
