@@ -7,6 +7,10 @@ enqueue on the current stream of the tensors' device (or on ``stream``) and retu
 synchronising, and there is no CPU fallback.  Outputs and workspaces come from torch's allocator
 on the stream that the call runs on, so a call can be captured into a graph.
 
+The gradients are functions of their own: nothing is recorded for autograd.  Where autograd is
+recording, a tensor that requires a gradient is refused rather than detached without a word; call
+under ``torch.no_grad()``, inside an ``autograd.Function``, or with ``tensor.detach()``.
+
 Layout: channels last.  Rows are (B, L, D) for B sequences of one length, or (rows, D) with
 ``seq_offsets`` (int32, S + 1 ascending) for sequences packed one behind the other.  A tensor of
 rows may be a slice of a wider one (any row stride); its last dimension is contiguous.
@@ -134,8 +138,19 @@ def _on(x: torch.Tensor, name: str, t: torch.Tensor):
         raise ValueError("%s must be on the device of the other tensors" % name)
 
 
+_recording = torch.is_grad_enabled
+
+
+def _no_graph(t: torch.Tensor, name: str):
+    """Refuses t if autograd would have to record what is done with it."""
+    if t.requires_grad and _recording():
+        raise ValueError("%s requires a gradient, which the sequence operators do not record: call them under torch.no_grad(), "
+                         "or with %s.detach()" % (name, name))
+
+
 def _refuse(t: torch.Tensor, name: str, shape, dtype):
-    """What is wrong with t, which was to have that shape and type and lie on the other tensors' device."""
+    """What is wrong with t, which was to have that shape and type, lie on the other tensors' device and need no graph."""
+    _no_graph(t, name)
     if t.shape != shape:
         raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
     if t.dtype != dtype:
@@ -176,7 +191,7 @@ def _plain(t: torch.Tensor, name: str, shape, dtype, device: int):
     """Address of t, a contiguous tensor of that shape, type and device (its index; -1: the host); None for None."""
     if t is None:
         return None
-    if t.shape != shape or t.dtype != dtype or t.get_device() != device:
+    if t.shape != shape or t.dtype != dtype or t.get_device() != device or (t.requires_grad and _recording()):
         _refuse(t, name, shape, dtype)
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
@@ -187,7 +202,7 @@ def _like(t: torch.Tensor, name: str, shape, dtype, device: int, width: int, inn
     """(address, row stride) of t, rows of `width` values in that shape, type and device; (None, 0) for None."""
     if t is None:
         return None, 0
-    if t.shape != shape or t.dtype != dtype or t.get_device() != device:
+    if t.shape != shape or t.dtype != dtype or t.get_device() != device or (t.requires_grad and _recording()):
         _refuse(t, name, shape, dtype)
     return t.data_ptr(), width if t.is_contiguous() else _rows(t, name, inner)
 
@@ -195,6 +210,7 @@ def _like(t: torch.Tensor, name: str, shape, dtype, device: int, width: int, inn
 def _x(x: torch.Tensor, name: str = "x"):
     if x.dtype not in _DTYPE:
         raise TypeError("%s must be float32, float16 or bfloat16" % name)
+    _no_graph(x, name)
     if not x.is_cuda:
         raise ValueError("%s must be a device tensor" % name)
 

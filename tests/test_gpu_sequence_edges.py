@@ -294,3 +294,35 @@ def test_scan_of_more_sequences_than_a_grid_row():
     state = torch.zeros(b, 1, 1, device="cuda")
     step = dw.selective_scan_step(x[:, 0], one[:, 0], args[2], one, one, state)
     assert torch.equal(step, x[:, 0]) and torch.equal(state, x)
+
+
+# ---------------------------------------------------------------------- autograd
+def test_parameters_are_refused_where_autograd_records():
+    rng = np.random.default_rng(120)
+    x, w = randn(rng, 2, 6, 16), torch.nn.Parameter(randn(rng, 16, 4))
+    table, tok = torch.nn.Parameter(randn(rng, 9, 16)), torch.zeros(3, dtype=torch.int32, device="cuda")
+    A, bc = torch.nn.Parameter(-randn(rng, 16, 8).abs()), randn(rng, 2, 6, 1, 8)
+    calls = [lambda: dw.embedding_lookup(tok, table), lambda: dw.causal_conv1d(x, w), lambda: dw.causal_conv1d_grad(x, x, w),
+             lambda: dw.causal_conv1d_step(x[:, 0], x[:, :3].contiguous(), w), lambda: dw.selective_scan(x, x, A, bc, bc),
+             lambda: dw.selective_scan_grad(x, x, x, A, bc, bc), lambda: dw.embedding_grad(tok, table[:3], 9),
+             lambda: dw.selective_scan_step(x[:, 0], x[:, 0], A, bc[:, 0], bc[:, 0], torch.zeros(2, 16, 8, device="cuda"))]
+    for call in calls:
+        with pytest.raises(ValueError, match="requires a gradient"):
+            call()
+        with torch.no_grad():
+            call()
+
+    class Conv(torch.autograd.Function):  # the way into a graph: both directions run outside of it
+        @staticmethod
+        def forward(ctx, x, w):
+            ctx.save_for_backward(x, w)
+            return dw.causal_conv1d(x, w, activation="silu")
+
+        @staticmethod
+        def backward(ctx, dy):
+            g = dw.causal_conv1d_grad(dy.contiguous(), *ctx.saved_tensors, activation="silu")
+            return g.dx, g.dweight
+    dy = randn(rng, 2, 6, 16)
+    Conv.apply(x, w).backward(dy)
+    with torch.no_grad():
+        assert torch.equal(w.grad, dw.causal_conv1d_grad(dy, x, w, activation="silu").dweight)
