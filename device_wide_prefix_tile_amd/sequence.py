@@ -229,10 +229,16 @@ def _lengths(x: torch.Tensor, seq_offsets):
     return x.shape[0], seq_offsets.shape[0] - 1, seq_offsets.data_ptr()
 
 
-def _out(out, x: torch.Tensor, name: str):
+def _new_rows(seq_offsets):
+    """What makes a new tensor for gradients of rows: the kernels write the rows of sequences, and the gradient
+    of a row that belongs to none is zero."""
+    return torch.empty if seq_offsets is None else torch.zeros
+
+
+def _out(out, x: torch.Tensor, name: str, new=torch.empty):
     """(tensor, address, row stride) of an output shaped like x: `out`, or a new one."""
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = new(x.shape, dtype=x.dtype, device=x.device)
         return out, out.data_ptr(), x.shape[-1]
     return (out,) + _like(out, name, x.shape, x.dtype, x.get_device(), x.shape[-1])
 
@@ -366,7 +372,7 @@ def causal_conv1d(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Te
     type or float32.  Inputs before a sequence come from initial_state (S, K - 1, D), oldest
     first, else they are zero.  final_state: a tensor (S, K - 1, D) for the last K - 1 inputs of
     every sequence, or True for a new one: (y, final_state) is returned then, else y.  Rows of y
-    that belong to no sequence are not written."""
+    that belong to no sequence are not written (in a new y they hold whatever the memory held)."""
     a, state = _conv_args(x, weight, bias, activation, seq_offsets, initial_state)
 
     def call(handle):
@@ -384,7 +390,8 @@ def causal_conv1d_grad(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, 
                        dx: Optional[torch.Tensor] = None, stream=None) -> ConvGrads:
     """Gradients of ``causal_conv1d`` (its arguments) for dy, and for dfinal_state if given.
 
-    dx may be given to write into (a slice of a wider tensor, say)."""
+    dx may be given to write into (a slice of a wider tensor, say); its rows that belong to no
+    sequence are not written then, and are zero otherwise."""
     a, state = _conv_args(x, weight, bias, activation, seq_offsets, initial_state)
     d, k = weight.shape
     g = _ConvGradArgs(a, *_like(dy, "dy", x.shape, x.dtype, x.get_device(), x.shape[-1]),
@@ -392,7 +399,7 @@ def causal_conv1d_grad(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, 
 
     def call(handle):
         L = _lib()
-        ox, g.dx, g.dx_stride = _out(dx, x, "dx")
+        ox, g.dx, g.dx_stride = _out(dx, x, "dx", _new_rows(seq_offsets))
         dw = torch.empty(d, k, dtype=torch.float32, device=x.device)
         db = None if bias is None else torch.empty(d, dtype=torch.float32, device=x.device)
         di = None if initial_state is None else torch.empty_like(initial_state)
@@ -421,7 +428,7 @@ def causal_conv1d_step(x: torch.Tensor, state: torch.Tensor, weight: torch.Tenso
     state (n_slots, K - 1, D) is shifted in place.
 
     slots: int32 (rows,), distinct within a call; None: row i has slot i.  A row whose slot lies
-    outside the state is skipped: its row of y is not written."""
+    outside the state is skipped: its row of y is not written (in a new y it holds whatever the memory held)."""
     _x(x)
     if x.dim() != 2 or state.dim() != 3:
         raise ValueError("x must be (rows, D), state (n_slots, K - 1, D)")
@@ -494,7 +501,8 @@ def selective_scan(x: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, B: tor
     type; G divides D, N <= 64.  A (D, N), D (D,), delta_bias (D,) and the states (S, D, N) are
     float32.  initial_state: h before every sequence (default zero).  final_state: a tensor for h
     after every sequence, or True for a new one.  save_for_grad: also return the states that
-    ``selective_scan_grad`` starts from.  Returns y, followed by what was asked for."""
+    ``selective_scan_grad`` starts from.  Returns y, followed by what was asked for.  Rows of y that
+    belong to no sequence are not written (in a new y they hold whatever the memory held)."""
     a, state = _scan_args(x, delta, A, B, C, D, z, delta_bias, delta_softplus, seq_offsets, initial_state)
 
     def call(handle):
@@ -527,7 +535,8 @@ def selective_scan_grad(dy: torch.Tensor, x: torch.Tensor, delta: torch.Tensor, 
 
     saved: what ``selective_scan(..., save_for_grad=True)`` returned for the same inputs; without
     it the states are scanned again.  dx and dz may be given to write into (two slices of one
-    tensor, say)."""
+    tensor, say).  Gradients of rows that belong to no sequence are zero, but for those of a given
+    dx or dz, which are not written."""
     a, state = _scan_args(x, delta, A, B, C, D, z, delta_bias, delta_softplus, seq_offsets, initial_state)
     g = _ScanGradArgs(a, *_like(dy, "dy", x.shape, x.dtype, x.get_device(), x.shape[-1]),
                       _plain(dfinal_state, "dfinal_state", state, torch.float32, x.get_device()))
@@ -547,11 +556,12 @@ def selective_scan_grad(dy: torch.Tensor, x: torch.Tensor, delta: torch.Tensor, 
             _check(L.selective_scan(ctypes.byref(a), handle), "selective_scan")
         a.saved = _plain(states, "saved", (need_saved,), torch.float32, x.get_device())
         g.args = a
-        ox, g.dx, g.dx_stride = _out(dx, x, "dx")
-        od, g.ddelta, g.ddelta_stride = _out(None, x, "ddelta")
-        oz, g.dz, g.dz_stride = (None, None, 0) if z is None else _out(dz, x, "dz")
-        oB = torch.empty(B.shape, dtype=x.dtype, device=x.device)
-        oC = torch.empty(C.shape, dtype=x.dtype, device=x.device)
+        new = _new_rows(seq_offsets)
+        ox, g.dx, g.dx_stride = _out(dx, x, "dx", new)
+        od, g.ddelta, g.ddelta_stride = _out(None, x, "ddelta", new)
+        oz, g.dz, g.dz_stride = (None, None, 0) if z is None else _out(dz, x, "dz", new)
+        oB = new(B.shape, dtype=x.dtype, device=x.device)
+        oC = new(C.shape, dtype=x.dtype, device=x.device)
         oA = torch.empty(A.shape, **f32)
         oD = None if D is None else torch.empty(D.shape, **f32)
         ob = None if delta_bias is None else torch.empty(delta_bias.shape, **f32)

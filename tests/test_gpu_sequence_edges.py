@@ -326,3 +326,22 @@ def test_parameters_are_refused_where_autograd_records():
     Conv.apply(x, w).backward(dy)
     with torch.no_grad():
         assert torch.equal(w.grad, dw.causal_conv1d_grad(dy, x, w, activation="silu").dweight)
+
+
+# ---------------------------------------------------------------------- rows of no sequence
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+def test_new_gradients_of_rows_without_a_sequence_are_zero(t):
+    """Whatever the allocator hands out: no output depends on those rows."""
+    rng = np.random.default_rng(130)
+    rows, d, n, lo, hi, t = 120, 64, 16, 3, 100, T[t]
+    v = scan_inputs(rng, (rows,), d, n, 2, t)
+    dy, w = randn(rng, rows, d, t=t), randn(rng, d, 4, t=t)
+    off = offsets([50, 0, 47], lo)
+    a, kw = call_args(v)
+    for _ in range(2):
+        junk = [torch.full(s, float("nan"), dtype=t, device="cuda") for s in [(rows, d)] * 8 + [(rows, 2, n)] * 4]
+        del junk
+        g = dw.selective_scan_grad(dy, *a, delta_softplus=True, seq_offsets=off, **kw)
+        c = dw.causal_conv1d_grad(dy, v["x"], w, seq_offsets=off)
+        for q in (g.dx, g.ddelta, g.dz, g.dB, g.dC, c.dx):
+            assert (q[:lo] == 0).all() and (q[hi:] == 0).all() and torch.isfinite(q).all() and q[lo:hi].any()
