@@ -7,9 +7,10 @@ import pytest
 import torch
 
 import device_wide_prefix_tile_amd as dw
+import sequence_errors as err
 import sequence_reference as ref
 from device_wide_prefix_tile_amd import sequence as seq
-from sequence_reference import close, f64  # noqa: F401
+from sequence_reference import f64
 
 pytestmark = pytest.mark.gpu
 
@@ -345,3 +346,40 @@ def test_new_gradients_of_rows_without_a_sequence_are_zero(t):
         c = dw.causal_conv1d_grad(dy, v["x"], w, seq_offsets=off)
         for q in (g.dx, g.ddelta, g.dz, g.dB, g.dC, c.dx):
             assert (q[:lo] == 0).all() and (q[hi:] == 0).all() and torch.isfinite(q).all() and q[lo:hi].any()
+
+
+# ---------------------------------------------------------------------- precision
+@pytest.mark.parametrize("t", list(T))
+@pytest.mark.parametrize("lengths,d,n", [([300, 2, 211], 24, 16), ([33, 64, 5], 72, 16), ([1500], 40, 16), ([700, 90], 40, 5), ([512], 24, 40),
+                                         ([129, 0, 400], 16, 64)])
+def test_scan_errors_do_not_grow_with_the_length(t, lengths, d, n):
+    """Within bounds that follow the recurrence (tests/test_sequence_errors_host.py shows that a state of
+    16 bits leaves them): no state, sum or factor is held in fewer than 32."""
+    rng = np.random.default_rng(sum(lengths) + n)
+    rows, t = sum(lengths), T[t]
+    v = scan_inputs(rng, (rows,), d, n, 1, t)
+    init, dfin, dy = randn(rng, len(lengths), d, n), randn(rng, len(lengths), d, n), randn(rng, rows, d, t=t)
+    a, kw = call_args(v)
+    kw.update(delta_softplus=True, seq_offsets=offsets(lengths), initial_state=init)
+    y, fin, saved = dw.selective_scan(*a, final_state=True, save_for_grad=True, **kw)
+    g = dw.selective_scan_grad(dy, *a, saved=saved, dfinal_state=dfin, **kw)._asdict()
+    g["dinitial"] = g.pop("dinitial_state")
+    ends = np.cumsum([0] + lengths)
+    want = err.scan(f64(v["x"]), f64(v["delta"]), f64(v["A"]), f64(v["B"]), f64(v["C"]), f64(v["D"]), f64(v["z"]), f64(v["delta_bias"]), True,
+                    list(zip(ends[:-1], ends[1:])), f64(init), f64(dy), f64(dfin))
+    for name, q in dict(g, y=y, final=fin).items():
+        err.near(q, *want[name], name)
+
+
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+def test_convolution_parameter_sums_of_long_blocks(t):
+    """Enough rows for the longest row blocks: dweight and dbias within the bounds of their own terms, which
+    a block left out leaves."""
+    rng = np.random.default_rng(131)
+    b, l, d, some, t = 64, 700, 1024, slice(480, 544), T[t]
+    x, dy = randn(rng, b, l, d, t=t), randn(rng, b, l, d, t=t)
+    w, bias = randn(rng, d, 4, t=t), randn(rng, d, t=t)
+    g = dw.causal_conv1d_grad(dy, x, w, bias, activation="silu")
+    dweight, dbias, dweight_e, dbias_e = err.conv_sums(f64(x[..., some]), f64(dy[..., some]), f64(w[some]), f64(bias[some]))
+    err.near(g.dweight[some], dweight, dweight_e, "dweight")
+    err.near(g.dbias[some], dbias, dbias_e, "dbias")
