@@ -480,7 +480,8 @@ bool valid_rows_out(const void* p, int64_t stride, const causal_conv1d_args_t& a
     return a.rows == 0 || (p && aligned(p, dtype_size(a.dtype)) && stride >= (int64_t)a.channels && stride <= ((int64_t)1 << 31));
 }
 
-// Whether the 16-byte path can be taken; V elements of dtype, weights of ws bytes.
+// Whether the vector path can be taken.  One rule for every form: whole 16-byte pieces of dtype, which the
+// single-token kernel moves; the other two move kPack elements and would do with those.
 bool vector_ok(const causal_conv1d_args_t& a, const void* extra0, int64_t s0, const void* extra1, int64_t s1,
                const void* extra2, const void* extra3)
 {

@@ -16,7 +16,8 @@
  *   - Channels come last and are contiguous; a `*_stride` counts elements
  *     from one row to the next.  16-byte aligned pointers, strides and
  *     channel counts select the vector path, anything else a slower path with
- *     the same results.
+ *     the same results, but for the convolution's dweight and dbias: the path
+ *     decides which rows are added up first, so their last bits may differ.
  *   - Rows are flat.  With seq_offsets == NULL there are `seqs` sequences of
  *     rows / seqs rows each.  Otherwise seq_offsets holds seqs + 1 ascending
  *     int32 (device memory) and sequence s is rows [seq_offsets[s],
@@ -32,7 +33,8 @@
  *     contents need not be kept or cleared).  Nothing is allocated and no
  *     state is kept, so the calls can be captured into a graph, and calls
  *     with different workspaces may overlap in time.
- *   - No floating-point atomics: results repeat bit for bit.
+ *   - No floating-point atomics: results repeat bit for bit (on one path, see
+ *     above).
  *   - Outputs must not overlap inputs or one another (SCAN_ERR_INVALID),
  *     except where a state is updated in place.
  */

@@ -383,3 +383,34 @@ def test_convolution_parameter_sums_of_long_blocks(t):
     dweight, dbias, dweight_e, dbias_e = err.conv_sums(f64(x[..., some]), f64(dy[..., some]), f64(w[some]), f64(bias[some]))
     err.near(g.dweight[some], dweight, dweight_e, "dweight")
     err.near(g.dbias[some], dbias, dbias_e, "dbias")
+
+
+# ---------------------------------------------------------------------- the vector path and the other one
+@pytest.mark.parametrize("t", list(T))
+def test_both_paths_give_the_same_bits_but_for_the_convolutions_sums(t):
+    """The same values at whole 16-byte pieces and two bytes beside them, as the header says."""
+    rng = np.random.default_rng(140)
+    b, l, d, n, t = 3, 290, 64, 16, T[t]
+    v = scan_inputs(rng, (b, l), d, n, 2, t)
+    dy, w, bias = randn(rng, b, l, d, t=t), randn(rng, d, 4, t=t), randn(rng, d, t=t)
+
+    def beside(q):
+        wide = torch.zeros(q.shape[:2] + (q[0, 0].numel() + 1,), dtype=q.dtype, device="cuda")
+        wide[..., 1:] = q.flatten(2)
+        return wide[..., 1:].unflatten(-1, q.shape[2:]) if q.dim() == 4 else wide[..., 1:]
+    a, kw = call_args(v)
+    a2 = [beside(q) if q.dim() > 2 else q for q in a]
+    kw2 = dict(kw, z=beside(v["z"]))
+    for p, q in zip(dw.selective_scan(*a, delta_softplus=True, final_state=True, **kw),
+                    dw.selective_scan(*a2, delta_softplus=True, final_state=True, **kw2)):
+        assert torch.equal(p, q)
+    for p, q in zip(dw.selective_scan_grad(dy, *a, delta_softplus=True, **kw),
+                    dw.selective_scan_grad(beside(dy), *a2, delta_softplus=True, **kw2)):
+        assert (p is None and q is None) or torch.equal(p, q)
+    assert torch.equal(dw.causal_conv1d(v["x"], w, bias, activation="silu"), dw.causal_conv1d(a2[0], w, bias, activation="silu"))
+    g, g2 = (dw.causal_conv1d_grad(r, x, w, bias, activation="silu") for r, x in ((dy, v["x"]), (beside(dy), a2[0])))
+    assert torch.equal(g.dx, g2.dx)
+    dweight, dbias, dweight_e, dbias_e = err.conv_sums(f64(v["x"]), f64(dy), f64(w), f64(bias))
+    for q in (g, g2):
+        err.near(q.dweight, dweight, dweight_e, "dweight")
+        err.near(q.dbias, dbias, dbias_e, "dbias")
