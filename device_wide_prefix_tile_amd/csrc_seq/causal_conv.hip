@@ -466,7 +466,7 @@ scan_status_t check_common(const causal_conv1d_args_t& a)
         return SCAN_ERR_UNSUPPORTED;
     if (a.channels < 1 || a.channels > kMaxChannels || a.rows >= ((uint64_t)1 << 31) || a.seqs >= ((uint64_t)1 << 31))
         return SCAN_ERR_INVALID;
-    if (a.seqs == 0 ? a.rows != 0 : (!a.seq_offsets && a.rows % a.seqs != 0)) return SCAN_ERR_INVALID;
+    if (!a.seq_offsets && (a.seqs == 0 ? a.rows != 0 : a.rows % a.seqs != 0)) return SCAN_ERR_INVALID;
     if (a.seq_offsets && !aligned(a.seq_offsets, 4)) return SCAN_ERR_INVALID;
     const size_t es = dtype_size(a.dtype), ws = dtype_size(a.weight_dtype);
     if (!a.weight || !aligned(a.weight, ws) || !aligned(a.bias, ws) || !aligned(a.initial_state, es)) return SCAN_ERR_INVALID;

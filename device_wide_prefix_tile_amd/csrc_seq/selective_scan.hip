@@ -1271,7 +1271,7 @@ scan_status_t check_scan(const selective_scan_args_t& a)
     const scan_status_t st = check_sizes(a.dtype, a.rows, a.channels, a.states, a.groups);
     if (st != SCAN_OK) return st;
     if (a.seqs >= ((uint64_t)1 << 31)) return SCAN_ERR_INVALID;
-    if (a.seqs == 0 ? a.rows != 0 : (!a.seq_offsets && a.rows % a.seqs != 0)) return SCAN_ERR_INVALID;
+    if (!a.seq_offsets && (a.seqs == 0 ? a.rows != 0 : a.rows % a.seqs != 0)) return SCAN_ERR_INVALID;
     if (!aligned(a.seq_offsets, 4)) return SCAN_ERR_INVALID;
     const Rows r{a.dtype, a.rows};
     const uint32_t gn = a.groups * a.states;

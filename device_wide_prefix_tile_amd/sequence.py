@@ -427,7 +427,7 @@ def causal_conv1d_step(x: torch.Tensor, state: torch.Tensor, weight: torch.Tenso
     """One token per row of x (rows, D): y from state[slots[i]] (its last K - 1 inputs) and x[i]; the
     state (n_slots, K - 1, D) is shifted in place.
 
-    slots: int32 (rows,), distinct within a call; None: row i has slot i.  A row whose slot lies
+    rows <= 65535.  slots: int32 (rows,), distinct within a call; None: row i has slot i.  A row whose slot lies
     outside the state is skipped: its row of y is not written (in a new y it holds whatever the memory held)."""
     _x(x)
     if x.dim() != 2 or state.dim() != 3:

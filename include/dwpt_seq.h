@@ -13,21 +13,24 @@
  * Conventions (besides those of dwpt_scan.h: device pointers on the current
  * device, stream as void*, calls only enqueue, argument errors returned
  * before anything is launched):
- *   - Channels come last and are contiguous; a `*_stride` counts elements
- *     from one row to the next.  16-byte aligned pointers, strides and
+ *   - Channels come last and are contiguous, at most 2^20; a `*_stride` counts
+ *     elements from one row to the next, at most 2^31.  Rows and sequences
+ *     number less than 2^31.  16-byte aligned pointers, strides and
  *     channel counts select the vector path, anything else a slower path with
  *     the same results, but for the convolution's dweight and dbias: the path
  *     decides which rows are added up first, so their last bits may differ.
  *   - Rows are flat.  With seq_offsets == NULL there are `seqs` sequences of
  *     rows / seqs rows each.  Otherwise seq_offsets holds seqs + 1 ascending
  *     int32 (device memory) and sequence s is rows [seq_offsets[s],
- *     seq_offsets[s+1]), possibly none.  Rows outside every sequence (before
- *     the first, behind the last) are neither read nor written.  Values that
- *     do not ascend or lie outside 0 .. rows give unspecified results, but no
- *     access outside the arrays.
+ *     seq_offsets[s+1]), possibly none; seqs may be 0.  Rows outside every
+ *     sequence (before the first, behind the last) are neither read nor
+ *     written.  Values that do not ascend or lie outside 0 .. rows give
+ *     unspecified results, but no access outside the arrays.
  *   - SEQ_F32, SEQ_F16 and SEQ_BF16 arrays are converted to 32 bits on the
  *     way in; every sum, state and activation is held in 32 bits; results are
- *     rounded once, to nearest even.
+ *     rounded once, to nearest even.  Infinities and NaN reach what the
+ *     formulas let them reach and nothing else; which of the two a state that
+ *     is no longer finite reads as may depend on how its sequence is cut.
  *   - Workspace is the caller's: `workspace` must hold the bytes the matching
  *     *_workspace function returns for the same arguments (256-byte aligned;
  *     contents need not be kept or cleared).  Nothing is allocated and no

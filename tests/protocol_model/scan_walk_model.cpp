@@ -142,7 +142,7 @@ int main(int argc, char** argv)
     const auto upto = [&](uint64_t n) { return rng() % (n + 1); };
     for (uint64_t c = 0; c < cases; ++c) {
         const int kind = (int)(c % 4);  // one length; ascending; any order; any order and outside the rows
-        const uint32_t seqs = 1 + (uint32_t)upto(upto(3) ? 9 : 300), channels = 1u << upto(13);
+        const uint32_t seqs = (uint32_t)upto(upto(3) ? 10 : 300) + (kind == 0), channels = 1u << upto(13);
         uint32_t rows = (uint32_t)upto(upto(3) ? 300 : 4000);
         if (kind == 0) rows = rows / seqs * seqs;
         std::vector<int32_t> off(seqs + 1);

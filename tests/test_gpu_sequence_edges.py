@@ -414,3 +414,25 @@ def test_both_paths_give_the_same_bits_but_for_the_convolutions_sums(t):
     for q in (g, g2):
         err.near(q.dweight, dweight, dweight_e, "dweight")
         err.near(q.dbias, dbias, dbias_e, "dbias")
+
+
+@pytest.mark.parametrize("packed", [True, False])
+def test_no_sequences(packed):
+    """Rows of no sequence, or a batch of none: nothing is written, sums over rows are zero."""
+    rng = np.random.default_rng(150)
+    d, n = 40, 16
+    lead = (70,) if packed else (0, 7)
+    v = scan_inputs(rng, lead, d, n)
+    dy, w, bias = randn(rng, *lead, d), randn(rng, d, 4), randn(rng, d)
+    off = torch.tensor([30], dtype=torch.int32, device="cuda") if packed else None
+    a, kw = call_args(v)
+    kw.update(delta_softplus=True, seq_offsets=off)
+    out = torch.full(lead + (d,), 4.0, device="cuda")
+    y, fin, saved = dw.selective_scan(*a, final_state=True, save_for_grad=True, out=out, **kw)
+    assert (out == 4.0).all() and fin.shape == (0, d, n)
+    g = dw.selective_scan_grad(dy, *a, saved=saved, **kw)
+    y, cs = dw.causal_conv1d(v["x"], w, bias, seq_offsets=off, final_state=True, out=out)
+    assert (out == 4.0).all() and cs.shape == (0, 3, d)
+    c = dw.causal_conv1d_grad(dy, v["x"], w, bias, seq_offsets=off)
+    for q in list(g) + list(c):
+        assert q is None or not q.any()

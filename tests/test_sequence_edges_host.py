@@ -29,3 +29,17 @@ def test_tensors_that_require_gradients_are_refused():
             check(p)
     with pytest.raises(ValueError, match="device tensor"):
         dw.embedding_lookup(tok, table)
+
+
+def test_no_sequences_with_offsets_is_a_call():
+    """Offsets of no sequence leave every row outside; without offsets rows need a sequence."""
+    import ctypes
+
+    L = seq._lib()
+    mb = 1 << 20  # fake device addresses: only sizes are asked for
+    args = dict(dtype=0, rows=64, seqs=0, channels=8, states=16, groups=1, x=mb, x_stride=8, delta=2 * mb, delta_stride=8, A=3 * mb,
+                B=4 * mb, b_stride=16, C=5 * mb, c_stride=16)
+    conv = dict(dtype=0, weight_dtype=0, width=4, rows=64, seqs=0, channels=8, x=mb, x_stride=8, weight=2 * mb)
+    for offsets, there in ((6 * mb, True), (None, False)):
+        assert (L.selective_scan_workspace(ctypes.byref(seq._ScanArgs(seq_offsets=offsets, **args))) > 0) == there
+        assert (L.causal_conv1d_grad_workspace(ctypes.byref(seq._ConvArgs(seq_offsets=offsets, **conv))) > 0) == there
