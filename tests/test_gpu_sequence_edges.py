@@ -436,3 +436,33 @@ def test_no_sequences(packed):
     c = dw.causal_conv1d_grad(dy, v["x"], w, bias, seq_offsets=off)
     for q in list(g) + list(c):
         assert q is None or not q.any()
+
+
+@pytest.mark.parametrize("where", ["B", "C"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("d,n", [(48, 16), (40, 16), (20, 5), (24, 40)])
+def test_scan_gradients_keep_a_state_to_itself(where, value, d, n):
+    """A value of B or C that is not finite reaches its own state alone: of dA and dC (or dB), one column."""
+    rng = np.random.default_rng(160 + n)
+    lengths, t0, n0 = [41, 22], 21, n // 2
+    v = scan_inputs(rng, (63,), d, n)
+    dy = randn(rng, 63, d)
+    clean, want_clean = run_scan(v, lengths, dy), scan_values(v, lengths, dy)
+    v[where][t0, 0, n0] = value
+    want = scan_values(v, lengths, dy)
+    assert np.isfinite(want["dA"]).all(0).sum() == n - 1
+    same_where_finite(run_scan(v, lengths, dy), clean, want, want_clean, "%s %s" % (where, value))
+
+
+@pytest.mark.parametrize("where", ["x", "delta", "z", "dy"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_values_that_are_not_finite_in_a_long_sequence(where, value):
+    """The same across the spans that a long sequence is cut into."""
+    rng = np.random.default_rng(170)
+    lengths, d, n, t0, c0 = [403, 100], 24, 16, 210, 17
+    v = scan_inputs(rng, (503,), d, n)
+    dy = randn(rng, 503, d)
+    clean, want_clean = run_scan(v, lengths, dy), scan_values(v, lengths, dy)
+    (dy if where == "dy" else v[where])[t0, c0] = value
+    got, want = run_scan(v, lengths, dy), scan_values(v, lengths, dy)
+    same_where_finite(got, clean, want, want_clean, "%s %s" % (where, value))
