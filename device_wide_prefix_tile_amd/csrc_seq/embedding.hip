@@ -32,8 +32,16 @@ namespace {
 
 constexpr int kGroupBlock = 1024;
 constexpr int kGroupWaves = kGroupBlock / 64;
-constexpr uint32_t kSegment = 65536;      // tokens that one pass of the grouping kernels reads
-constexpr uint32_t kMaxPerBucket = 2048;  // table rows per bucket: 16 wavefronts' counters take 128 KB of LDS
+// Tokens that one pass of the grouping kernels reads.  Every workgroup reads a segment whole, which
+// short ones make cheaper, but every segment's counts of the whole table go through memory.  Gradient
+// with 65536 / 32768 / 16384 / 8192 / 4096, us: 65536 x 2048 bfloat16 into 50000 rows 139 / 143 / 132 /
+// 137 / 149; 262144 x 1024 into 50000 228 / 223 / 229 / 257 / 308; 65536 x 64 into 2^20 163 / 193 / 221 /
+// 321 / 510; 65536 x 8 into 2^24 2714 / 3204 / 4220 / 5812 / 9087.
+constexpr uint32_t kSegment = 65536;
+// Table rows per bucket: 16 wavefronts' counters take 128 KB of LDS.  Fewer make more workgroups that
+// read every token: 65536 tokens into 2^20 rows 163 / 176 / 214 us with 2048 / 1024 / 512, 262144 into
+// 2^20 346 / 382 / 552; into 2^24 rows 2714 / 2307 / 2884.
+constexpr uint32_t kMaxPerBucket = 2048;
 constexpr int kPiece = 64;                // sorted positions per window of the long rows
 constexpr size_t kMaxRows = (size_t)1 << 24;
 
@@ -51,8 +59,10 @@ GroupPlan make_plan(size_t n, size_t v)
     p.v = (uint32_t)v;
     p.segments = (uint32_t)((n + kSegment - 1) / kSegment);
     if (p.segments == 0) p.segments = 1;
-    // one workgroup per compute unit; with several segments 64 buckets each fill the chip and
-    // read every token a quarter as often
+    // one workgroup per compute unit (16384 x 1024 bfloat16 into 50000 rows: 128 / 256 / 512 buckets
+    // 40.8 / 40.4 / 43.8 us, 65536 x 2048 142 / 139 / 151); with several segments 64 buckets each fill the
+    // chip and read every token a quarter as often (262144 x 1024: 32 / 64 / 256 buckets 235 / 228 / 265
+    // us, 2^20 x 256 390 / 411 / 554)
     p.log_buckets = p.segments == 1 ? 8 : 6;
     while (((v + ((size_t)1 << p.log_buckets) - 1) >> p.log_buckets) > kMaxPerBucket) ++p.log_buckets;
     p.buckets = 1u << p.log_buckets;

@@ -4,10 +4,12 @@
 // its gradient, and its form for single tokens.
 //
 // The recurrence is a scan of real affine maps h -> a h + b, as many as
-// rows x channels x states, that are made from far fewer inputs and never
-// leave the registers.  Per map: one exponential and three or four multiplies
-// or fused multiply-adds, against 1/16 of the bytes of a row: the kernels are
-// bound by the issue of vector instructions, not by memory.
+// rows x channels x states, that are made from far fewer inputs and are not
+// stored.  Per map: one exponential and three or four multiplies or fused
+// multiply-adds, against 1/16 of the bytes of a row: the kernels are bound by
+// the issue of vector instructions, not by memory.  One wavefront's
+// instruction takes 1.73 ns of its SIMD, an exponential or reciprocal 3.48
+// (measured on chains of them at full occupancy).
 //
 // Layout.  A wavefront owns 16 channels (32 in the gradient); four lanes share a channel's states, S =
 // states / 4 rounded up to 4, 8 or 16 each (Place).  The sum over a channel's states is then S - 1 adds
@@ -372,12 +374,14 @@ __device__ __forceinline__ void step_sizes(const float (&delta)[V], const float 
 // columns of 16 by four rows of 16 (a fused product of 32-bit values, exact but for its one rounding)
 // and leaves state 4 q + i of channel d in lane 16 q + d, where the recurrence wants it.  Left per row,
 // channel and state: a product and an exponential for the factor, a fused multiply-add for the state,
-// one for the output.  Counted on 16384 rows of 2048 channels: 56 vector instructions per row and 16
-// channels for 64 lanes x 4 states, the vector units busy 83% of the time.
+// one for the output.  Counted on 16384 rows of 2048 channels, per row and 16 channels (64 lanes x 4
+// states): 29 vector instructions in the output's pass, 160 us, and 19 in the totals', 98; the vector
+// units are busy 86% of the time.
 //
 // CH channels per lane: two would share what a lane reads of C, but need 248 registers (two wavefronts
 // per SIMD); one, held to 168 for three, measured 190 against 207 us on ragged prompts (6001 x 4096)
-// and the same on one prompt (16384 x 2048).
+// and the same on one prompt (16384 x 2048).  At 168 registers float32 inputs and rows without whole
+// 16-byte pieces spill 14 to 17 of them (60 to 72 bytes of scratch per lane).
 constexpr int kFwdWaveChannels = 16;
 constexpr int kFwdWaves = kWgChannels / kFwdWaveChannels;
 
@@ -709,8 +713,9 @@ struct Grads {
 
 // Backwards, g = a[t+1] dh[t+1] is what the later rows pass on to row t's state:
 //   dh = dv C + g;  g' = a dh         (dv = dy silu(z))
-// Totals of a span for the spans before it (110 us for 8192 x 4096 channels, bound as the forward pass): g at its first row from g = 0 behind its last (or from
-// dfinal where the sequence ends in it), and the sum of dt.
+// Totals of a span for the spans before it: g at its first row from g = 0 behind its last (or from
+// dfinal where the sequence ends in it), and the sum of dt.  110 us for 8192 x 4096 channels, the vector
+// units busy all the while.
 template <typename T, int S, bool VEC>
 __global__ __launch_bounds__(kGradWaves * 64) void grad_totals_kernel(Plan pl, Inputs in, Grads gr, SpanTotals totals)
 {
@@ -799,11 +804,13 @@ __global__ __launch_bounds__(kGradWaves * 64) void grad_totals_kernel(Plan pl, I
     if (me.q == 0 && me.d < me.nch) totals.dt_sum[(size_t)span * pl.channels + me.c0 + me.d] = sum;
 }
 
-// Every gradient of a span's rows.  Measured: 727 of the 1117 us of a training step (4 x 2048 x 4096
-// channels, 16 states, bfloat16); 107 vector instructions per row and 16 channels for 4 states per
-// lane keep the vector units busy 58% of the time, the matrix unit is busy 16% of it; two wavefronts
-// per SIMD (256 registers).  With one channel per lane, eight rows' factors in registers and twice
-// the matrix instructions it took 870.
+// Every gradient of a span's rows.  Measured: 697 of the 1069 us of a training step (4 x 2048 x 4096
+// channels, 16 states, bfloat16); 113 vector instructions per row and 16 channels for 4 states per
+// lane keep the vector units busy 64% of the time, the matrix unit is busy 17% of it; two wavefronts
+// per SIMD at 256 registers, 31 more of which are spilled (128 bytes of scratch per lane; 17 to 32
+// states 76 and 276, above that one wavefront per SIMD with 256 accumulation registers, 23 and 96).
+// With one channel per lane, eight rows' factors in registers and twice the matrix instructions it
+// took 870.
 //
 // Tiles are taken from the last to the first.  A tile's states
 // are recomputed from its saved one: once forwards, keeping the state in front of every kSub rows,
@@ -818,7 +825,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void grad_totals_kernel(Plan pl, I
 // instruction and one selection per row and state (a lane's channels are added up before); what is
 // left is a sum over the 4 channels of a lane row, once a tile.  (A first matrix that is 1 in one row
 // and 0 elsewhere would need no selection, but 0 times a value that is not finite would reach the
-// tile's other rows; 1114 against 1126 us.)  The wavefronts of a workgroup add theirs in LDS, the
+// tile's other rows; the training step takes 1% less with it.)  The wavefronts of a workgroup add theirs in LDS, the
 // workgroups theirs in a second launch, always in the same order.
 template <int S>
 struct Bwd {

@@ -120,15 +120,15 @@ struct Plan {
 };
 
 // Workgroups that the rows are cut for.  Measured (one prompt of 16384 x 2048 channels / ragged 6001 x
-// 4096 / training 4 x 2048 x 4096, us): 512 workgroups 278 / 215 / 1703, 768 264 / 198 / 1245, 1024 256 /
-// 194 / 1117, 2048 260 / 194 / 1107.
+// 4096 / training 4 x 2048 x 4096, us): 512 workgroups 266 / 206 / 1680, 768 257 / 193 / 1212, 1024 247 /
+// 180 / 1069, 2048 251 / 188 / 1094.
 constexpr uint32_t kTargetWorkgroups = 1024;
 // Shortest span, and the most workgroups for the sake of many short sequences (which bounds the
 // workspace).  A span's rows are walked twice and its start joins the spans before it one by one, so
 // a sequence of L rows is cut into about sqrt(L) spans at most.  Spans of at least 128 / 64 / 32 rows:
-// forward 512 rows x 2048 channels 30 / 23 / 23 us, 2048 x 1024 34 / 31 / 40 (64 spans: the joins);
-// forward and gradients 1 x 256 x 2048 150 / 91 / 71, 1 x 1024 x 2048 166 / 135 / 109; 128 rows x 2048
-// forward 20 (one launch) / 23 / 23.
+// forward 512 rows x 2048 channels 30 / 23 / 23 us, 2048 x 1024 32 / 30 / 30 (at 64 spans, without the
+// square root, 40: the joins); forward and gradients 1 x 256 x 2048 245 / 94 / 69, 1 x 1024 x 2048 169 /
+// 134 / 108; 128 rows x 2048 forward 20 (one launch) / 20 / 23.
 constexpr uint32_t kMinSpanRows = 32;
 constexpr uint32_t kMostWorkgroups = 8192;
 
