@@ -825,8 +825,8 @@ __global__ __launch_bounds__(kGradWaves * 64) void grad_totals_kernel(Plan pl, I
 // instruction and one selection per row and state (a lane's channels are added up before); what is
 // left is a sum over the 4 channels of a lane row, once a tile.  (A first matrix that is 1 in one row
 // and 0 elsewhere would need no selection, but 0 times a value that is not finite would reach the
-// tile's other rows; the training step takes 1% less with it.)  The wavefronts of a workgroup add theirs in LDS, the
-// workgroups theirs in a second launch, always in the same order.
+// tile's other rows; the training step takes 1% less with it.)  The wavefronts of a workgroup add
+// theirs in LDS, the workgroups theirs in a second launch, always in the same order.
 template <int S>
 struct Bwd {
     static constexpr int CW = S == 4 ? 32 : 16, WAVES = kWgChannels / CW;
