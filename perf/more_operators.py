@@ -162,12 +162,12 @@ def _own(s, kind):
                                 min_p=s["min_p"])
     if kind.startswith("experts"):
         plan = dw.expert_split(s["experts"], s["e"])
-        rows = dw.expert_dispatch(s["x"], plan.places)
-        out = dw.expert_combine(s["y"], plan.places, s["weights"])
+        rows = dw.expert_dispatch(s["x"], plan)
+        out = dw.expert_combine(s["y"], plan, s["weights"])
         if kind == "experts":
             return plan.offsets, plan.places, plan.source, rows, out
-        g = dw.expert_combine_grad(s["dout"], s["y"], plan.places, s["weights"])
-        dx = dw.expert_dispatch_grad(s["drows"], plan.places)
+        g = dw.expert_combine_grad(s["dout"], s["y"], plan, s["weights"])
+        dx = dw.expert_dispatch_grad(s["drows"], plan)
         return plan.offsets, plan.places, plan.source, rows, out, g.dy, g.dweights, dx
     args = (s["x"], s["decay_gate"], s["input_gate"], s["rate"])
     if kind == "gate_step":
