@@ -25,10 +25,12 @@ EXPORTS = ("scan_inclusive", "scan_exclusive", "segmented_scan", "compact", "sca
            "scan_get_device_error", "scan_release_workspace", "scan_set_small_n_max",
            "scan_set_spin_limit", "scan_set_multi_tile_mode", "scan_copy_probe", "csr_row_offsets",
            "radix_split", "scan_noalloc",
-           # dwpt_seq.h, bound in sequence.py
+           # dwpt_seq.h, bound in sequence.py, experts.py and sampling.py
            "embedding_lookup", "embedding_grad", "embedding_grad_workspace", "causal_conv1d", "causal_conv1d_grad",
            "causal_conv1d_grad_workspace", "causal_conv1d_step", "selective_scan", "selective_scan_workspace",
-           "selective_scan_saved", "selective_scan_grad", "selective_scan_grad_workspace", "selective_scan_step")
+           "selective_scan_saved", "selective_scan_grad", "selective_scan_grad_workspace", "selective_scan_step",
+           "gated_scan", "gated_scan_workspace", "gated_scan_saved", "gated_scan_grad", "gated_scan_grad_workspace", "gated_scan_step",
+           "expert_split", "expert_split_workspace", "expert_dispatch", "expert_combine", "expert_combine_grad", "sample_tokens")
 
 _lib = None
 

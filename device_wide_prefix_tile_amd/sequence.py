@@ -1,6 +1,6 @@
 """Sequence-model operators over torch tensors: embedding lookup and its gradient by sorted
-tokens, the short causal convolution and the selective state-space scan, with their gradients
-and their single-token forms (C ABI in include/dwpt_seq.h).
+tokens, the short causal convolution, the selective state-space scan and the gated linear
+recurrence, with their gradients and their single-token forms (C ABI in include/dwpt_seq.h).
 
 Argument marshalling only, as in ``binding``: every step runs in the library's HIP kernels, calls
 enqueue on the current stream of the tensors' device (or on ``stream``) and return without
@@ -68,6 +68,27 @@ class _ScanStepArgs(ctypes.Structure):
                 + [("state", _P), ("y", _P), ("y_stride", _I64)])
 
 
+_GATED_INPUTS = [("channels", _U32), ("reserved2", _U32), ("x", _P), ("x_stride", _I64), ("decay_gate", _P), ("decay_stride", _I64),
+                 ("input_gate", _P), ("input_stride", _I64), ("rate", _P)]
+
+
+class _GatedArgs(ctypes.Structure):
+    _fields_ = ([("dtype", _I), ("reserved", _I), ("rows", _U64), ("seqs", _U64), ("seq_offsets", _P)] + _GATED_INPUTS
+                + [("initial_state", _P), ("y", _P), ("y_stride", _I64), ("final_state", _P), ("saved", _P),
+                   ("workspace", _P), ("workspace_bytes", _U64)])
+
+
+class _GatedGradArgs(ctypes.Structure):
+    _fields_ = [("args", _GatedArgs), ("dy", _P), ("dy_stride", _I64), ("dfinal_state", _P), ("dx", _P), ("dx_stride", _I64),
+                ("ddecay_gate", _P), ("ddecay_stride", _I64), ("dinput_gate", _P), ("dinput_stride", _I64), ("drate", _P),
+                ("dinitial_state", _P)]
+
+
+class _GatedStepArgs(ctypes.Structure):
+    _fields_ = ([("dtype", _I), ("reserved", _I), ("rows", _U64), ("n_slots", _U64), ("slots", _P)] + _GATED_INPUTS
+                + [("state", _P), ("y", _P), ("y_stride", _I64)])
+
+
 SIGNATURES = {
     "embedding_lookup": ([_I, _P, _I, _U64, _P, _I64, _U64, _U32, ctypes.c_float, _P, _P], _I),
     "embedding_grad": ([_I, _I, _P, _I, _U64, _P, _I64, _U64, _U32, ctypes.c_float, _I, _P, _P, _U64, _P], _I),
@@ -82,9 +103,20 @@ SIGNATURES = {
     "selective_scan_grad": ([ctypes.POINTER(_ScanGradArgs), _P], _I),
     "selective_scan_grad_workspace": ([ctypes.POINTER(_ScanGradArgs)], _U64),
     "selective_scan_step": ([ctypes.POINTER(_ScanStepArgs), _P], _I),
+    "gated_scan": ([ctypes.POINTER(_GatedArgs), _P], _I),
+    "gated_scan_workspace": ([ctypes.POINTER(_GatedArgs)], _U64),
+    "gated_scan_saved": ([ctypes.POINTER(_GatedArgs)], _U64),
+    "gated_scan_grad": ([ctypes.POINTER(_GatedGradArgs), _P], _I),
+    "gated_scan_grad_workspace": ([ctypes.POINTER(_GatedArgs)], _U64),
+    "gated_scan_step": ([ctypes.POINTER(_GatedStepArgs), _P], _I),
 }
 
 _seq_lib = None
+
+
+def _register(signatures):
+    """Adds another module's functions of the library."""
+    SIGNATURES.update(signatures)
 
 
 def _lib():
@@ -597,6 +629,130 @@ def selective_scan_step(x: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, B
     def call(handle):
         y, a.y, a.y_stride = _out(out, x, "out")
         _check(_lib().selective_scan_step(ctypes.byref(a), handle), "selective_scan_step")
+        return y
+
+    return _enqueue(x, stream, call)
+
+
+# ---------------------------------------------------------------------- gated recurrence
+class GatedGrads(NamedTuple):
+    """Gradients of gated_scan; drate and dinitial_state are float32, dinitial_state None where the input was."""
+    dx: torch.Tensor
+    ddecay_gate: torch.Tensor
+    dinput_gate: torch.Tensor
+    drate: torch.Tensor
+    dinitial_state: Optional[torch.Tensor]
+
+
+def _gated_inputs(x, decay_gate, input_gate, rate):
+    """The fields of _GATED_INPUTS."""
+    shape, device, t = x.shape, x.get_device(), x.dtype
+    d = shape[-1]
+    return (d, 0, x.data_ptr(), _rows(x, "x"), *_like(decay_gate, "decay_gate", shape, t, device, d),
+            *_like(input_gate, "input_gate", shape, t, device, d), _plain(rate, "rate", (d,), torch.float32, device))
+
+
+def _gated_args(x, decay_gate, input_gate, rate, seq_offsets, initial_state):
+    _x(x)
+    rows, seqs, offsets = _lengths(x, seq_offsets)
+    state = (seqs, x.shape[-1])
+    return _GatedArgs(_DTYPE[x.dtype], 0, rows, seqs, offsets, *_gated_inputs(x, decay_gate, input_gate, rate),
+                      _plain(initial_state, "initial_state", state, torch.float32, x.get_device())), state
+
+
+def gated_scan(x: torch.Tensor, decay_gate: torch.Tensor, input_gate: torch.Tensor, rate: torch.Tensor,
+               seq_offsets: Optional[torch.Tensor] = None, initial_state: Optional[torch.Tensor] = None, final_state=None,
+               save_for_grad: bool = False, out: Optional[torch.Tensor] = None, stream=None):
+    """Gated linear recurrence along every sequence, per channel d:
+
+        a = exp(rate[d] sigmoid(decay_gate[t, d]))
+        h[t] = a h[t-1] + sqrt(1 - a^2) sigmoid(input_gate[t, d]) x[t, d],  y[t] = h[t]
+
+    x, decay_gate, input_gate: (B, L, D), or (rows, D) with seq_offsets, all of x's type.  rate (D,), not above
+    zero, and the states (S, D) are float32.  initial_state: h before every sequence (default zero).
+    final_state: a tensor for h after every sequence, or True for a new one.  save_for_grad: also return the
+    states that ``gated_scan_grad`` starts from.  Returns y, followed by what was asked for.  Rows of y that
+    belong to no sequence are not written (in a new y they hold whatever the memory held)."""
+    a, state = _gated_args(x, decay_gate, input_gate, rate, seq_offsets, initial_state)
+
+    def call(handle):
+        L = _lib()
+        y, a.y, a.y_stride = _out(out, x, "out")
+        got = [y]
+        fin, a.final_state = _optional_state(final_state, "final_state", state, torch.float32, x)
+        if fin is not None:
+            got.append(fin)
+        if save_for_grad:
+            saved = torch.empty(L.gated_scan_saved(ctypes.byref(a)), dtype=torch.float32, device=x.device)
+            a.saved = saved.data_ptr()
+            got.append(saved)
+        need = L.gated_scan_workspace(ctypes.byref(a))
+        ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+        a.workspace, a.workspace_bytes = ws.data_ptr(), need
+        _check(L.gated_scan(ctypes.byref(a), handle), "gated_scan")
+        return y if len(got) == 1 else tuple(got)
+
+    return _enqueue(x, stream, call)
+
+
+def gated_scan_grad(dy: torch.Tensor, x: torch.Tensor, decay_gate: torch.Tensor, input_gate: torch.Tensor, rate: torch.Tensor,
+                    seq_offsets: Optional[torch.Tensor] = None, initial_state: Optional[torch.Tensor] = None,
+                    dfinal_state: Optional[torch.Tensor] = None, saved: Optional[torch.Tensor] = None,
+                    dx: Optional[torch.Tensor] = None, ddecay_gate: Optional[torch.Tensor] = None,
+                    dinput_gate: Optional[torch.Tensor] = None, stream=None) -> GatedGrads:
+    """Gradients of ``gated_scan`` (its arguments) for dy, and for dfinal_state if given.
+
+    saved: what ``gated_scan(..., save_for_grad=True)`` returned for the same inputs; without it the states
+    are scanned again.  dx, ddecay_gate and dinput_gate may be given to write into (slices of one tensor, say);
+    their rows that belong to no sequence are not written then, and are zero otherwise."""
+    a, state = _gated_args(x, decay_gate, input_gate, rate, seq_offsets, initial_state)
+    g = _GatedGradArgs(a, *_like(dy, "dy", x.shape, x.dtype, x.get_device(), x.shape[-1]),
+                       _plain(dfinal_state, "dfinal_state", state, torch.float32, x.get_device()))
+
+    def call(handle):
+        L = _lib()
+        f32 = dict(dtype=torch.float32, device=x.device)
+        need_saved = L.gated_scan_saved(ctypes.byref(a))
+        states = saved
+        if states is None:
+            states = torch.empty(need_saved, **f32)
+            need = L.gated_scan_workspace(ctypes.byref(a))
+            ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+            a.saved, a.workspace, a.workspace_bytes = states.data_ptr(), ws.data_ptr(), need
+            _check(L.gated_scan(ctypes.byref(a), handle), "gated_scan")
+        a.saved = _plain(states, "saved", (need_saved,), torch.float32, x.get_device())
+        g.args = a
+        new = _new_rows(seq_offsets)
+        ox, g.dx, g.dx_stride = _out(dx, x, "dx", new)
+        od, g.ddecay_gate, g.ddecay_stride = _out(ddecay_gate, x, "ddecay_gate", new)
+        oi, g.dinput_gate, g.dinput_stride = _out(dinput_gate, x, "dinput_gate", new)
+        orate = torch.empty(rate.shape, **f32)
+        oinit = None if initial_state is None else torch.empty(state, **f32)
+        g.drate, g.dinitial_state = orate.data_ptr(), _ptr(oinit)
+        need = L.gated_scan_grad_workspace(ctypes.byref(a))
+        ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+        g.args.workspace, g.args.workspace_bytes = ws.data_ptr(), need
+        _check(L.gated_scan_grad(ctypes.byref(g), handle), "gated_scan_grad")
+        return GatedGrads(ox, od, oi, orate, oinit)
+
+    return _enqueue(x, stream, call)
+
+
+def gated_scan_step(x: torch.Tensor, decay_gate: torch.Tensor, input_gate: torch.Tensor, rate: torch.Tensor, state: torch.Tensor,
+                    slots: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, stream=None):
+    """One token per row: one step of ``gated_scan``'s recurrence from state[slots[i]], which is updated in place.
+
+    x, decay_gate, input_gate: (rows, D); state: (n_slots, D) float32.  slots as in ``causal_conv1d_step``."""
+    _x(x)
+    if x.dim() != 2 or state.dim() != 2:
+        raise ValueError("x must be (rows, D), state (n_slots, D)")
+    n = state.shape[0]
+    a = _GatedStepArgs(_DTYPE[x.dtype], 0, x.shape[0], n, _slots(x, slots, n), *_gated_inputs(x, decay_gate, input_gate, rate),
+                       _plain(state, "state", (n, x.shape[1]), torch.float32, x.get_device()))
+
+    def call(handle):
+        y, a.y, a.y_stride = _out(out, x, "out")
+        _check(_lib().gated_scan_step(ctypes.byref(a), handle), "gated_scan_step")
         return y
 
     return _enqueue(x, stream, call)

@@ -1,8 +1,9 @@
 /*
  * dwpt_seq.h -- C ABI of the sequence-model operators of libdwpt_scan.so:
  * embedding lookup and its gradient by sorted tokens, the short causal
- * convolution and the selective state-space scan, each with its gradient and
- * (convolution, scan) its form for single tokens.
+ * convolution, the selective state-space scan and the gated linear recurrence,
+ * each with its gradient and (all but the embedding) its form for single
+ * tokens; tokens sorted by expert and back, with gradients; sampling of tokens.
  *
  * The selective scan is the affine recurrence of SCAN_OP_AFFINE over real
  * maps, one per channel and state, made from the inputs on the way in and
@@ -261,6 +262,188 @@ typedef struct {
     int64_t y_stride;
 } selective_scan_step_args_t;
 scan_status_t selective_scan_step(const selective_scan_step_args_t* args, void* stream);
+
+/*
+ * Gated linear recurrence.  For every channel d of a sequence:
+ *   a[t] = exp(rate[d] * sigmoid(decay_gate[t][d]))
+ *   h[t] = a[t] * h[t-1] + sqrt(1 - a[t]^2) * sigmoid(input_gate[t][d]) * x[t][d],   y[t] = h[t]
+ * h before the first row is initial_state[s] (NULL: zeros); final_state[s] (may be NULL) receives h after the
+ * last row (initial_state where the sequence is empty).  x, decay_gate, input_gate, y: dtype; rate (channels),
+ * not above 0 (a above 1 gives NaN), and the states (seqs x channels): float32, contiguous.  saved (may be NULL)
+ * receives gated_scan_saved() float32 values, the states that gated_scan_grad starts from.  y may be NULL if only
+ * the states are wanted.
+ */
+typedef struct {
+    int32_t dtype, reserved;
+    uint64_t rows, seqs;
+    const int32_t* seq_offsets;
+    uint32_t channels, reserved2;
+    const void* x;
+    int64_t x_stride;
+    const void* decay_gate;
+    int64_t decay_stride;
+    const void* input_gate;
+    int64_t input_stride;
+    const float* rate;
+    const float* initial_state;
+    void* y;
+    int64_t y_stride;
+    float* final_state;
+    float* saved;
+    void* workspace;
+    uint64_t workspace_bytes;
+} gated_scan_args_t;
+scan_status_t gated_scan(const gated_scan_args_t* args, void* stream);
+size_t gated_scan_workspace(const gated_scan_args_t* args);
+size_t gated_scan_saved(const gated_scan_args_t* args);
+
+/*
+ * Gradients of gated_scan for dy (and dfinal_state, may be NULL: zeros).  `args` are the forward call's, with
+ * `saved` as it left it; y and final_state are not used, workspace is this call's.  dx, ddecay_gate and
+ * dinput_gate of dtype; drate (summed over all rows) and dinitial_state (may be NULL) float32.  Where
+ * 1 - a^2 is 0 in 32 bits (no decay), the derivative of its root is taken as 0.
+ */
+typedef struct {
+    gated_scan_args_t args;
+    const void* dy;
+    int64_t dy_stride;
+    const float* dfinal_state;
+    void* dx;
+    int64_t dx_stride;
+    void* ddecay_gate;
+    int64_t ddecay_stride;
+    void* dinput_gate;
+    int64_t dinput_stride;
+    float* drate;
+    float* dinitial_state;
+} gated_scan_grad_args_t;
+scan_status_t gated_scan_grad(const gated_scan_grad_args_t* args, void* stream);
+size_t gated_scan_grad_workspace(const gated_scan_args_t* args);
+
+/*
+ * One token per row: one step of the recurrence from state[slots[i]] (n_slots x channels float32, contiguous,
+ * updated in place).  slots as in causal_conv1d_step; rows < 2^31.
+ */
+typedef struct {
+    int32_t dtype, reserved;
+    uint64_t rows, n_slots;
+    const int32_t* slots;
+    uint32_t channels, reserved2;
+    const void* x;
+    int64_t x_stride;
+    const void* decay_gate;
+    int64_t decay_stride;
+    const void* input_gate;
+    int64_t input_stride;
+    const float* rate;
+    float* state;
+    void* y;
+    int64_t y_stride;
+} gated_scan_step_args_t;
+scan_status_t gated_scan_step(const gated_scan_step_args_t* args, void* stream);
+
+/*
+ * Tokens sorted by expert and back.  A token's choices are `choices` expert numbers; those outside
+ * 0 .. n_experts - 1 go to no expert.
+ *
+ * expert_split: the stable split of n choices (token by token) by expert.  offsets (n_experts + 1): expert e has
+ * rows [offsets[e], offsets[e+1]) of the experts' order, its choices in ascending order; places (n): the row of every
+ * choice, -1 where it has no expert; source (n): the choice of every row, -1 from row offsets[n_experts] on.
+ * n < 2^31, n_experts <= 1024.
+ */
+scan_status_t expert_split(const int32_t* experts, size_t n, uint32_t n_experts, int32_t* offsets, int32_t* places,
+                           int32_t* source, void* workspace, size_t workspace_bytes, void* stream);
+size_t expert_split_workspace(size_t n, uint32_t n_experts);
+
+/*
+ * expert_dispatch: out[places[t][j]] = x[t] for every token t and choice j; places outside 0 .. rows - 1 are
+ * skipped (here and below), a row that two choices lead to holds either's.  used (device memory, may be NULL: offsets +
+ * n_experts): the rows from *used on are set to zero; other rows that no choice leads to are left as they were.
+ * x: tokens x channels, out: rows x channels; choices <= 256, tokens * choices < 2^31.  The gradient of x is
+ * expert_combine without weights.
+ */
+typedef struct {
+    int32_t dtype, reserved;
+    uint64_t tokens, rows;
+    uint32_t choices, channels;
+    const int32_t* places;
+    const int32_t* used;
+    const void* x;
+    int64_t x_stride;
+    void* out;
+    int64_t out_stride;
+} expert_dispatch_args_t;
+scan_status_t expert_dispatch(const expert_dispatch_args_t* args, void* stream);
+
+/*
+ * expert_combine: out[t] = the sum over j of weights[t][j] * y[places[t][j]], in the order of j.  weights (tokens x
+ * choices, contiguous, weight_dtype: dtype or SEQ_F32) may be NULL: ones.
+ */
+typedef struct {
+    int32_t dtype, weight_dtype;
+    uint64_t tokens, rows;
+    uint32_t choices, channels;
+    const int32_t* places;
+    const void* weights;
+    const void* y;
+    int64_t y_stride;
+    void* out;
+    int64_t out_stride;
+} expert_combine_args_t;
+scan_status_t expert_combine(const expert_combine_args_t* args, void* stream);
+
+/*
+ * Gradients of expert_combine: dy[places[t][j]] = weights[t][j] * dout[t] (used as in expert_dispatch), and
+ * dweights[t][j] (tokens x choices float32; may be NULL, y may be NULL then) = the sum over the channels of dout[t] *
+ * y[places[t][j]], 0 where there is no place.
+ */
+typedef struct {
+    int32_t dtype, weight_dtype;
+    uint64_t tokens, rows;
+    uint32_t choices, channels;
+    const int32_t* places;
+    const int32_t* used;
+    const void* weights;
+    const void* dout;
+    int64_t dout_stride;
+    const void* y;
+    int64_t y_stride;
+    void* dy;
+    int64_t dy_stride;
+    float* dweights;
+} expert_combine_grad_args_t;
+scan_status_t expert_combine_grad(const expert_combine_grad_args_t* args, void* stream);
+
+/*
+ * Sampling from given random numbers: tokens[r] for every row of logits (rows x n, n <= 2^19).  With settings
+ * from the row's own temperature, top_k, top_p and min_p (device memory, rows values each) or, where that is NULL, the
+ * call's:
+ *   weights w[i] = exp((logits[r][i] - max) / temperature); minus infinity and NaN weigh nothing, and
+ *   next to a plus infinity only those weigh
+ *   tokens by falling logit, equal ones by ascending index, of which are kept
+ *     the first top_k (<= 0: all); of these the first whose predecessors' weights add up to less than
+ *     top_p times the weight of them all, and at least one; and those with w >= min_p (at most 1)
+ *   tokens[r] = the first kept i, by ascending index, up to which the kept weights add up to more than
+ *     uniform[r] times the kept weight (uniform outside [0, 1): the first or the last)
+ * A temperature that is not above 0 takes the first largest logit.  A row without a finite or plus infinite
+ * logit gives -1.  Weights are held in 32 bits, their sums in 64.  tokens: int32 (token_bytes 4) or int64 (8).
+ */
+typedef struct {
+    int32_t dtype, token_bytes;
+    uint64_t rows;
+    uint32_t n, reserved;
+    const void* logits;
+    int64_t logits_stride;
+    const float* uniform;
+    const float* temperatures;
+    const int32_t* top_ks;
+    const float* top_ps;
+    const float* min_ps;
+    double temperature, top_p, min_p;
+    int64_t top_k;
+    void* tokens;
+} sample_tokens_args_t;
+scan_status_t sample_tokens(const sample_tokens_args_t* args, void* stream);
 
 #ifdef __cplusplus
 }

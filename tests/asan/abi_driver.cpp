@@ -48,6 +48,21 @@ static void seq_host_checks(uint32_t* buf)
     EXPECT(selective_scan_workspace(&a) == 0 && selective_scan_saved(&a) == 0);
     EXPECT(selective_scan_grad(nullptr, nullptr) == SCAN_ERR_INVALID);
     EXPECT(selective_scan_step(nullptr, nullptr) == SCAN_ERR_INVALID);
+    gated_scan_args_t g{};
+    EXPECT(gated_scan(&g, nullptr) == SCAN_ERR_INVALID);  // no channels
+    EXPECT(gated_scan_workspace(&g) == 0 && gated_scan_saved(&g) == 0 && gated_scan_grad_workspace(nullptr) == 0);
+    EXPECT(gated_scan_grad(nullptr, nullptr) == SCAN_ERR_INVALID && gated_scan_step(nullptr, nullptr) == SCAN_ERR_INVALID);
+    int32_t* ints = reinterpret_cast<int32_t*>(buf);
+    EXPECT(expert_split(ints, 4, 4, ints + 8, ints + 4, ints + 16, nullptr, 0, nullptr) == SCAN_ERR_INVALID);  // no workspace
+    EXPECT(expert_split_workspace(100000, 64) >= 64 * 25 * 4);
+    expert_dispatch_args_t d{};
+    EXPECT(expert_dispatch(&d, nullptr) == SCAN_ERR_INVALID);
+    expert_combine_args_t m{};
+    m.choices = m.channels = 1;
+    EXPECT(expert_combine(&m, nullptr) == SCAN_OK);  // no tokens
+    EXPECT(expert_combine_grad(nullptr, nullptr) == SCAN_ERR_INVALID);
+    sample_tokens_args_t t{};
+    EXPECT(sample_tokens(&t, nullptr) == SCAN_ERR_INVALID);
 }
 
 static void host_checks()
@@ -171,6 +186,107 @@ static void seq_device_checks(hipStream_t st)
     for (void* p : mem) HIPCHECK(hipFree(p));
 }
 
+// A recurrent layer with experts and the next tokens on a stream: gated scan and back, a split of every row to two
+// experts, their rows out and in, and a sampled channel per row.
+static void recurrent_device_checks(hipStream_t st)
+{
+    const uint32_t rows = 400, seqs = 2, d = 72, e = 5, k = 2;
+    std::vector<int32_t> experts(rows * k);
+    for (uint32_t i = 0; i < rows * k; ++i) experts[i] = (int32_t)(i * 7 % (e + 1));  // some of no expert
+    std::vector<float> ones(rows * d, 1.0f), rate(d, -0.5f);
+    std::vector<void*> mem;
+    const auto dev = [&](const void* src, size_t bytes) {
+        void* p = nullptr;
+        HIPCHECK(hipMalloc(&p, bytes));
+        mem.push_back(p);
+        if (src)
+            HIPCHECK(hipMemcpy(p, src, bytes, hipMemcpyHostToDevice));
+        else
+            HIPCHECK(hipMemset(p, 0, bytes));
+        return p;
+    };
+    const size_t big = rows * d * 4;
+    gated_scan_grad_args_t g{};
+    gated_scan_args_t& a = g.args;
+    a.rows = rows;
+    a.seqs = seqs;
+    a.channels = d;
+    a.x = a.decay_gate = a.input_gate = dev(ones.data(), big);
+    a.x_stride = a.decay_stride = a.input_stride = a.y_stride = d;
+    a.rate = (const float*)dev(rate.data(), d * 4);
+    a.y = dev(nullptr, big);
+    a.saved = (float*)dev(nullptr, gated_scan_saved(&a) * 4);
+    a.workspace_bytes = gated_scan_workspace(&a);
+    a.workspace = dev(nullptr, a.workspace_bytes);
+    EXPECT(gated_scan(&a, st) == SCAN_OK);
+    g.dy = a.y;
+    g.dx = dev(nullptr, big);
+    g.ddecay_gate = dev(nullptr, big);
+    g.dinput_gate = dev(nullptr, big);
+    g.dy_stride = g.dx_stride = g.ddecay_stride = g.dinput_stride = d;
+    g.drate = (float*)dev(nullptr, d * 4);
+    a.workspace_bytes = gated_scan_grad_workspace(&a);
+    a.workspace = dev(nullptr, a.workspace_bytes);
+    EXPECT(gated_scan_grad(&g, st) == SCAN_OK);
+
+    int32_t *choices = (int32_t*)dev(experts.data(), experts.size() * 4), *offsets = (int32_t*)dev(nullptr, (e + 1) * 4);
+    int32_t *places = (int32_t*)dev(nullptr, rows * k * 4), *source = (int32_t*)dev(nullptr, rows * k * 4);
+    const size_t need = expert_split_workspace(rows * k, e);
+    EXPECT(expert_split(choices, rows * k, e, offsets, places, source, dev(nullptr, need), need, st) == SCAN_OK);
+    expert_dispatch_args_t x{};
+    x.tokens = rows;
+    x.rows = rows * k;
+    x.choices = k;
+    x.channels = d;
+    x.places = places;
+    x.used = offsets + e;
+    x.x = a.y;
+    x.out = dev(nullptr, k * big);
+    x.x_stride = x.out_stride = d;
+    EXPECT(expert_dispatch(&x, st) == SCAN_OK);
+    expert_combine_args_t c{};
+    c.tokens = rows;
+    c.rows = rows * k;
+    c.choices = k;
+    c.channels = d;
+    c.places = places;
+    c.y = x.out;
+    c.out = dev(nullptr, big);
+    c.y_stride = c.out_stride = d;
+    EXPECT(expert_combine(&c, st) == SCAN_OK);
+    expert_combine_grad_args_t q{};
+    q.tokens = rows;
+    q.rows = rows * k;
+    q.choices = k;
+    q.channels = d;
+    q.places = places;
+    q.used = offsets + e;
+    q.dout = c.out;
+    q.y = x.out;
+    q.dy = dev(nullptr, k * big);
+    q.dout_stride = q.y_stride = q.dy_stride = d;
+    q.dweights = (float*)dev(nullptr, rows * k * 4);
+    EXPECT(expert_combine_grad(&q, st) == SCAN_OK);
+    sample_tokens_args_t t{};
+    t.token_bytes = 4;
+    t.rows = rows;
+    t.n = d;
+    t.logits = c.out;
+    t.logits_stride = d;
+    t.uniform = (const float*)dev(nullptr, rows * 4);
+    t.temperature = t.top_p = 1.0;
+    t.tokens = source;
+    EXPECT(sample_tokens(&t, st) == SCAN_OK);
+    HIPCHECK(hipStreamSynchronize(st));
+    int32_t first = -1, used = 0;  // equal channels and a random number of 0: token 0
+    HIPCHECK(hipMemcpy(&first, source, 4, hipMemcpyDeviceToHost));
+    HIPCHECK(hipMemcpy(&used, offsets + e, 4, hipMemcpyDeviceToHost));
+    int32_t want = 0;
+    for (int32_t v : experts) want += v < (int32_t)e;
+    EXPECT(first == 0 && used == want);
+    for (void* p : mem) HIPCHECK(hipFree(p));
+}
+
 static void device_checks()
 {
     int ndev = 0;
@@ -229,6 +345,7 @@ static void device_checks()
         EXPECT(scan_release_workspace() == SCAN_OK);
     }
     for (int i = 0; i < 2; ++i) seq_device_checks(s[i]);
+    for (int i = 0; i < 2; ++i) recurrent_device_checks(s[i]);
     HIPCHECK(hipFree(x));
     HIPCHECK(hipFree(y));
     HIPCHECK(hipFree(cnt));
