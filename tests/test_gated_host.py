@@ -76,12 +76,12 @@ def test_step_refusals(L):
 def test_sizes(L):
     """One tile of rows waits for nothing; more of them hold a map per channel and tile."""
     ws = lambda **kw: L.gated_scan_workspace(ctypes.byref(args(**kw)))  # noqa: E731
-    assert ws() == 256 and ws(rows=64) == 256
-    assert ws(rows=130) >= 3 * 256 * 8
+    assert ws() == 256 and ws(rows=128) == 256
+    assert ws(rows=130) >= 4 * 256 * 8  # two sequences of 65 rows: two tiles each
     assert ws(rows=33) == 0
-    assert L.gated_scan_saved(ctypes.byref(args(rows=130))) == 3 * 8 * 256
+    assert L.gated_scan_saved(ctypes.byref(args(rows=130))) == 4 * 8 * 256
     assert L.gated_scan_saved(ctypes.byref(args(rows=0, seqs=0, x=None, decay_gate=None, input_gate=None))) == 0
-    assert L.gated_scan_grad_workspace(ctypes.byref(args(rows=130))) >= ws(rows=130) + 3 * 256 * 4
+    assert L.gated_scan_grad_workspace(ctypes.byref(args(rows=130))) >= ws(rows=130) + 4 * 256 * 4
     # no sequences is a call where offsets say so
     assert L.gated_scan_workspace(ctypes.byref(args(seqs=0, seq_offsets=16 * MB))) > 0
 

@@ -56,7 +56,7 @@ def named(g):
     return r
 
 
-# 64 rows to a tile, 16 tiles to a group
+# 64 rows to a tile, 8 tiles to a group
 LENGTHS = [[1], [2, 0, 31, 1], [0, 0], [64], [65], [33, 64, 5], [128, 0, 64], [130], [7, 120, 1, 0, 47, 300], [1024], [1025, 3],
            [5, 2200], [640, 640, 1100]]
 
@@ -105,6 +105,25 @@ def test_batch(t, b, l, d):
     out = torch.full((b, l, d + 5), 3.0, dtype=t, device="cuda")
     dw.gated_scan(*v, initial_state=init, out=out[..., :d])
     assert torch.equal(out[..., :d], y) and (out[..., d:] == 3.0).all()
+
+
+@pytest.mark.parametrize("t", list(T))
+@pytest.mark.parametrize("b,l,d", [(260, 130, 24), (128, 65, 200), (33, 200, 1030), (256, 128, 3)])
+def test_many_sequences_at_once(t, b, l, d):
+    """Enough sequences that workgroups walk through whole ones in the gradient; last tiles of one to all rows."""
+    rng = np.random.default_rng(b + l + d)
+    t = T[t]
+    v = inputs(rng, (b, l), d, t, strided=True)
+    dy, init, dfin = randn(rng, b, l, d, t=t), randn(rng, b, d), randn(rng, b, d)
+    want = reference(v, ref.ranges(v[0].shape, None), init, dy, dfin)
+    y, fin, saved = dw.gated_scan(*v, initial_state=init, final_state=True, save_for_grad=True)
+    check(dict(y=y, final=fin), want, "many")
+    g = dw.gated_scan_grad(dy, *v, initial_state=init, dfinal_state=dfin, saved=saved)
+    check(named(g), want, "many")
+    bare = reference(v, ref.ranges(v[0].shape, None), None, dy)
+    check(named(dw.gated_scan_grad(dy, *v)), bare, "many, no states")
+    for p, q in zip(g, dw.gated_scan_grad(dy, *v, initial_state=init, dfinal_state=dfin, saved=saved)):
+        assert torch.equal(p, q)
 
 
 def test_many_short_sequences():
