@@ -1,16 +1,25 @@
 // Sampling of tokens with temperature, top-k, top-p and min-p from given random numbers.
 //
-// One workgroup per row.  With w[i] = exp((logit[i] - max) / temperature), the tokens by falling logit (equal
-// ones by ascending index) have a first part that top-k, top-p and min-p leave; the sampled token
-// is the first kept one in the order of the indices up to which the kept weights exceed uniform times
-// their sum: a scan of the row, of which only the path to one element is needed.
+// One workgroup per row, which it reads once for every pass over it: from the caches but for the first.  (Held in
+// registers, 64 of them for 128000 logits of 16 bits, every pass is unrolled over all pieces, and the instructions
+// come from memory instead: 256 x 128000 top-k 56 us against 36.)  With w[i] = exp((logit[i] - max) / temperature), the
+// tokens by falling logit (equal ones by ascending index) have a first part that top-k, top-p and min-p leave; the
+// sampled token is the first kept one in the order of the indices up to which the kept weights exceed uniform
+// times their sum: a scan of the row, of which only the path to one element is needed.
 //
-// The border of the first part is found without a sort.  Counts or weights go into bins by the logit's
+// top-k up to kMostSorted: the k-th largest of the threads' largest logits bounds the k-th largest of the row
+// from below, and hardly more than k logits reach it.  They go to LDS, are sorted, cut by top-k, top-p and
+// min-p, sorted by index and scanned.
+//
+// Otherwise the border of the first part is found without a sort.  Counts or weights go into bins by the logit's
 // distance from the largest (kPerOctave bins for every halving of the weight), a prefix over the bins gives
-// the bin in which the limit is met, and the few logits in that bin are told apart by eight bits of
-// their value at a time.  Weights are integers there (multiples of 2^-44), so that the order in which
-// LDS atomics add them up does not matter: 2^19 of them fit 64 bits.  The final sums are of fixed order,
-// in 32 bits over the elements of a 16-byte piece and in 64 bits beyond.
+// the bin in which the limit is met, and the few logits in that bin are ranked against one another (many: told apart by
+// eight bits of their value at a time).  Weights so small that all of the row's tokens with such weights could not hold the share that
+// top-p leaves out are only added up.
+//
+// Weights are integers there (multiples of 2^-44), so that the order in which LDS atomics add them up does not matter:
+// 2^19 of them fit 64 bits.  The final sums over a row are of fixed order, in 32 bits over a wavefront's 64 pieces of
+// 16 bytes and in 64 bits beyond.
 #include <cfloat>
 #include <cmath>
 
@@ -25,6 +34,7 @@ constexpr int kWaves = kBlock / 64;
 constexpr int kBins = 2 * kBlock;
 constexpr float kPerOctave = 32.0f;  // the last bin holds weights below 2^-64, which are 0 as multiples of 2^-44
 constexpr uint32_t kList = 4096;     // logits of the bin with the border that are kept in LDS; more are looked up in the row
+constexpr uint32_t kRanked = 64;     // of them, every one is compared with every other one
 constexpr int kMostSums = (kMaxTokens / 4 + 1 + kBlock - 1) / kBlock * kWaves;
 
 struct Settings {
@@ -34,8 +44,12 @@ struct Settings {
     int64_t top_k;
 };
 
+constexpr uint32_t kSorted = 2 * kBlock;  // logits that are sorted in LDS
+// Largest top-k that is sorted: the bound from 1024 threads' largest logits leaves 0.6% of a row for 512 of them, 3% for 1000.
+constexpr int64_t kMostSorted = kBlock / 2;
+
 struct Shared {
-    uint64_t bins[kBins];
+    uint64_t bins[kBins];  // also the logits that are sorted
     float list_logit[kList];
     uint32_t list_index[kList];
     double sums[kMostSums];
@@ -63,16 +77,61 @@ struct Row {
     }
     // Index of element e of piece q; wraps around to a large number in front of the row.
     __device__ uint32_t index(uint32_t q, int e) const { return q * V + (uint32_t)e - off; }
-    __device__ void load(uint32_t q, float (&f)[V]) const
+    __device__ Pack<T, V> load(uint32_t q) const
     {
         const uint32_t i = index(q, 0);
-        if (i < n && n - i >= (uint32_t)V) {
-            unpack(load_pack<T, V>(p + i), f);
-        } else {
+        if (i < n && n - i >= (uint32_t)V) return load_pack<T, V>(p + i);
+        Pack<T, V> f;
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const uint32_t k = index(q, e);
-                f[e] = k < n ? (float)p[k] : -INFINITY;
+        for (int e = 0; e < V; ++e) {
+            const uint32_t k = index(q, e);
+            f.v[e] = k < n ? p[k] : (T)-INFINITY;
+        }
+        return f;
+    }
+};
+
+// Logits in 32 bits; NaN becomes minus infinity (the maximum of a number and NaN is the number).
+template <typename T, int V>
+__device__ __forceinline__ void unpack_clean(const Pack<T, V>& p, float (&l)[V])
+{
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        const float v = (float)p.v[e];
+        asm("v_max_f32 %0, 0xff800000, %1" : "=v"(l[e]) : "v"(v));
+    }
+}
+
+// The pieces of a thread.
+template <typename T>
+struct Pieces {
+    static constexpr int V = Row<T>::V;
+    // low bits that are 0 in every logit of the type, 8 of them together
+    static constexpr int kZeros = std::is_same<T, bf16>::value ? 16 : std::is_same<T, f16>::value ? 8 : 0;
+    static constexpr int kFlight = 4;  // pieces whose loads are in flight together
+    Row<T> row;
+
+    __device__ Pieces(const T* q, uint32_t len) : row(q, len) {}
+    // f(piece's number, its logits) for every one of the thread's pieces
+    template <class F>
+    __device__ __forceinline__ void each(F f) const
+    {
+        const uint32_t lane = threadIdx.x & 63;
+        // whole wavefronts: lanes behind the last piece see minus infinity
+        for (uint32_t q = threadIdx.x; q - lane < row.pieces; q += kFlight * kBlock) {
+            Pack<T, V> a[kFlight];
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) a[i] = row.load(min(q + i * kBlock, row.pieces - 1));
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) {
+                if (q - lane + i * kBlock >= row.pieces) break;
+                float l[V];
+                unpack_clean(a[i], l);
+                if (q + i * kBlock >= row.pieces) {
+#pragma unroll
+                    for (int e = 0; e < V; ++e) l[e] = -INFINITY;
+                }
+                f(q + i * kBlock, l);
             }
         }
     }
@@ -105,6 +164,23 @@ __device__ __forceinline__ uint32_t block_min(uint32_t v, Shared& s)
     return v;
 }
 
+// The sum over the wavefront, in lane 63, in an order that depends on the lanes alone: within rows of 16, then over
+// the rows.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float add_from(float v)
+{
+    return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 0xF, false));
+}
+__device__ __forceinline__ float wave_sum(float v)
+{
+    v = add_from<0x111, 0xF>(v);  // row_shr:1
+    v = add_from<0x112, 0xF>(v);
+    v = add_from<0x114, 0xF>(v);
+    v = add_from<0x118, 0xF>(v);
+    v = add_from<0x142, 0xA>(v);  // row_bcast:15 into rows 1 and 3
+    return add_from<0x143, 0xC>(v);  // row_bcast:31 into rows 2 and 3
+}
+
 // Exclusive prefix over the threads, and the sum.
 __device__ __forceinline__ uint64_t block_prefix(uint64_t v, Shared& s, uint64_t& total)
 {
@@ -130,23 +206,20 @@ __device__ __forceinline__ uint64_t block_prefix(uint64_t v, Shared& s, uint64_t
 
 // ------------------------------------------------------------ weights
 // t = log2 of the weight: (logit - max) log2(e) / temperature, the factor in two parts (both above 0, so that minus
-// infinity stays what it is).  `usual`: the largest logit is finite, the temperature below 2^60.
+// infinity stays what it is).  pre is 1, or 2^-100 for temperatures from 2^60 on, whose factor holds the 2^100.  Next to a
+// plus infinity everything else is at minus infinity; its own difference is NaN, of which the minimum with 0 makes 0.
 struct Scale {
-    float max, hi, lo;
-    bool usual;
+    float pre, max, hi, lo;  // max: times pre
 
     __device__ float log2_weight(float logit) const
     {
-        float d = logit - max;
-        if (!usual) {
-            if (max == INFINITY)
-                d = logit == max ? 0.0f : -INFINITY;  // next to a plus infinity nothing else weighs
-            else
-                d = logit * 0x1p-100f - max * 0x1p-100f;  // the factor holds 2^100
-        }
+        const float d = fminf(fmaf(logit, pre, -max), 0.0f);
         return fmaf(d, lo, d * hi);
     }
-    __device__ static float weight(float t) { return fmaxf(exp2_fast(t), 0.0f); }  // NaN: 0
+    __device__ static float weight(float t) { return exp2_fast(t); }
+    // The logit whose weight is 2^t, but for roundings; minus infinity where that is not to be had.
+    __device__ bool usual() const { return pre == 1.0f && max < INFINITY; }
+    __device__ float logit_at(float t) const { return usual() ? max + t / (hi + lo) : -INFINITY; }
 };
 
 __device__ __forceinline__ Scale make_scale(float max, double temperature)
@@ -158,7 +231,8 @@ __device__ __forceinline__ Scale make_scale(float max, double temperature)
     c = fmin(fmax(c, 0x1p-60), 0x1p100);
     float hi = (float)c;
     if ((double)hi >= c) hi = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, hi) - 1);
-    return Scale{max, hi, (float)(c - (double)hi), !high && max < INFINITY};
+    const float pre = high ? 0x1p-100f : 1.0f;
+    return Scale{pre, max == INFINITY ? max : max * pre, hi, (float)(c - (double)hi)};
 }
 
 __device__ __forceinline__ uint32_t bin_of(float t) { return (uint32_t)fminf(-t * kPerOctave, (float)(kBins - 1)); }
@@ -191,40 +265,77 @@ struct Cut {
     __device__ bool keeps(float l, uint32_t i) const { return l > logit || (l == logit && i <= index); }
 };
 
-// What an element counts: 1 (COUNT), or its weight as an integer, if `all` keeps it; 0 elsewhere.
-template <bool COUNT>
+// What an element counts: 1 (COUNT), or its weight as an integer, if `all` keeps it (ALL: it keeps everything); 0 elsewhere.
+template <bool COUNT, bool ALL>
 __device__ __forceinline__ uint64_t value_of(float l, uint32_t i, float t, const Cut& all)
 {
-    if (!all.keeps(l, i)) return 0;
-    return COUNT ? (l > -INFINITY ? 1u : 0u) : mass(Scale::weight(t));
+    if (!ALL && !all.keeps(l, i)) return 0;
+    return COUNT ? 1u : mass(Scale::weight(t));
+}
+
+// A logit that at least k of the row's reach: the least of the threads' largest logits up to the bin in which the k-th of
+// those lies.  mine: the thread's largest.  Minus infinity if fewer threads have one.
+__device__ __forceinline__ float bound_of(const Scale& scale, float mine, uint32_t k, Shared& s)
+{
+    const uint32_t tid = threadIdx.x;
+    const bool any = mine > -INFINITY;
+    const uint32_t bin = any ? bin_of(scale.log2_weight(mine)) : 0;
+    __syncthreads();
+    s.bins[2 * tid] = s.bins[2 * tid + 1] = 0;
+    if (tid == 0) s.at = 0xFFFFFFFFu;
+    __syncthreads();
+    if (any) atomicAdd((unsigned long long*)&s.bins[bin], 1ull);
+    __syncthreads();
+    uint64_t total;
+    const uint64_t b0 = s.bins[2 * tid], b1 = s.bins[2 * tid + 1], before = block_prefix(b0 + b1, s, total);
+    if (before < k && k <= before + b0 + b1) s.at = 2 * tid + (before + b0 < k ? 1 : 0);
+    __syncthreads();
+    if (s.at == 0xFFFFFFFFu) return -INFINITY;
+    return -block_max(any && bin <= s.at ? -mine : -INFINITY, s);
 }
 
 // The first part of what `all` keeps, up to the element at which the values add up to the limit: `limit` itself
-// (COUNT), or share times the sum of the values.
-template <bool COUNT, typename T>
-__device__ Cut find_cut(const Row<T>& row, const Scale& scale, const Cut& all, uint64_t limit, double share, Shared& s)
+// (COUNT), or share times the sum of the values.  bound: a logit that the element reaches (COUNT).
+template <bool COUNT, bool ALL, typename P>
+__device__ __forceinline__ Cut find_cut(const P& pieces, const Scale& scale, const Cut& all, uint64_t limit, double share, float bound, Shared& s)
 {
-    constexpr int V = Row<T>::V;
+    constexpr int V = P::V;
+    const auto& row = pieces.row;
     const uint32_t tid = threadIdx.x;
     __syncthreads();
     s.bins[2 * tid] = s.bins[2 * tid + 1] = 0;
     if (tid == 0) s.at = 0xFFFFFFFFu, s.count = 0;
     __syncthreads();
-    for (uint32_t q = tid; q < row.pieces; q += kBlock) {
-        float l[V];
-        row.load(q, l);
+    // the row's weights below this logit add up to less than half of what the share leaves out of a sum of at least 1
+    const float small = COUNT ? bound : scale.logit_at(__builtin_amdgcn_logf((float)((1.0 - share) / row.n)) - 1.0f);
+    float rest = 0.0f;
+    pieces.each([&](uint32_t q, const float(&l)[V]) __attribute__((always_inline)) {
+        if (!COUNT) {
+            // their sum: one part of the factor is enough for it
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float w = exp2_fast((l[e] - scale.max) * scale.hi);
+                rest += l[e] < small && (ALL || all.keeps(l[e], row.index(q, e))) ? w : 0.0f;
+            }
+        }
 #pragma unroll
         for (int e = 0; e < V; ++e) {
+            if (l[e] < small) continue;
+            // one more minus infinity among the counts is one more in the last bin, behind every other
             const float t = scale.log2_weight(l[e]);
-            const uint64_t v = value_of<COUNT>(l[e], row.index(q, e), t, all);
-            if (v) atomicAdd((unsigned long long*)&s.bins[bin_of(t)], (unsigned long long)v);
+            const uint64_t v = value_of<COUNT, ALL>(l[e], row.index(q, e), t, all);
+            if (ALL || v) atomicAdd((unsigned long long*)&s.bins[bin_of(t)], (unsigned long long)v);
         }
-    }
+    });
     __syncthreads();
     uint64_t total;
     const uint64_t b0 = s.bins[2 * tid], b1 = s.bins[2 * tid + 1];
     const uint64_t before = block_prefix(b0 + b1, s, total);
-    if (!COUNT) limit = max((uint64_t)1, (uint64_t)ceil(share * (double)total));
+    if (!COUNT) {
+        uint64_t more;
+        block_prefix(mass(rest), s, more);
+        limit = max((uint64_t)1, (uint64_t)ceil(share * (double)(total + more)));
+    }
     if (before < limit && limit <= before + b0 + b1) {
         const bool second = before + b0 < limit;
         s.at = 2 * tid + (second ? 1 : 0);
@@ -235,14 +346,20 @@ __device__ Cut find_cut(const Row<T>& row, const Scale& scale, const Cut& all, u
     if (bin == 0xFFFFFFFFu) return all;  // less than the limit in all
     uint64_t base = s.base;
 
-    // the bin's elements
-    for (uint32_t q = tid; q < row.pieces; q += kBlock) {
-        float l[V];
-        row.load(q, l);
+    // the bin's elements: an interval of logits, with room for roundings, and in it the bin itself
+    float from = -INFINITY, to = INFINITY;
+    if (scale.usual() && bin + 1 < (uint32_t)kBins) {
+        from = scale.logit_at(-(float)(bin + 1) / kPerOctave);
+        to = scale.logit_at(-(float)bin / kPerOctave);
+        const float room = (fabsf(from) + fabsf(scale.max)) * 0x1p-20f;
+        from -= room, to += room;
+    }
+    pieces.each([&](uint32_t q, const float(&l)[V]) __attribute__((always_inline)) {
 #pragma unroll
         for (int e = 0; e < V; ++e) {
+            if (!(l[e] >= from && l[e] <= to)) continue;
             const float t = scale.log2_weight(l[e]);
-            if (bin_of(t) == bin && value_of<COUNT>(l[e], row.index(q, e), t, all)) {
+            if (bin_of(t) == bin && value_of<COUNT, ALL>(l[e], row.index(q, e), t, all)) {
                 const uint32_t at = atomicAdd(&s.count, 1u);
                 if (at < kList) {
                     s.list_logit[at] = l[e];
@@ -250,9 +367,34 @@ __device__ Cut find_cut(const Row<T>& row, const Scale& scale, const Cut& all, u
                 }
             }
         }
-    }
+    });
     __syncthreads();
     const uint32_t listed = s.count;
+    if (listed <= kRanked) {
+        // the one up to which those before it, by logit and index, and itself reach the limit
+        const bool in = tid < listed;
+        const float l = in ? s.list_logit[tid] : 0.0f;
+        const uint32_t index = in ? s.list_index[tid] : 0;
+        const uint64_t v = !in ? 0 : COUNT ? 1 : mass(Scale::weight(scale.log2_weight(l)));
+        if (in) s.bins[tid] = v;
+        if (tid == 0) s.at = 0;
+        __syncthreads();
+        if (in) {
+            uint64_t before = base;
+            bool later = false;  // one that equals it follows
+            for (uint32_t k = 0; k < listed; ++k) {
+                const float o = s.list_logit[k];
+                const uint32_t i = s.list_index[k];
+                if (o > l || (o == l && i < index)) before += s.bins[k];
+                later |= o == l && i > index;
+            }
+            if (before < limit && limit <= before + v) s.at = tid, s.count = later ? 1u : 0u;
+        }
+        __syncthreads();
+        const uint32_t k = s.at;
+        const float logit = s.list_logit[k];
+        return Cut{logit, s.count ? s.list_index[k] : all.logit == logit ? all.index : 0xFFFFFFFFu};
+    }
     // f(logit, index, value) for each of them
     const auto each = [&](auto f) {
         if (listed <= kList) {
@@ -263,11 +405,11 @@ __device__ Cut find_cut(const Row<T>& row, const Scale& scale, const Cut& all, u
         } else {
             for (uint32_t q = tid; q < row.pieces; q += kBlock) {
                 float l[V];
-                row.load(q, l);
+                unpack_clean(row.load(q), l);
                 for (int e = 0; e < V; ++e) {
                     const float t = scale.log2_weight(l[e]);
                     if (bin_of(t) != bin) continue;
-                    const uint64_t v = value_of<COUNT>(l[e], row.index(q, e), t, all);
+                    const uint64_t v = value_of<COUNT, ALL>(l[e], row.index(q, e), t, all);
                     if (v) f(l[e], row.index(q, e), v);
                 }
             }
@@ -277,7 +419,7 @@ __device__ Cut find_cut(const Row<T>& row, const Scale& scale, const Cut& all, u
     // their values, eight bits at a time from the top
     uint32_t key = 0, mask = 0;
     uint64_t equal = 0;  // the values of the elements with the key so far
-    for (int shift = 24; shift >= 0; shift -= 8) {
+    for (int shift = 24; shift >= P::kZeros; shift -= 8) {
         __syncthreads();
         if (tid < 256) s.bins[tid] = 0;
         __syncthreads();
@@ -300,6 +442,7 @@ __device__ Cut find_cut(const Row<T>& row, const Scale& scale, const Cut& all, u
         base = s.base;
         equal = s.bins[0];
     }
+    if (!(key & 0x80000000u)) key |= (1u << P::kZeros) - 1;  // the bits of negative numbers are turned over
     const float logit = logit_of(key);
     const uint64_t each_value = COUNT ? 1 : mass(Scale::weight(scale.log2_weight(logit)));
     const uint64_t wanted = (limit - base + each_value - 1) / each_value, there = equal / each_value;
@@ -331,77 +474,213 @@ __device__ Cut find_cut(const Row<T>& row, const Scale& scale, const Cut& all, u
     return Cut{logit, index};
 }
 
+// ------------------------------------------------------------ top-k by sorting
+// Sorts a[0 .. size) ascending (size: a power of two, at most 2 kBlock).
+__device__ void sort(uint64_t* a, uint32_t size)
+{
+    for (uint32_t run = 2; run <= size; run *= 2) {
+        for (uint32_t step = run / 2; step > 0; step /= 2) {
+            __syncthreads();
+            const uint32_t i = threadIdx.x;
+            if (i < size / 2) {
+                const uint32_t lo = (i / step) * 2 * step + i % step, hi = lo + step;
+                const uint64_t x = a[lo], y = a[hi];
+                if ((x > y) != ((lo & run) != 0)) a[lo] = y, a[hi] = x;
+            }
+        }
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ uint32_t power_of_two(uint32_t n)
+{
+    uint32_t p = 2;
+    while (p < n) p *= 2;
+    return p;
+}
+
+// The token, if no more than kSorted of the row's logits reach `bound`, which the first k do; false elsewhere.
+template <typename P>
+__device__ __forceinline__ bool sample_sorted(const P& pieces, const Scale& scale, float bound, uint32_t k, double top_p, float least, float uniform,
+                                              Shared& s, uint32_t& token)
+{
+    constexpr int V = P::V;
+    const auto& row = pieces.row;
+    const uint32_t tid = threadIdx.x;
+    __syncthreads();
+    if (tid == 0) s.count = 0;
+    __syncthreads();
+    pieces.each([&](uint32_t q, const float(&l)[V]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            if (l[e] >= bound && l[e] > -INFINITY) {
+                const uint32_t at = atomicAdd(&s.count, 1u);
+                // by falling logit, then by index
+                if (at < kSorted) s.bins[at] = (uint64_t)~key_of(l[e]) << 32 | row.index(q, e);
+            }
+        }
+    });
+    __syncthreads();
+    const uint32_t count = s.count;
+    if (count > kSorted) return false;
+    uint32_t size = power_of_two(count);
+    for (uint32_t i = count + tid; i < size; i += kBlock) s.bins[i] = ~0ull;
+    sort(s.bins, size);
+    const uint32_t first = min(k, count);
+    // thread t has ranks 2 t and 2 t + 1
+    uint64_t m[2], total;
+    uint32_t index[2];
+    float w[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const uint32_t r = 2 * tid + j;
+        const uint64_t v = r < first ? s.bins[r] : 0;
+        index[j] = (uint32_t)v;
+        w[j] = r < first ? Scale::weight(scale.log2_weight(logit_of(~(uint32_t)(v >> 32)))) : 0.0f;
+        m[j] = mass(w[j]);
+    }
+    const uint64_t before = block_prefix(m[0] + m[1], s, total);
+    const uint64_t limit = top_p < 1.0 ? max((uint64_t)1, (uint64_t)ceil(fmax(top_p, 0.0) * (double)total)) : ~0ull;
+    if (tid == 0) s.count = 0;
+    __syncthreads();
+    // what is kept, by index; weights that are 0 as integers are never met
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        if (m[j] && (j ? before + m[0] : before) < limit && w[j] >= least)
+            s.bins[atomicAdd(&s.count, 1u)] = (uint64_t)index[j] << 32 | __builtin_bit_cast(uint32_t, w[j]);
+    }
+    __syncthreads();
+    const uint32_t kept = s.count;
+    size = power_of_two(kept);
+    for (uint32_t i = kept + tid; i < size; i += kBlock) s.bins[i] = ~0ull;
+    sort(s.bins, size);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const uint32_t r = 2 * tid + j;
+        const uint64_t v = r < kept ? s.bins[r] : 0;
+        index[j] = (uint32_t)(v >> 32);
+        m[j] = r < kept ? mass(__builtin_bit_cast(float, (uint32_t)v)) : 0;
+    }
+    const uint64_t start = block_prefix(m[0] + m[1], s, total);
+    const double target = (double)uniform * (double)total;
+    // the first whose sum exceeds the target, else the last
+    if (tid == 0) s.at = (uint32_t)(s.bins[kept - 1] >> 32);
+    __syncthreads();
+    if ((double)start <= target) {
+        if ((double)(start + m[0]) > target)
+            s.at = index[0];
+        else if ((double)(start + m[0] + m[1]) > target)
+            s.at = index[1];
+    }
+    __syncthreads();
+    token = s.at;
+    return true;
+}
+
 // ------------------------------------------------------------ the kernel
-template <typename T, typename I>
+template <typename T>
 __global__ __launch_bounds__(kBlock) void sample_kernel(Settings set, uint32_t rows, uint32_t n, const T* __restrict__ logits,
-                                                        int64_t stride, I* __restrict__ tokens)
+                                                        int64_t stride, void* __restrict__ tokens, int token_bytes)
 {
     constexpr int V = Row<T>::V;
     __shared__ Shared s;
     const uint32_t r = workgroup(), tid = threadIdx.x;
     if (r >= rows) return;
     const int lane = tid & 63, w = uniform((int)(tid >> 6));
-    const Row<T> row(logits + (int64_t)r * stride, n);
+    const Pieces<T> pieces(logits + (int64_t)r * stride, n);
+    const Row<T>& row = pieces.row;
     const double temperature = set.temperatures ? (double)set.temperatures[r] : set.temperature;
     const int64_t top_k = set.top_ks ? (int64_t)set.top_ks[r] : set.top_k;
     const double top_p = set.top_ps ? (double)set.top_ps[r] : set.top_p;
     const double min_p = set.min_ps ? (double)set.min_ps[r] : set.min_p;
+    const float u = set.uniform[r], uniform01 = u > 0.0f ? fminf(u, 1.0f) : 0.0f;
+    const auto result = [&](int64_t token) {
+        if (token_bytes == 4)
+            static_cast<int32_t*>(tokens)[r] = (int32_t)token;
+        else
+            static_cast<int64_t*>(tokens)[r] = token;
+    };
 
-    float most = -INFINITY;
-    for (uint32_t q = tid; q < row.pieces; q += kBlock) {
-        float l[V];
-        row.load(q, l);
+    float mine = -INFINITY;
+    pieces.each([&](uint32_t, const float(&l)[V]) __attribute__((always_inline)) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) most = fmaxf(most, l[e]);
-    }
-    most = block_max(most, s);
+        for (int e = 0; e < V; ++e) mine = fmaxf(mine, l[e]);
+    });
+    const float most = block_max(mine, s);
     if (most == -INFINITY) {
-        if (tid == 0) tokens[r] = (I)-1;
+        if (tid == 0) result(-1);
         return;
     }
     if (!(temperature > 0.0)) {
         uint32_t first = 0xFFFFFFFFu;
-        for (uint32_t q = tid; q < row.pieces; q += kBlock) {
-            float l[V];
-            row.load(q, l);
+        if (mine == most) {
+            pieces.each([&](uint32_t q, const float(&l)[V]) __attribute__((always_inline)) {
 #pragma unroll
-            for (int e = 0; e < V; ++e)
-                if (l[e] == most) first = min(first, row.index(q, e));
+                for (int e = 0; e < V; ++e)
+                    if (l[e] == most) first = min(first, row.index(q, e));
+            });
         }
         first = block_min(first, s);
-        if (tid == 0) tokens[r] = (I)first;
+        if (tid == 0) result(first);
         return;
     }
     const Scale scale = make_scale(most, temperature);
-    Cut cut{-INFINITY, 0xFFFFFFFFu};
-    if (top_k > 0 && top_k < (int64_t)n) cut = find_cut<true>(row, scale, cut, (uint64_t)top_k, 0.0, s);
-    if (top_p < 1.0) cut = find_cut<false>(row, scale, cut, 0, fmax(top_p, 0.0), s);
     float least = 0.0f;  // the smallest float that is not below min_p
     if (min_p > 0.0) {
         least = (float)fmin(min_p, 1.0);
         if ((double)least < fmin(min_p, 1.0)) least = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, least) + 1);
     }
-    // the kept weights of piece q, and their sum
-    const auto kept = [&](uint32_t q, float (&f)[V]) {
-        row.load(q, f);
+    Cut cut{-INFINITY, 0xFFFFFFFFu};
+    if (top_k > 0 && top_k < (int64_t)n) {
+        uint32_t token;
+        const float bound = top_k <= kBlock && n > kSorted ? bound_of(scale, mine, (uint32_t)top_k, s) : -INFINITY;
+        if ((n <= kSorted || (bound > -INFINITY && top_k <= kMostSorted)) &&
+            sample_sorted(pieces, scale, bound, (uint32_t)min(top_k, (int64_t)n), top_p, least, uniform01, s, token)) {
+            if (tid == 0) result(token);
+            return;
+        }
+        cut = find_cut<true, true>(pieces, scale, cut, (uint64_t)top_k, 0.0, bound, s);
+        if (top_p < 1.0) cut = find_cut<false, false>(pieces, scale, cut, 0, fmax(top_p, 0.0), 0.0f, s);
+    } else if (top_p < 1.0) {
+        cut = find_cut<false, true>(pieces, scale, cut, 0, fmax(top_p, 0.0), 0.0f, s);
+    }
+    // The kept weights of a piece, and their sum.  CHECK 0: everything is kept, 1: logits from the cut's on with the least
+    // weight, 2: some of those that equal the cut's are not.
+    const auto kept = [&](auto check, uint32_t q, const float(&l)[V], float(&f)[V]) __attribute__((always_inline)) {
+        constexpr int CHECK = decltype(check)::value;
         float sum = 0.0f;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-            const float v = Scale::weight(scale.log2_weight(f[e]));
-            f[e] = cut.keeps(f[e], row.index(q, e)) && v >= least ? v : 0.0f;
+            const float v = Scale::weight(scale.log2_weight(l[e]));
+            const bool keep = CHECK == 0 || (v >= least && (CHECK == 1 ? l[e] >= cut.logit : cut.keeps(l[e], row.index(q, e))));
+            f[e] = keep ? v : 0.0f;
             sum += f[e];
         }
         return sum;
     };
-    const uint32_t entries = (row.pieces + kBlock - 1) / kBlock * kWaves;
-    for (uint32_t q0 = 0; q0 < row.pieces; q0 += kBlock) {
-        const uint32_t q = q0 + tid;
-        float f[V];
-        double sum = q < row.pieces ? (double)kept(q, f) : 0.0;
+    const auto sums = [&](auto check) __attribute__((always_inline)) {
+        pieces.each([&](uint32_t q, const float(&l)[V]) __attribute__((always_inline)) {
+            if (decltype(check)::value > 0) {
+                // where little is kept, most wavefronts have nothing to keep
+                float largest = l[0];
 #pragma unroll
-        for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
-        if (lane == 0) s.sums[q0 / kBlock * kWaves + w] = sum;
-    }
+                for (int e = 1; e < V; ++e) largest = fmaxf(largest, l[e]);
+                if (!__builtin_amdgcn_ballot_w64(largest >= cut.logit)) return;
+            }
+            float f[V];
+            const float sum = wave_sum(kept(check, q, l, f));
+            if (lane == 63) s.sums[q / kBlock * kWaves + w] = (double)sum;
+        });
+    };
+    const uint32_t entries = (row.pieces + kBlock - 1) / kBlock * kWaves;
+    for (uint32_t k = tid; k < entries; k += kBlock) s.sums[k] = 0.0;
+    __syncthreads();
+    if (cut.index != 0xFFFFFFFFu)
+        sums(std::integral_constant<int, 2>());
+    else if (cut.logit > -INFINITY || least > 0.0f)
+        sums(std::integral_constant<int, 1>());
+    else
+        sums(std::integral_constant<int, 0>());
     __syncthreads();
     if (w != 0) return;
 
@@ -419,15 +698,14 @@ __global__ __launch_bounds__(kBlock) void sample_kernel(Settings set, uint32_t r
         return v;
     };
     const uint32_t run = (entries + 63) / 64, lo = min(lane * run, entries), hi = min(lo + run, entries);
-    double mine = 0.0;
-    for (uint32_t k = lo; k < hi; ++k) mine += s.sums[k];
-    double incl = prefix(mine);
-    const float u = set.uniform[r];
-    const double target = (double)(u > 0.0f ? fminf(u, 1.0f) : 0.0f) * __shfl(incl, 63, 64);
-    int leader = pick(incl, mine, target);
+    double own = 0.0;
+    for (uint32_t k = lo; k < hi; ++k) own += s.sums[k];
+    double incl = prefix(own);
+    const double target = (double)uniform01 * __shfl(incl, 63, 64);
+    int leader = pick(incl, own, target);
     // that lane's entries one after another; every lane walks along
     const uint32_t from = (uint32_t)__builtin_amdgcn_readlane((int)lo, leader), to = (uint32_t)__builtin_amdgcn_readlane((int)hi, leader);
-    double base = __shfl(incl - mine, leader, 64), at = base;
+    double base = __shfl(incl - own, leader, 64), at = base;
     uint32_t entry = from;
     for (uint32_t k = from; k < to; ++k) {
         const double v = s.sums[k];
@@ -439,14 +717,18 @@ __global__ __launch_bounds__(kBlock) void sample_kernel(Settings set, uint32_t r
         at += v;
     }
     const uint32_t q = entry / kWaves * kBlock + entry % kWaves * 64 + lane;
-    float f[V];
+    float l[V], f[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) f[e] = 0.0f;
-    mine = q < row.pieces ? (double)kept(q, f) : 0.0;
-    incl = base + prefix(mine);
-    leader = pick(incl, mine, target);
+    own = 0.0;
+    if (q < row.pieces) {
+        unpack_clean(row.load(q), l);
+        own = (double)kept(std::integral_constant<int, 2>(), q, l, f);
+    }
+    incl = base + prefix(own);
+    leader = pick(incl, own, target);
     if (lane != leader) return;
-    at = incl - mine;
+    at = incl - own;
     uint32_t token = 0;
     for (int e = 0; e < V; ++e) {
         if (f[e] > 0.0f) {
@@ -455,7 +737,7 @@ __global__ __launch_bounds__(kBlock) void sample_kernel(Settings set, uint32_t r
             if (at > target) break;
         }
     }
-    tokens[r] = (I)token;
+    result(token);
 }
 
 }  // namespace
@@ -486,13 +768,8 @@ scan_status_t sample_tokens(const sample_tokens_args_t* args, void* stream)
     const hipStream_t s = static_cast<hipStream_t>(stream);
     return with_dtype(a.dtype, [&](auto e) -> scan_status_t {
         using T = decltype(e);
-        const T* logits = static_cast<const T*>(a.logits);
-        if (a.token_bytes == 4)
-            hipLaunchKernelGGL((sample_kernel<T, int32_t>), grid_of(a.rows), dim3(kBlock), 0, s, set, (uint32_t)a.rows, a.n, logits,
-                               a.logits_stride, static_cast<int32_t*>(a.tokens));
-        else
-            hipLaunchKernelGGL((sample_kernel<T, int64_t>), grid_of(a.rows), dim3(kBlock), 0, s, set, (uint32_t)a.rows, a.n, logits,
-                               a.logits_stride, static_cast<int64_t*>(a.tokens));
+        hipLaunchKernelGGL((sample_kernel<T>), grid_of(a.rows), dim3(kBlock), 0, s, set, (uint32_t)a.rows, a.n, static_cast<const T*>(a.logits),
+                           a.logits_stride, a.tokens, a.token_bytes);
         return launched();
     });
 }

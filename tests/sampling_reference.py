@@ -1,8 +1,8 @@
 """Sampling from its definition in 64 bits on the host.
 
 A weight of the kernel is off by a relative error of at most 2 |t| U (t = (logit - max) / temperature log2 e: the
-difference, the product) + 4 U (the exponential's unit, its argument's last rounding), U = 2^-24; sums of
-up to 8 weights in 32 bits add 8 U.  Shares of the sum are then off by no more than twice the mean of that over the
+difference, the product) + 4 U (the exponential's unit, its argument's last rounding), U = 2^-24; sums over a
+wavefront's pieces in 32 bits add 14 U (8 elements, 6 sums over lanes).  Shares of the sum are then off by no more than twice the mean of that over the
 kept weights, and a border (a share that top-p or the random number is compared with, or a weight next to min_p)
 may fall on the other side only if it lies closer than that."""
 import numpy as np
@@ -39,7 +39,7 @@ def token(z, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     over = run > u * run[-1]
     i = int(np.argmax(over)) if over.any() else int(np.nonzero(w)[0][-1])
     depth = np.where(w > 0, np.abs(np.where(np.isfinite(t), t, 0.0)), 0.0) * 1.4427
-    return i, float(2 * (w * (2 * depth + 12) * U).sum() / run[-1])
+    return i, float(2 * (w * (2 * depth + 18) * U).sum() / run[-1])
 
 
 def accepted(z, u, got, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
