@@ -164,18 +164,31 @@ __global__ __launch_bounds__(kBlock) void prefix_kernel(SplitPlan p, uint32_t* _
 template <bool FEW>
 __global__ __launch_bounds__(kBlock) void place_kernel(const int32_t* __restrict__ experts, SplitPlan p,
                                                        const uint32_t* __restrict__ counts, const uint32_t* __restrict__ totals,
-                                                       int32_t* __restrict__ offsets, int32_t* __restrict__ places,
-                                                       int32_t* __restrict__ source)
+                                                       int32_t* __restrict__ offsets, int32_t* places, int32_t* __restrict__ source)
 {
     __shared__ uint32_t s_base[kMaxExperts], s_part[kWaves];
     const uint32_t t = threadIdx.x;
+    uint32_t e[kRounds], rank[kRounds];
+#pragma unroll
+    for (int u = 0; u < kRounds; ++u) {
+        const uint32_t i = min(blockIdx.x * kChunk + u * kBlock + t, p.n - 1);
+        e[u] = (uint32_t)experts[i];
+        rank[u] = (uint32_t)places[i];
+    }
     uint32_t before = 0, sum = 0;  // of expert t: in the chunks before this one, in all
     if (t < p.experts) {
         if (FEW) {
-            for (uint32_t c = 0; c < p.chunks; ++c) {
-                const uint32_t v = counts[(size_t)c * p.experts + t];
-                before += c < blockIdx.x ? v : 0u;
-                sum += v;
+            // eight loads in flight together
+            for (uint32_t c0 = 0; c0 < p.chunks; c0 += 8) {
+                uint32_t v[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) v[u] = counts[(size_t)min(c0 + u, p.chunks - 1) * p.experts + t];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const uint32_t n = c0 + u < p.chunks ? v[u] : 0u;
+                    before += c0 + u < blockIdx.x ? n : 0u;
+                    sum += n;
+                }
             }
         } else {
             before = counts[(size_t)blockIdx.x * p.experts + t];
@@ -190,11 +203,12 @@ __global__ __launch_bounds__(kBlock) void place_kernel(const int32_t* __restrict
     }
     if (blockIdx.x == 0 && t == 0) offsets[p.experts] = (int32_t)total;
     __syncthreads();
-    const uint32_t first = blockIdx.x * kChunk, last = min(first + kChunk, p.n);
-    for (uint32_t i = first + t; i < last; i += kBlock) {
-        const uint32_t e = (uint32_t)experts[i];
-        if (e < p.experts) {
-            const uint32_t at = s_base[e] + (uint32_t)places[i];
+#pragma unroll
+    for (int u = 0; u < kRounds; ++u) {
+        const uint32_t i = blockIdx.x * kChunk + u * kBlock + t;
+        if (i >= p.n) break;
+        if (e[u] < p.experts) {
+            const uint32_t at = s_base[e[u]] + rank[u];
             places[i] = (int32_t)at;
             source[at] = (int32_t)i;
         }
@@ -224,6 +238,16 @@ __device__ __forceinline__ void store_stream(T* out, const Pack<T, V>& p)
         __builtin_nontemporal_store(__builtin_bit_cast(u32x4, p), reinterpret_cast<u32x4*>(out));
     else
         *reinterpret_cast<Pack<T, V>*>(out) = p;
+}
+
+// A row of the experts' order is read once.
+template <typename T, int V>
+__device__ __forceinline__ Pack<T, V> load_stream(const T* p)
+{
+    if constexpr (sizeof(Pack<T, V>) == 16)
+        return __builtin_bit_cast(Pack<T, V>, __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p)));
+    else
+        return load_pack<T, V>(p);
 }
 
 constexpr uint32_t kClearStep = 256;  // workgroups that clear the rows of no expert
@@ -288,7 +312,7 @@ __global__ __launch_bounds__(256) void combine_kernel(Moves m, uint32_t chunks, 
         for (int u = 0; u < kAhead; ++u) {
             at[u] = j0 + u < m.choices ? place_of(m, (uint32_t)t, j0 + u) : -1;
             w[u] = weights && at[u] >= 0 ? (float)weights[t * m.choices + j0 + u] : 1.0f;
-            if (at[u] >= 0) p[u] = load_pack<T, V>(y + (int64_t)at[u] * y_stride + c);
+            if (at[u] >= 0) p[u] = load_stream<T, V>(y + (int64_t)at[u] * y_stride + c);
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
@@ -297,7 +321,7 @@ __global__ __launch_bounds__(256) void combine_kernel(Moves m, uint32_t chunks, 
             for (int k = 0; k < V; ++k) acc[k] = fmaf(w[u], (float)p[u].v[k], acc[k]);
         }
     }
-    *reinterpret_cast<Pack<T, V>*>(out + (int64_t)t * out_stride + c) = pack<T, V>(acc);
+    store_stream<T, V>(out + (int64_t)t * out_stride + c, pack<T, V>(acc));
 }
 
 // One workgroup per token: dy at the token's places is its weight times dout, the weight's gradient the product
@@ -329,7 +353,7 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(Moves m, const W* __r
             if (dweights) {
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u)
-                    if (at[u] >= 0) p[u] = load_pack<T, V>(y + (int64_t)at[u] * y_stride + c);
+                    if (at[u] >= 0) p[u] = load_stream<T, V>(y + (int64_t)at[u] * y_stride + c);
             }
             unpack(d, g);
 #pragma unroll
