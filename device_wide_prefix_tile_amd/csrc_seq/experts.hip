@@ -449,19 +449,19 @@ size_t expert_split_workspace(size_t n, uint32_t n_experts)
 {
     if (n >= ((size_t)1 << 31) || n_experts < 1 || n_experts > kMaxExperts) return 0;
     const SplitPlan p = make_plan(n, n_experts);
-    return p.chunks == 1 ? 256 : round_up(((size_t)p.chunks + 1) * n_experts * 4, 256);
+    return p.chunks == 1 ? 0 : round_up(((size_t)p.chunks + 1) * n_experts * 4, 256);
 }
 
 scan_status_t expert_split(const int32_t* experts, size_t n, uint32_t n_experts, int32_t* offsets, int32_t* places, int32_t* source,
                            void* workspace, size_t workspace_bytes, void* stream)
 {
+    if (n >= ((size_t)1 << 31) || n_experts < 1 || n_experts > kMaxExperts) return SCAN_ERR_INVALID;
     const size_t need = expert_split_workspace(n, n_experts);
-    if (need == 0) return SCAN_ERR_INVALID;
     if (!offsets || (n && (!experts || !places || !source))) return SCAN_ERR_INVALID;
     for (const void* p : {(const void*)experts, (const void*)offsets, (const void*)places, (const void*)source})
         if (!aligned(p, 4)) return SCAN_ERR_INVALID;
-    if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return SCAN_ERR_INVALID;
-    const Range outs[] = {range(offsets, ((uint64_t)n_experts + 1) * 4), range(places, n * 4), range(source, n * 4), range(workspace, need)};
+    if (need && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return SCAN_ERR_INVALID;
+    const Range outs[] = {range(offsets, ((uint64_t)n_experts + 1) * 4), range(places, n * 4), range(source, n * 4), range(need ? workspace : nullptr, need)};
     const Range ins[] = {range(experts, n * 4)};
     if (any_overlap(outs, ins)) return SCAN_ERR_INVALID;
     const SplitPlan p = make_plan(n, n_experts);

@@ -17,7 +17,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from .sequence import (_DTYPE, _I, _I64, _P, _U32, _U64, _check, _enqueue, _lib, _like, _no_graph, _on, _plain, _register, _rows, _x)
+from .sequence import (_DTYPE, _I, _I64, _P, _U32, _U64, _check, _enqueue, _lib, _like, _no_graph, _plain, _ptr, _register, _rows, _x)
 
 
 class _DispatchArgs(ctypes.Structure):
@@ -77,11 +77,11 @@ def expert_split(experts: torch.Tensor, n_experts: int, stream=None) -> ExpertPl
     def call(handle):
         L = _lib()
         need = L.expert_split_workspace(n, n_experts)
-        new = dict(dtype=torch.int32, device=experts.device)
-        offsets, places, source = torch.empty(n_experts + 1, **new), torch.empty(experts.shape, **new), torch.empty(n, **new)
-        ws = torch.empty(max(need, 1), dtype=torch.uint8, device=experts.device)
-        _check(L.expert_split(experts.data_ptr(), n, n_experts, offsets.data_ptr(), places.data_ptr(), source.data_ptr(), ws.data_ptr(),
-                              need, handle), "expert_split")
+        new = experts.new_empty
+        offsets, places, source = new(n_experts + 1), new(experts.shape), new(n)
+        ws = new((need + 3) // 4) if need else None
+        _check(L.expert_split(experts.data_ptr(), n, n_experts, offsets.data_ptr(), places.data_ptr(), source.data_ptr(), _ptr(ws), need,
+                              handle), "expert_split")
         return ExpertPlan(offsets, places, source)
 
     return _enqueue(experts, stream, call)
@@ -109,7 +109,7 @@ def _matrix(t: torch.Tensor, name: str, rows=None):
 def _result(out, shape, like: torch.Tensor, name: str):
     """(tensor, address, row stride) of an output of that shape: `out`, or a new one."""
     if out is None:
-        out = torch.empty(shape, dtype=like.dtype, device=like.device)
+        out = like.new_empty(shape)
         return out, out.data_ptr(), shape[1]
     return (out,) + _like(out, name, torch.Size(shape), like.dtype, like.get_device(), shape[1])
 

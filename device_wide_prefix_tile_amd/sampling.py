@@ -55,7 +55,7 @@ def sample_tokens(logits: torch.Tensor, uniform: torch.Tensor, temperature=1.0, 
         raise TypeError("out must be int32 or int64")
 
     def call(handle):
-        y = torch.empty(rows, dtype=torch.int32, device=logits.device) if out is None else out
+        y = uniform.new_empty(rows, dtype=torch.int32) if out is None else out
         to = _plain(y, "out", (rows,), y.dtype, device)
         a = _SampleArgs(_DTYPE[logits.dtype], y.element_size(), rows, n, 0, logits.data_ptr(), stride, u, ts, ks, ps, ms, t, p, m, k, to)
         _check(_lib().sample_tokens(ctypes.byref(a), handle), "sample_tokens")

@@ -349,7 +349,7 @@ scan_status_t gated_scan_step(const gated_scan_step_args_t* args, void* stream);
  * expert_split: the stable split of n choices (token by token) by expert.  offsets (n_experts + 1): expert e has
  * rows [offsets[e], offsets[e+1]) of the experts' order, its choices in ascending order; places (n): the row of every
  * choice, -1 where it has no expert; source (n): the choice of every row, -1 from row offsets[n_experts] on.
- * n < 2^31, n_experts <= 1024.
+ * n < 2^31, n_experts <= 1024.  Up to 4096 choices need no workspace (0 bytes; it may be NULL).
  */
 scan_status_t expert_split(const int32_t* experts, size_t n, uint32_t n_experts, int32_t* offsets, int32_t* places,
                            int32_t* source, void* workspace, size_t workspace_bytes, void* stream);
@@ -357,7 +357,7 @@ size_t expert_split_workspace(size_t n, uint32_t n_experts);
 
 /*
  * expert_dispatch: out[places[t][j]] = x[t] for every token t and choice j; places outside 0 .. rows - 1 are
- * skipped (here and below), a row that two choices lead to holds either's.  used (device memory, may be NULL: offsets +
+ * skipped (here and below), a row that two choices lead to holds parts of either's.  used (device memory, may be NULL: offsets +
  * n_experts): the rows from *used on are set to zero; other rows that no choice leads to are left as they were.
  * x: tokens x channels, out: rows x channels; choices <= 256, tokens * choices < 2^31.  The gradient of x is
  * expert_combine without weights.

@@ -53,7 +53,8 @@ static void seq_host_checks(uint32_t* buf)
     EXPECT(gated_scan_workspace(&g) == 0 && gated_scan_saved(&g) == 0 && gated_scan_grad_workspace(nullptr) == 0);
     EXPECT(gated_scan_grad(nullptr, nullptr) == SCAN_ERR_INVALID && gated_scan_step(nullptr, nullptr) == SCAN_ERR_INVALID);
     int32_t* ints = reinterpret_cast<int32_t*>(buf);
-    EXPECT(expert_split(ints, 4, 4, ints + 8, ints + 4, ints + 16, nullptr, 0, nullptr) == SCAN_ERR_INVALID);  // no workspace
+    EXPECT(expert_split(ints, 4, 4, ints + 8, ints + 4, ints + 10, nullptr, 0, nullptr) == SCAN_ERR_INVALID);  // outputs overlap
+    EXPECT(expert_split(ints, 5000, 4, ints, ints, ints, nullptr, 0, nullptr) == SCAN_ERR_INVALID);           // no workspace
     EXPECT(expert_split_workspace(100000, 64) >= 64 * 25 * 4);
     expert_dispatch_args_t d{};
     EXPECT(expert_dispatch(&d, nullptr) == SCAN_ERR_INVALID);
@@ -232,7 +233,8 @@ static void recurrent_device_checks(hipStream_t st)
     int32_t *choices = (int32_t*)dev(experts.data(), experts.size() * 4), *offsets = (int32_t*)dev(nullptr, (e + 1) * 4);
     int32_t *places = (int32_t*)dev(nullptr, rows * k * 4), *source = (int32_t*)dev(nullptr, rows * k * 4);
     const size_t need = expert_split_workspace(rows * k, e);
-    EXPECT(expert_split(choices, rows * k, e, offsets, places, source, dev(nullptr, need), need, st) == SCAN_OK);
+    EXPECT(need == 0);  // one chunk of choices
+    EXPECT(expert_split(choices, rows * k, e, offsets, places, source, nullptr, 0, st) == SCAN_OK);
     expert_dispatch_args_t x{};
     x.tokens = rows;
     x.rows = rows * k;
