@@ -30,12 +30,13 @@ namespace {
 
 constexpr uint32_t kMaxChannels = 1u << 20;
 // Rows of a wavefront (the forward pass saves the state before every such rows for the gradient) and wavefronts of a
-// workgroup.  4 / 8 wavefronts: forward of 8 x 2048 x 4096 bfloat16 142 / 129 us, of 16384 x 2048 float16 108 / 80.
+// workgroup.  4 / 8 wavefronts: forward of 8 x 2048 x 4096 bfloat16 136 / 123 us, its gradient 262 / 213, forward of
+// 16384 x 2048 float16 115 / 80.
 constexpr int kRows = 8;
 constexpr int kWaves = 8;
 constexpr uint32_t kTileRows = kRows * kWaves;
 // Tiles of a group.  Few make the chain of groups long, many make more maps to read and to wait for: 4 / 8 / 12 / 16 forward of
-// 16384 x 2048 float16 98 / 82 / 91 / 92 us, of 8 x 2048 x 4096 bfloat16 128 / 123 / 167 / 170.
+// 16384 x 2048 float16 96 / 80 / 91 / 92 us, of 8 x 2048 x 4096 bfloat16 122 / 123 / 166 / 170.
 constexpr uint32_t kGroup = 8;
 constexpr uint32_t kChannelPad = 256;  // channels of a tile in the workspace and the saved states: a multiple of this
 constexpr uint32_t kEmptyStep = 32;    // workgroups per channel block that look for empty sequences
@@ -288,7 +289,7 @@ struct Walk {
         asm("" : "+s"(row));
     }
     // V columns from `at` bytes behind the row's start on.  Every value is used once, past the caches: forward of 8 x
-    // 2048 x 4096 bfloat16 130 -> 122 us, gradient of 8 x 2048 x 1024 float32 136 -> 120.
+    // 2048 x 4096 bfloat16 130 -> 123 us, its gradient 219 -> 213, gradient of 8 x 2048 x 1024 float32 138 -> 120.
     __device__ Pack<T, V> load(uint32_t at) const
     {
         return __builtin_bit_cast(Pack<T, V>, __builtin_nontemporal_load((const DWPT_GLOBAL R*)(row + at)));
@@ -403,10 +404,10 @@ struct ForwardShared {
     uint32_t head[kWaves], tile;
 };
 
-// 8 x 2048 x 4096 bfloat16: 123 us, 4.4 TB/s (float32 191 us, 5.6 TB/s); vector units busy 66%, 34 vector instructions per
+// 8 x 2048 x 4096 bfloat16: 123 us, 4.4 TB/s (float32 186 us, 5.8 TB/s); vector units busy 66%, 34 vector instructions per
 // element, 6 of them transcendental.  What is left is waiting: a round trip through memory takes some 5 us while the
-// card streams, and a tile makes two between its loads and its results (without them, and without their
-// results, 101 us).  One prompt of 16384 x 2048: 82 us, of which the chain of 32 groups sets most.
+// card streams, and a tile makes two between its loads and its results (an earlier version
+// of 129 us took 101 without them, and without their results).  One prompt of 16384 x 2048: 80 us, of which the chain of 32 groups sets most.
 template <typename T, int V, bool CHAIN, bool PLAIN>
 __device__ __forceinline__ void forward_tile(const Forward& p, ForwardShared<V>& s, const Tile& t, uint32_t c0)
 {
@@ -744,7 +745,7 @@ __global__ __launch_bounds__(kWaves * 64) void backward_kernel(Backward p)
 // With enough runs and channels to fill the chip a workgroup walks through its run's tiles one after another, from the
 // last to the first, and nothing passes through memory between tiles: every wavefront composes all wavefronts' maps of
 // a tile from LDS, which takes turns between two halves so that one barrier per tile is enough.  The next tile's rows
-// are on their way while this one's are finished.  (8 x 2048 x 4096 bfloat16: 214 us, 265 with tiles that wait for one another.
+// are on their way while this one's are finished.  (8 x 2048 x 4096 bfloat16: 213 us, 266 with tiles that wait for one another.
 // Forwards the same gained nothing, 125 against 122: its tiles wait less, two workgroups to a compute unit.)
 template <typename T, int V>
 __global__ __launch_bounds__(kWaves * 64) void backward_run_kernel(Backward p)
@@ -919,9 +920,10 @@ bool valid_rows(int dtype, uint64_t rows, uint32_t width, const Array& a)
     return a.p && aligned(a.p, dtype_size(dtype)) && a.stride >= (int64_t)width && a.stride <= ((int64_t)1 << 31);
 }
 
-// The most channels per lane, of 4, 2 and 1, that every row can be cut into: forward of 16384 x 2048 float16 82 / 79 / 113 us,
-// of 2048 x 2048 bfloat16 19 / 21 / 25, of 8 x 2048 x 4096 123 / 130 / 125.  The gradient takes 2 at most: 4 do not fit the
-// registers.
+// The most channels per lane, of 4, 2 and 1, that every row can be cut into.  Forward with 4 / 2 / 1: 8 x 2048 x 4096 bfloat16
+// 123 / 130 / 214 us, 2048 x 2048 18 / 20 / 25, 16384 x 2048 float16 80 / 78 / 114; float32 rows fill 8 bytes a lane with 2, which
+// are the most there: 8 x 2048 x 4096 191 / 186 / 237, 8 x 2048 x 1024 65 / 62 / 70, 16 x 1024 x 2048 108 / 106 / 126.  The gradient
+// takes 2 at most: 4 do not fit the registers.
 template <size_t N>
 int channels_per_lane(int dtype, uint32_t channels, const Array (&arrays)[N])
 {
@@ -962,10 +964,14 @@ void unset(const Cut& c, const Space& w, hipStream_t s)
     hipLaunchKernelGGL(unset_kernel, grid_of((maps + 511) / 512), dim3(256), 0, s, w.counter, w.maps, maps, w.starts, starts);
 }
 
-// Whether the gradient's workgroups walk through whole runs: from one workgroup per compute unit on.
+// Whether the gradient's workgroups walk through whole runs with this many channels per lane: from one workgroup per
+// compute unit on.  Tiles / runs: 512 workgroups (16 x 1024 x 2048 float32) 210 / 188 us, 256 (8 x 2048 x 4096 bfloat16, 2
+// channels) 266 / 213, 128 (8 x 2048 x 1024 float32) 119 / 134, 16 (one run of 16384 x 2048
+// float16) 142 / 1358.
 constexpr uint64_t kRunWorkgroups = 256;
-bool by_runs(const Cut& c, uint32_t blocks)
+bool by_runs(const Cut& c, uint32_t channels, int per_lane)
 {
+    const uint32_t blocks = (channels + 64 * per_lane - 1) / (64 * per_lane);
     return !c.seqs.offsets && c.run > 1 && c.run_rows == c.seqs.len && (uint64_t)c.runs * blocks >= kRunWorkgroups;
 }
 
@@ -990,7 +996,7 @@ scan_status_t forward(const gated_scan_args_t& a, hipStream_t s)
     return with_dtype(a.dtype, [&](auto e) -> scan_status_t {
         using T = decltype(e);
         scan_status_t st = SCAN_OK;
-        with_channels<4>(v, [&](auto n) {
+        with_channels<std::is_same<T, float>::value ? 2 : 4>(v, [&](auto n) {
             constexpr int V = decltype(n)::value;
             p.blocks = (a.channels + 64 * V - 1) / (64 * V);
             const bool chain = p.cut.run > 1;
@@ -1022,12 +1028,13 @@ scan_status_t gradient(const gated_scan_grad_args_t& g, hipStream_t s)
         scan_status_t st = SCAN_OK;
         with_channels<2>(v, [&](auto n) {
             constexpr int V = decltype(n)::value;
-            p.blocks = (a.channels + 64 * V - 1) / (64 * V);
-            // two channels of float32 rows per lane would spill registers
+            // Whole runs: two channels of float32 rows per lane would spill registers; rows of 16 bits take one where two leave too few
+            // workgroups: 4 x 2048 x 4096 bfloat16 tiles / runs 139 / 119 us, 8 x 2048 x 2048 145 / 121.
             constexpr int RV = std::is_same<T, float>::value ? 1 : V;
-            const uint32_t run_blocks = (a.channels + 64 * RV - 1) / (64 * RV);
-            const bool chain = p.cut.run > 1, runs = by_runs(p.cut, run_blocks);
-            if (runs) p.blocks = run_blocks;
+            const int run_channels = by_runs(p.cut, a.channels, RV) ? RV : 1;
+            const bool chain = p.cut.run > 1, runs = by_runs(p.cut, a.channels, run_channels);
+            const uint32_t width = 64 * (runs ? run_channels : V);
+            p.blocks = (a.channels + width - 1) / width;
             const uint64_t wgs = (uint64_t)p.cut.tiles * p.blocks, extra = g.dinitial_state && a.seqs ? kEmptyStep : 0;
             if (wgs + extra > kMostInGrid) {
                 st = SCAN_ERR_INVALID;
@@ -1035,7 +1042,8 @@ scan_status_t gradient(const gated_scan_grad_args_t& g, hipStream_t s)
             }
             if (chain && !runs) unset(p.cut, p.ws, s);
             if (runs)
-                hipLaunchKernelGGL((backward_run_kernel<T, RV>), grid_of((uint64_t)p.cut.runs * p.blocks), dim3(kWaves * 64), 0, s, p);
+                hipLaunchKernelGGL((run_channels == RV ? backward_run_kernel<T, RV> : backward_run_kernel<T, 1>),
+                                   grid_of((uint64_t)p.cut.runs * p.blocks), dim3(kWaves * 64), 0, s, p);
             else if (wgs + extra)
                 hipLaunchKernelGGL((chain ? backward_kernel<T, V, true> : backward_kernel<T, V, false>), grid_of(wgs + extra),
                                    dim3(kWaves * 64), 0, s, p);

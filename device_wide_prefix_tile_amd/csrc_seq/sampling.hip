@@ -34,8 +34,8 @@ constexpr int kWaves = kBlock / 64;
 constexpr int kBins = 2 * kBlock;
 constexpr float kPerOctave = 32.0f;  // the last bin holds weights below 2^-64, which are 0 as multiples of 2^-44
 constexpr uint32_t kList = 4096;     // logits of the bin with the border that are kept in LDS; more are looked up in the row
-// Of them, every one is compared with every other one, up to this many: 300 rows of 1000 float32 logits 28 us, 35 by digits
-// alone; with up to 512 256 rows of 128000 bfloat16 logits and top-p 125 instead of 91.
+// Of them, every one is compared with every other one, up to this many.  0 / 64 / 512: 300 rows of 1000 float32 logits 36 / 28 /
+// 28 us, 64 of 50001 64 / 57 / 65, 256 of 128000 bfloat16 with top-p 91 / 91 / 126.
 constexpr uint32_t kRanked = 64;
 constexpr int kMostSums = (kMaxTokens / 4 + 1 + kBlock - 1) / kBlock * kWaves;
 

@@ -108,7 +108,7 @@ def test_batch(t, b, l, d):
 
 
 @pytest.mark.parametrize("t", list(T))
-@pytest.mark.parametrize("b,l,d", [(260, 130, 24), (128, 65, 200), (33, 200, 1030), (256, 128, 3)])
+@pytest.mark.parametrize("b,l,d", [(260, 130, 24), (128, 65, 200), (33, 200, 1030), (256, 128, 3), (130, 65, 128), (100, 70, 140)])
 def test_many_sequences_at_once(t, b, l, d):
     """Enough sequences that workgroups walk through whole ones in the gradient; last tiles of one to all rows."""
     rng = np.random.default_rng(b + l + d)
