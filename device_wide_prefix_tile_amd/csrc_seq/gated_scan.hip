@@ -965,9 +965,8 @@ void unset(const Cut& c, const Space& w, hipStream_t s)
 }
 
 // Whether the gradient's workgroups walk through whole runs with this many channels per lane: from one workgroup per
-// compute unit on.  Tiles / runs: 512 workgroups (16 x 1024 x 2048 float32) 210 / 188 us, 256 (8 x 2048 x 4096 bfloat16, 2
-// channels) 266 / 213, 128 (8 x 2048 x 1024 float32) 119 / 134, 16 (one run of 16384 x 2048
-// float16) 142 / 1358.
+// compute unit on.  Tiles / runs: 512 workgroups, float32, 16 x 1024 x 2048 210 / 190 us, 8 x 2048 x 4096 398 / 408 to 425; 256 (8 x
+// 2048 x 4096 bfloat16, 2 channels) 266 / 213; 128 (8 x 2048 x 1024 float32) 119 / 134; 16 (one run of 16384 x 2048 float16) 142 / 1358.
 constexpr uint64_t kRunWorkgroups = 256;
 bool by_runs(const Cut& c, uint32_t channels, int per_lane)
 {

@@ -584,7 +584,7 @@ __device__ __forceinline__ bool sample_sorted(const P& pieces, const Scale& scal
 // ------------------------------------------------------------ the kernel
 // 512 rows of 131072 bfloat16 logits without a cut 62 us: HBM is read once (134 MB, 20 us), the second pass comes from the
 // caches; vector units busy 66%.  256 x 128000 with settings of their own 121 us: the longest row's, which takes five
-// passes (counts, their border, weights, their border, sums) and some 15 us of barriers.
+// passes (counts, their border, weights, their border, sums).
 template <typename T>
 __global__ __launch_bounds__(kBlock) void sample_kernel(Settings set, uint32_t rows, uint32_t n, const T* __restrict__ logits,
                                                         int64_t stride, void* __restrict__ tokens, int token_bytes)
