@@ -17,9 +17,11 @@
 // eight bits of their value at a time).  Weights so small that all of the row's tokens with such weights could not hold the share that
 // top-p leaves out are only added up.
 //
-// Weights are integers there (multiples of 2^-44), so that the order in which LDS atomics add them up does not matter:
-// 2^19 of them fit 64 bits.  The final sums over a row are of fixed order, in 32 bits over a wavefront's 64 pieces of
-// 16 bytes and in 64 bits beyond.
+// Weights and their sums are held in 64 bits: of 2^17 kept tokens each has some 2^-17 of the sum, and an error of e in
+// the running sum moves a row's token with a probability of some 2^17 e.  (32 bits in the weights or in the partial sums, one
+// alone as much as both, gave another token than the definition in 1 of 800 rows of 131072.)  Where LDS atomics add weights
+// up, they are integers, so that the order does not matter: rounded multiples of 2^-63 n, of which n fit 64 bits.  All other
+// sums are of fixed order.
 #include <cfloat>
 #include <cmath>
 
@@ -58,6 +60,7 @@ struct Shared {
     uint32_t list_index[kList];
     double sums[kMostSums];
     uint64_t part[kWaves];
+    double dpart[kWaves];
     float fpart[kWaves];
     uint32_t upart[kWaves];
     uint64_t base;
@@ -171,11 +174,14 @@ __device__ __forceinline__ uint32_t block_min(uint32_t v, Shared& s)
 // The sum over the wavefront, in lane 63, in an order that depends on the lanes alone: within rows of 16, then over
 // the rows.
 template <int CTRL, int ROWS>
-__device__ __forceinline__ float add_from(float v)
+__device__ __forceinline__ double add_from(double v)
 {
-    return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 0xF, false));
+    const u32x2 u = __builtin_bit_cast(u32x2, v);
+    const u32x2 o = {(uint32_t)__builtin_amdgcn_update_dpp(0, (int)u.x, CTRL, ROWS, 0xF, false),
+                     (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u.y, CTRL, ROWS, 0xF, false)};
+    return v + __builtin_bit_cast(double, o);
 }
-__device__ __forceinline__ float wave_sum(float v)
+__device__ __forceinline__ double wave_sum(double v)
 {
     v = add_from<0x111, 0xF>(v);  // row_shr:1
     v = add_from<0x112, 0xF>(v);
@@ -185,50 +191,87 @@ __device__ __forceinline__ float wave_sum(float v)
     return add_from<0x143, 0xC>(v);  // row_bcast:31 into rows 2 and 3
 }
 
-// Exclusive prefix over the threads, and the sum.
-__device__ __forceinline__ uint64_t block_prefix(uint64_t v, Shared& s, uint64_t& total)
+// Exclusive prefix over the threads, and the sum, in a fixed order.  part: kWaves values in LDS.
+template <typename N>
+__device__ __forceinline__ N block_prefix(N v, N* part, N& total)
 {
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    uint64_t incl = v;
+    N incl = v;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
-        const uint64_t t = __shfl_up((unsigned long long)incl, o, 64);
+        const N t = __shfl_up(incl, o, 64);
         if (lane >= o) incl += t;
     }
+    const N excl = __shfl_up(incl, 1, 64);
     __syncthreads();
-    if (lane == 63) s.part[w] = incl;
+    if (lane == 63) part[w] = incl;
     __syncthreads();
-    uint64_t before = 0, all = 0;
+    N before = 0, all = 0;
 #pragma unroll
     for (int q = 0; q < kWaves; ++q) {
-        before += q < w ? s.part[q] : 0;
-        all += s.part[q];
+        before = q < w ? before + part[q] : before;
+        all += part[q];
     }
     total = all;
-    return before + incl - v;
+    return lane ? before + excl : before;
 }
+__device__ __forceinline__ uint64_t block_prefix(uint64_t v, Shared& s, uint64_t& total)
+{
+    unsigned long long all;
+    const uint64_t before = block_prefix<unsigned long long>(v, reinterpret_cast<unsigned long long*>(s.part), all);
+    total = all;
+    return before;
+}
+__device__ __forceinline__ double block_prefix(double v, Shared& s, double& total) { return block_prefix<double>(v, s.dpart, total); }
 
 // ------------------------------------------------------------ weights
-// t = log2 of the weight: (logit - max) log2(e) / temperature, the factor in two parts (both above 0, so that minus
-// infinity stays what it is).  pre is 1, or 2^-100 for temperatures from 2^60 on, whose factor holds the 2^100.  Next to a
+// 2^t for t <= 0 in 64 bits.  With n the integer next to t and f = t - n (exact), 2^f = 1 + f q(f): q of degree 8 takes the
+// values of (2^f - 1) / f at nine Chebyshev nodes of [-1/2, 1/2] (computed in 70 digits), the error is 2^-44.6 at most, and
+// 2^0 is 1.  Below 2^-1074 the weight is 0.
+__device__ __forceinline__ double exp2_wide(double t)
+{
+    t = fmax(t, -1100.0);
+    const double n = __builtin_rint(t), f = t - n;
+    double q = 0x1.b63880a30e9ffp-24;
+    q = fma(q, f, 0x1.63d136366db24p-20);
+    q = fma(q, f, 0x1.ffcb9515a8016p-17);
+    q = fma(q, f, 0x1.4308ac85aa947p-13);
+    q = fma(q, f, 0x1.5d87fe86fe88ep-10);
+    q = fma(q, f, 0x1.3b2ab7181b755p-7);
+    q = fma(q, f, 0x1.c6b08d7047e52p-5);
+    q = fma(q, f, 0x1.ebfbdff823cedp-3);
+    q = fma(q, f, 0x1.62e42fefa39efp-1);
+    return __builtin_amdgcn_ldexp(fma(f, q, 1.0), (int)n);
+}
+
+// Weights, and where they lie.  t = log2 of the weight, (logit - max) log2(e) / temperature.
+// For the bins 32 bits of t are enough, as long as t falls with the logit: the factor in two parts (both above 0, so that
+// minus infinity stays what it is); pre is 1, or 2^-100 for temperatures from 2^60 on, whose factor holds the 2^100.  Next to a
 // plus infinity everything else is at minus infinity; its own difference is NaN, of which the minimum with 0 makes 0.
+// The weight itself in 64 bits: the difference is exact but for its last bit, top is 2^1000 next to a plus infinity.
 struct Scale {
     float pre, max, hi, lo;  // max: times pre
+    double top, factor, unit;  // unit: of weights as integers
 
     __device__ float log2_weight(float logit) const
     {
         const float d = fminf(fmaf(logit, pre, -max), 0.0f);
         return fmaf(d, lo, d * hi);
     }
-    __device__ static float weight(float t) { return exp2_fast(t); }
+    __device__ double weight(float logit) const { return exp2_wide(fmin(((double)logit - top) * factor, 0.0)); }
+    // The weight as a multiple of 1 / unit
+    __device__ uint64_t mass(double w) const { return (uint64_t)fma(w, unit, 0.5); }
     // The logit whose weight is 2^t, but for roundings; minus infinity where that is not to be had.
     __device__ bool usual() const { return pre == 1.0f && max < INFINITY; }
     __device__ float logit_at(float t) const { return usual() ? max + t / (hi + lo) : -INFINITY; }
 };
 
-__device__ __forceinline__ Scale make_scale(float max, double temperature)
+// n: logits of a row
+__device__ __forceinline__ Scale make_scale(float max, double temperature, uint32_t n)
 {
     double c = 1.4426950408889634 / temperature;
+    // an infinite temperature: 2^-200 makes all weights of finite logits 1; above 2^900 only ties with the largest are left
+    const double factor = fmin(fmax(c, 0x1p-200), 0x1p900);
     const bool high = c < 0x1p-60;
     if (high) c *= 0x1p100;
     // an infinite temperature: 2^-160 makes all weights of finite logits 1; above 2^100 only ties with the largest are left
@@ -236,19 +279,12 @@ __device__ __forceinline__ Scale make_scale(float max, double temperature)
     float hi = (float)c;
     if ((double)hi >= c) hi = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, hi) - 1);
     const float pre = high ? 0x1p-100f : 1.0f;
-    return Scale{pre, max == INFINITY ? max : max * pre, hi, (float)(c - (double)hi)};
+    const int bits = n > 1 ? 32 - __builtin_clz(n - 1) : 0;  // n <= 2^bits
+    return Scale{pre, max == INFINITY ? max : max * pre, hi, (float)(c - (double)hi), max == INFINITY ? 0x1p1000 : (double)max, factor,
+                 __builtin_amdgcn_ldexp(1.0, 63 - bits)};
 }
 
 __device__ __forceinline__ uint32_t bin_of(float t) { return (uint32_t)fminf(-t * kPerOctave, (float)(kBins - 1)); }
-
-// floor(w 2^44), w <= 1
-__device__ __forceinline__ uint64_t mass(float w)
-{
-    const float s = w * 0x1p44f;
-    const uint32_t hi = (uint32_t)(s * 0x1p-32f);
-    const uint32_t lo = (uint32_t)fmaf((float)hi, -0x1p32f, s);
-    return (uint64_t)hi << 32 | lo;
-}
 
 // Unsigned numbers in the order of the floats; both zeros are one.
 __device__ __forceinline__ uint32_t key_of(float f)
@@ -271,10 +307,10 @@ struct Cut {
 
 // What an element counts: 1 (COUNT), or its weight as an integer, if `all` keeps it (ALL: it keeps everything); 0 elsewhere.
 template <bool COUNT, bool ALL>
-__device__ __forceinline__ uint64_t value_of(float l, uint32_t i, float t, const Cut& all)
+__device__ __forceinline__ uint64_t value_of(float l, uint32_t i, const Scale& scale, const Cut& all)
 {
     if (!ALL && !all.keeps(l, i)) return 0;
-    return COUNT ? 1u : mass(Scale::weight(t));
+    return COUNT ? 1u : scale.mass(scale.weight(l));
 }
 
 // A logit that at least k of the row's reach: the least of the threads' largest logits up to the bin in which the k-th of
@@ -312,23 +348,22 @@ __device__ __forceinline__ Cut find_cut(const P& pieces, const Scale& scale, con
     __syncthreads();
     // the row's weights below this logit add up to less than half of what the share leaves out of a sum of at least 1
     const float small = COUNT ? bound : scale.logit_at(__builtin_amdgcn_logf((float)((1.0 - share) / row.n)) - 1.0f);
-    float rest = 0.0f;
+    double rest = 0.0;
     pieces.each([&](uint32_t q, const float(&l)[V]) __attribute__((always_inline)) {
+        double w[V];
         if (!COUNT) {
-            // their sum: one part of the factor is enough for it
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                const float w = exp2_fast((l[e] - scale.max) * scale.hi);
-                rest += l[e] < small && (ALL || all.keeps(l[e], row.index(q, e))) ? w : 0.0f;
+                w[e] = ALL || all.keeps(l[e], row.index(q, e)) ? scale.weight(l[e]) : 0.0;
+                rest += l[e] < small ? w[e] : 0.0;
             }
         }
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             if (l[e] < small) continue;
             // one more minus infinity among the counts is one more in the last bin, behind every other
-            const float t = scale.log2_weight(l[e]);
-            const uint64_t v = value_of<COUNT, ALL>(l[e], row.index(q, e), t, all);
-            if (ALL || v) atomicAdd((unsigned long long*)&s.bins[bin_of(t)], (unsigned long long)v);
+            const uint64_t v = COUNT ? (uint64_t)(ALL || all.keeps(l[e], row.index(q, e))) : scale.mass(w[e]);
+            if (ALL || v) atomicAdd((unsigned long long*)&s.bins[bin_of(scale.log2_weight(l[e]))], (unsigned long long)v);
         }
     });
     __syncthreads();
@@ -337,7 +372,7 @@ __device__ __forceinline__ Cut find_cut(const P& pieces, const Scale& scale, con
     const uint64_t before = block_prefix(b0 + b1, s, total);
     if (!COUNT) {
         uint64_t more;
-        block_prefix(mass(rest), s, more);
+        block_prefix(scale.mass(rest), s, more);
         limit = max((uint64_t)1, (uint64_t)ceil(share * (double)(total + more)));
     }
     if (before < limit && limit <= before + b0 + b1) {
@@ -362,8 +397,7 @@ __device__ __forceinline__ Cut find_cut(const P& pieces, const Scale& scale, con
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             if (!(l[e] >= from && l[e] <= to)) continue;
-            const float t = scale.log2_weight(l[e]);
-            if (bin_of(t) == bin && value_of<COUNT, ALL>(l[e], row.index(q, e), t, all)) {
+            if (bin_of(scale.log2_weight(l[e])) == bin && value_of<COUNT, ALL>(l[e], row.index(q, e), scale, all)) {
                 const uint32_t at = atomicAdd(&s.count, 1u);
                 if (at < kList) {
                     s.list_logit[at] = l[e];
@@ -379,7 +413,7 @@ __device__ __forceinline__ Cut find_cut(const P& pieces, const Scale& scale, con
         const bool in = tid < listed;
         const float l = in ? s.list_logit[tid] : 0.0f;
         const uint32_t index = in ? s.list_index[tid] : 0;
-        const uint64_t v = !in ? 0 : COUNT ? 1 : mass(Scale::weight(scale.log2_weight(l)));
+        const uint64_t v = !in ? 0 : COUNT ? 1 : scale.mass(scale.weight(l));
         if (in) s.bins[tid] = v;
         if (tid == 0) s.at = 0;
         __syncthreads();
@@ -404,16 +438,15 @@ __device__ __forceinline__ Cut find_cut(const P& pieces, const Scale& scale, con
         if (listed <= kList) {
             for (uint32_t k = tid; k < listed; k += kBlock) {
                 const float l = s.list_logit[k];
-                f(l, s.list_index[k], COUNT ? (uint64_t)1 : mass(Scale::weight(scale.log2_weight(l))));
+                f(l, s.list_index[k], COUNT ? (uint64_t)1 : scale.mass(scale.weight(l)));
             }
         } else {
             for (uint32_t q = tid; q < row.pieces; q += kBlock) {
                 float l[V];
                 unpack_clean(row.load(q), l);
                 for (int e = 0; e < V; ++e) {
-                    const float t = scale.log2_weight(l[e]);
-                    if (bin_of(t) != bin) continue;
-                    const uint64_t v = value_of<COUNT, ALL>(l[e], row.index(q, e), t, all);
+                    if (bin_of(scale.log2_weight(l[e])) != bin) continue;
+                    const uint64_t v = value_of<COUNT, ALL>(l[e], row.index(q, e), scale, all);
                     if (v) f(l[e], row.index(q, e), v);
                 }
             }
@@ -448,7 +481,7 @@ __device__ __forceinline__ Cut find_cut(const P& pieces, const Scale& scale, con
     }
     if (!(key & 0x80000000u)) key |= (1u << P::kZeros) - 1;  // the bits of negative numbers are turned over
     const float logit = logit_of(key);
-    const uint64_t each_value = COUNT ? 1 : mass(Scale::weight(scale.log2_weight(logit)));
+    const uint64_t each_value = COUNT ? 1 : scale.mass(scale.weight(logit));
     const uint64_t wanted = (limit - base + each_value - 1) / each_value, there = equal / each_value;
     if (wanted >= there) return Cut{logit, all.logit == logit ? all.index : 0xFFFFFFFFu};
 
@@ -478,6 +511,9 @@ __device__ __forceinline__ Cut find_cut(const P& pieces, const Scale& scale, con
     return Cut{logit, index};
 }
 
+// What the sums are compared with; with a random number of 1 no sum exceeds it, however it was rounded.
+__device__ __forceinline__ double share_of(float uniform, double total) { return uniform < 1.0f ? (double)uniform * total : INFINITY; }
+
 // ------------------------------------------------------------ top-k by sorting
 // Sorts a[0 .. size) ascending (size: a power of two, at most 2 kBlock).
 __device__ void sort(uint64_t* a, uint32_t size)
@@ -505,7 +541,7 @@ __device__ __forceinline__ uint32_t power_of_two(uint32_t n)
 
 // The token, if no more than kSorted of the row's logits reach `bound`, which the first k do; false elsewhere.
 template <typename P>
-__device__ __forceinline__ bool sample_sorted(const P& pieces, const Scale& scale, float bound, uint32_t k, double top_p, float least, float uniform,
+__device__ __forceinline__ bool sample_sorted(const P& pieces, const Scale& scale, float bound, uint32_t k, double top_p, double least, float uniform,
                                               Shared& s, uint32_t& token)
 {
     constexpr int V = P::V;
@@ -532,26 +568,25 @@ __device__ __forceinline__ bool sample_sorted(const P& pieces, const Scale& scal
     sort(s.bins, size);
     const uint32_t first = min(k, count);
     // thread t has ranks 2 t and 2 t + 1
-    uint64_t m[2], total;
-    uint32_t index[2];
-    float w[2];
+    double w[2], total;
+    uint64_t entry[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const uint32_t r = 2 * tid + j;
         const uint64_t v = r < first ? s.bins[r] : 0;
-        index[j] = (uint32_t)v;
-        w[j] = r < first ? Scale::weight(scale.log2_weight(logit_of(~(uint32_t)(v >> 32)))) : 0.0f;
-        m[j] = mass(w[j]);
+        const float l = logit_of(~(uint32_t)(v >> 32));
+        entry[j] = v << 32 | __builtin_bit_cast(uint32_t, l);
+        w[j] = r < first ? scale.weight(l) : 0.0;
     }
-    const uint64_t before = block_prefix(m[0] + m[1], s, total);
-    const uint64_t limit = top_p < 1.0 ? max((uint64_t)1, (uint64_t)ceil(fmax(top_p, 0.0) * (double)total)) : ~0ull;
+    const double before = block_prefix(w[0] + w[1], s, total);
+    const double limit = top_p < 1.0 ? fmax(top_p, 0.0) * total : INFINITY;
     if (tid == 0) s.count = 0;
     __syncthreads();
-    // what is kept, by index; weights that are 0 as integers are never met
+    // what is kept, by index
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        if (m[j] && (j ? before + m[0] : before) < limit && w[j] >= least)
-            s.bins[atomicAdd(&s.count, 1u)] = (uint64_t)index[j] << 32 | __builtin_bit_cast(uint32_t, w[j]);
+        if (w[j] > 0.0 && ((j ? before + w[0] : before) < limit || 2 * tid + j == 0) && w[j] >= least)
+            s.bins[atomicAdd(&s.count, 1u)] = entry[j];
     }
     __syncthreads();
     const uint32_t kept = s.count;
@@ -561,21 +596,16 @@ __device__ __forceinline__ bool sample_sorted(const P& pieces, const Scale& scal
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const uint32_t r = 2 * tid + j;
-        const uint64_t v = r < kept ? s.bins[r] : 0;
-        index[j] = (uint32_t)(v >> 32);
-        m[j] = r < kept ? mass(__builtin_bit_cast(float, (uint32_t)v)) : 0;
+        entry[j] = r < kept ? s.bins[r] : 0;
+        w[j] = r < kept ? scale.weight(__builtin_bit_cast(float, (uint32_t)entry[j])) : 0.0;
     }
-    const uint64_t start = block_prefix(m[0] + m[1], s, total);
-    const double target = (double)uniform * (double)total;
+    const double start = block_prefix(w[0] + w[1], s, total);
+    const double target = share_of(uniform, total);
     // the first whose sum exceeds the target, else the last
-    if (tid == 0) s.at = (uint32_t)(s.bins[kept - 1] >> 32);
-    __syncthreads();
-    if ((double)start <= target) {
-        if ((double)(start + m[0]) > target)
-            s.at = index[0];
-        else if ((double)(start + m[0] + m[1]) > target)
-            s.at = index[1];
-    }
+    uint32_t over = kept - 1;
+    if (start + (w[0] + w[1]) > target) over = min(over, 2 * tid + (start + w[0] > target ? 0u : 1u));
+    over = block_min(over, s);
+    if (tid == 0) s.at = (uint32_t)(s.bins[over] >> 32);
     __syncthreads();
     token = s.at;
     return true;
@@ -631,12 +661,8 @@ __global__ __launch_bounds__(kBlock) void sample_kernel(Settings set, uint32_t r
         if (tid == 0) result(first);
         return;
     }
-    const Scale scale = make_scale(most, temperature);
-    float least = 0.0f;  // the smallest float that is not below min_p
-    if (min_p > 0.0) {
-        least = (float)fmin(min_p, 1.0);
-        if ((double)least < fmin(min_p, 1.0)) least = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, least) + 1);
-    }
+    const Scale scale = make_scale(most, temperature, n);
+    const double least = min_p > 0.0 ? fmin(min_p, 1.0) : 0.0;
     Cut cut{-INFINITY, 0xFFFFFFFFu};
     if (top_k > 0 && top_k < (int64_t)n) {
         uint32_t token;
@@ -653,14 +679,14 @@ __global__ __launch_bounds__(kBlock) void sample_kernel(Settings set, uint32_t r
     }
     // The kept weights of a piece, and their sum.  CHECK 0: everything is kept, 1: logits from the cut's on with the least
     // weight, 2: some of those that equal the cut's are not.
-    const auto kept = [&](auto check, uint32_t q, const float(&l)[V], float(&f)[V]) __attribute__((always_inline)) {
+    const auto kept = [&](auto check, uint32_t q, const float(&l)[V], double(&f)[V]) __attribute__((always_inline)) {
         constexpr int CHECK = decltype(check)::value;
-        float sum = 0.0f;
+        double sum = 0.0;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-            const float v = Scale::weight(scale.log2_weight(l[e]));
+            const double v = scale.weight(l[e]);
             const bool keep = CHECK == 0 || (v >= least && (CHECK == 1 ? l[e] >= cut.logit : cut.keeps(l[e], row.index(q, e))));
-            f[e] = keep ? v : 0.0f;
+            f[e] = keep ? v : 0.0;
             sum += f[e];
         }
         return sum;
@@ -674,9 +700,9 @@ __global__ __launch_bounds__(kBlock) void sample_kernel(Settings set, uint32_t r
                 for (int e = 1; e < V; ++e) largest = fmaxf(largest, l[e]);
                 if (!__builtin_amdgcn_ballot_w64(largest >= cut.logit)) return;
             }
-            float f[V];
-            const float sum = wave_sum(kept(check, q, l, f));
-            if (lane == 63) s.sums[q / kBlock * kWaves + w] = (double)sum;
+            double f[V];
+            const double sum = wave_sum(kept(check, q, l, f));
+            if (lane == 63) s.sums[q / kBlock * kWaves + w] = sum;
         });
     };
     const uint32_t entries = (row.pieces + kBlock - 1) / kBlock * kWaves;
@@ -684,7 +710,7 @@ __global__ __launch_bounds__(kBlock) void sample_kernel(Settings set, uint32_t r
     __syncthreads();
     if (cut.index != 0xFFFFFFFFu)
         sums(std::integral_constant<int, 2>());
-    else if (cut.logit > -INFINITY || least > 0.0f)
+    else if (cut.logit > -INFINITY || least > 0.0)
         sums(std::integral_constant<int, 1>());
     else
         sums(std::integral_constant<int, 0>());
@@ -708,7 +734,7 @@ __global__ __launch_bounds__(kBlock) void sample_kernel(Settings set, uint32_t r
     double own = 0.0;
     for (uint32_t k = lo; k < hi; ++k) own += s.sums[k];
     double incl = prefix(own);
-    const double target = (double)uniform01 * __shfl(incl, 63, 64);
+    const double target = share_of(uniform01, __shfl(incl, 63, 64));
     int leader = pick(incl, own, target);
     // that lane's entries one after another; every lane walks along
     const uint32_t from = (uint32_t)__builtin_amdgcn_readlane((int)lo, leader), to = (uint32_t)__builtin_amdgcn_readlane((int)hi, leader);
@@ -724,13 +750,14 @@ __global__ __launch_bounds__(kBlock) void sample_kernel(Settings set, uint32_t r
         at += v;
     }
     const uint32_t q = entry / kWaves * kBlock + entry % kWaves * 64 + lane;
-    float l[V], f[V];
+    float l[V];
+    double f[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) f[e] = 0.0f;
+    for (int e = 0; e < V; ++e) f[e] = 0.0;
     own = 0.0;
     if (q < row.pieces) {
         unpack_clean(row.load(q), l);
-        own = (double)kept(std::integral_constant<int, 2>(), q, l, f);
+        own = kept(std::integral_constant<int, 2>(), q, l, f);
     }
     incl = base + prefix(own);
     leader = pick(incl, own, target);
@@ -738,9 +765,9 @@ __global__ __launch_bounds__(kBlock) void sample_kernel(Settings set, uint32_t r
     at = incl - own;
     uint32_t token = 0;
     for (int e = 0; e < V; ++e) {
-        if (f[e] > 0.0f) {
+        if (f[e] > 0.0) {
             token = row.index(q, e);
-            at += (double)f[e];
+            at += f[e];
             if (at > target) break;
         }
     }

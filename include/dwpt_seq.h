@@ -426,7 +426,8 @@ scan_status_t expert_combine_grad(const expert_combine_grad_args_t* args, void* 
  *   tokens[r] = the first kept i, by ascending index, up to which the kept weights add up to more than
  *     uniform[r] times the kept weight (uniform outside [0, 1): the first or the last)
  * A temperature that is not above 0 takes the first largest logit.  A row without a finite or plus infinite
- * logit gives -1.  Weights are held in 32 bits, their sums in 64.  tokens: int32 (token_bytes 4) or int64 (8).
+ * logit gives -1.  Weights (off by 2^-44 of themselves at most, 0 below 2^-1074) and their sums are held in 64 bits.
+ * tokens: int32 (token_bytes 4) or int64 (8).
  */
 typedef struct {
     int32_t dtype, token_bytes;
