@@ -98,14 +98,15 @@ struct Row {
     }
 };
 
-// Logits in 32 bits; NaN becomes minus infinity (the maximum of a number and NaN is the number).
+// Logits in 32 bits; NaN becomes minus infinity.  By a comparison: the hardware's maximum of a number and a signalling NaN
+// is a NaN.
 template <typename T, int V>
 __device__ __forceinline__ void unpack_clean(const Pack<T, V>& p, float (&l)[V])
 {
 #pragma unroll
     for (int e = 0; e < V; ++e) {
         const float v = (float)p.v[e];
-        asm("v_max_f32 %0, 0xff800000, %1" : "=v"(l[e]) : "v"(v));
+        l[e] = v == v ? v : -INFINITY;
     }
 }
 
