@@ -201,12 +201,17 @@ __device__ __forceinline__ float one_minus_square(float a, float y)
     return y >= -0.5f * kLog2e ? a * y * s : fmaf(-a, a, 1.0f);
 }
 
+// The hardware's roots take values below 2^-126 as 0 (the inverse one is infinite then): 1 - a^2 of a nearly closed gate
+// is that small, so the roots are taken of 2^24 times as much.  (Forward and gradient of 8 x 2048 x 4096 bfloat16 339 us
+// with, 337 without.)
+constexpr float kRootScale = 0x1p24f, kRootBack = 0x1p-12f;
+
 // A row's map h -> a h + b; log2_rate: the rate times log2 e.
 __device__ __forceinline__ void make_map(float decay, float input, float x, float log2_rate, float& a, float& b)
 {
     const float y = log2_rate * sigmoid(decay);
     a = exp2_fast(y);
-    b = __builtin_amdgcn_sqrtf(one_minus_square(a, y)) * sigmoid(input) * x;
+    b = __builtin_amdgcn_sqrtf(one_minus_square(a, y) * kRootScale) * kRootBack * sigmoid(input) * x;
 }
 
 // ------------------------------------------------------------ a wavefront's rows
@@ -566,8 +571,8 @@ __device__ __forceinline__ void make_factors(float decay, float input, float x, 
     const float f = rcp_fast(1.0f + eu), g = rcp_fast(1.0f + es), gx = g * x;
     const float y = rate * kLog2e * f;
     a = exp2_fast(y);
-    const float w2 = one_minus_square(a, y), w = __builtin_amdgcn_sqrtf(w2);
-    const float back = w2 == 0.0f ? 0.0f : __builtin_amdgcn_rsqf(w2);  // 1 / w
+    const float w2 = one_minus_square(a, y) * kRootScale, w = __builtin_amdgcn_sqrtf(w2) * kRootBack;
+    const float back = w2 == 0.0f ? 0.0f : __builtin_amdgcn_rsqf(w2) * (1.0f / kRootBack);  // 1 / w
     const float b = w * gx;
     fx = w * g;
     fi = b * rest(es, g);

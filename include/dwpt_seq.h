@@ -301,7 +301,7 @@ size_t gated_scan_saved(const gated_scan_args_t* args);
  * Gradients of gated_scan for dy (and dfinal_state, may be NULL: zeros).  `args` are the forward call's, with
  * `saved` as it left it; y and final_state are not used, workspace is this call's.  dx, ddecay_gate and
  * dinput_gate of dtype; drate (summed over all rows) and dinitial_state (may be NULL) float32.  Where
- * 1 - a^2 is 0 in 32 bits (no decay), the derivative of its root is taken as 0.
+ * 1 - a^2 is 0 in 32 bits (no decay; a sigmoid below 2^-126 counts as 0), the derivative of its root is taken as 0.
  */
 typedef struct {
     gated_scan_args_t args;
