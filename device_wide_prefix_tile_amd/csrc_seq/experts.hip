@@ -224,7 +224,6 @@ __global__ __launch_bounds__(kBlock) void place_kernel(const int32_t* __restrict
 struct Moves {
     const int32_t* places;
     uint32_t tokens, rows, choices, channels;
-    const int32_t* used;  // device: rows of the experts' order that have an expert
 };
 
 // The place of choice j of token t; -1 if there is none in the array.
@@ -253,15 +252,43 @@ __device__ __forceinline__ Pack<T, V> load_stream(const T* p)
         return load_pack<T, V>(p);
 }
 
-constexpr uint32_t kClearStep = 256;  // workgroups that clear the rows of no expert
+// Which rows are cleared before a move fills those that a place leads to: from *used on, or all (used NULL).  Rows that
+// `source` shows to be led to are left out: the move writes them.
+struct Clear {
+    const int32_t *used, *source;
+    uint32_t source_rows;
+};
 
+// A workgroup looks at kClearRows rows and sets 64 V kClearParts channels of them to zero, a wavefront every fourth row.  It runs in front of the move, so a
+// row that is cleared although a place leads to it (a source of another origin) is written afterwards.  A map of the rows
+// that are led to would need memory; this needs the launch (2.4 us for 512 rows, 5.3 for 65536), and writes no more than the rows without a choice
+// where source is the split's.
+constexpr int kClearRows = 16;
+constexpr int kClearParts = 8;
 template <typename T, int V>
-__device__ __forceinline__ void clear_rows(const Moves& m, uint32_t wg, T* out, int64_t stride)
+__global__ __launch_bounds__(256) void clear_kernel(Moves m, Clear c, uint32_t chunks, T* __restrict__ out, int64_t stride)
 {
-    const int used = *m.used;
-    for (uint64_t r = (uint64_t)(used < 0 ? 0 : used) + wg; r < m.rows; r += kClearStep)
-        for (uint32_t c = threadIdx.x * V; c < m.channels; c += 256 * V)
-            *reinterpret_cast<Pack<T, V>*>(out + (int64_t)r * stride + c) = zero_pack<T, V>();
+    const uint32_t wg = workgroup();
+    const int lane = threadIdx.x & 63, w = uniform((int)(threadIdx.x >> 6));
+    const uint64_t r0 = (uint64_t)(wg / chunks) * kClearRows, r = r0 + (uint32_t)lane;
+    if (r0 >= m.rows) return;
+    bool empty = lane < kClearRows && r < m.rows;
+    if (empty && c.used) empty = (int64_t)r >= (int64_t)*c.used;
+    if (empty && r < c.source_rows) {
+        const int i = c.source[r];
+        empty = i < 0 || (uint32_t)i >= m.tokens * m.choices || m.places[i] != (int)r;
+    }
+    const uint32_t c0 = (wg % chunks * (64 * kClearParts) + (uint32_t)lane) * V;
+    int n = w;
+    for (uint64_t rows = __builtin_amdgcn_ballot_w64(empty); rows; rows &= rows - 1) {
+        if (n++ % 4) continue;
+        T* row = out + (int64_t)(r0 + (uint32_t)__builtin_ctzll(rows)) * stride;
+#pragma unroll
+        for (int u = 0; u < kClearParts; ++u) {
+            const uint32_t at = c0 + u * 64 * V;
+            if (at < m.channels) *reinterpret_cast<Pack<T, V>*>(row + at) = zero_pack<T, V>();
+        }
+    }
 }
 
 // A wavefront copies 64 V kCopies channels of a token to the token's places.  8192 tokens to 8 places of 2048 bfloat16
@@ -269,15 +296,10 @@ __device__ __forceinline__ void clear_rows(const Moves& m, uint32_t wg, T* out, 
 // every time, with 2 / 4 / 8 copies 51 / 55 / 60 us.
 constexpr int kCopies = 2;
 template <typename T, int V>
-__global__ __launch_bounds__(256) void dispatch_kernel(Moves m, uint32_t chunks, uint64_t workgroups, const T* __restrict__ x,
-                                                       int64_t x_stride, T* __restrict__ out, int64_t out_stride)
+__global__ __launch_bounds__(256) void dispatch_kernel(Moves m, uint32_t chunks, const T* __restrict__ x, int64_t x_stride,
+                                                       T* __restrict__ out, int64_t out_stride)
 {
-    const uint32_t wg = workgroup();
-    if (wg >= workgroups) {
-        if (m.used && wg - workgroups < kClearStep) clear_rows<T, V>(m, (uint32_t)(wg - workgroups), out, out_stride);
-        return;
-    }
-    const uint64_t unit = (uint64_t)wg * 4 + (uint32_t)uniform((int)(threadIdx.x >> 6));
+    const uint64_t unit = (uint64_t)workgroup() * 4 + (uint32_t)uniform((int)(threadIdx.x >> 6));
     const uint64_t t = unit / chunks;
     if (t >= m.tokens) return;
     const uint32_t c0 = (uint32_t)(unit % chunks * 64 * kCopies + (threadIdx.x & 63)) * V;
@@ -340,10 +362,7 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(Moves m, const W* __r
 {
     __shared__ float s_sum[4][kAhead];
     const uint32_t t = workgroup();
-    if (t >= m.tokens) {
-        if (m.used && t - m.tokens < kClearStep) clear_rows<T, V>(m, t - m.tokens, dy, dy_stride);
-        return;
-    }
+    if (t >= m.tokens) return;
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     for (uint32_t j0 = 0; j0 < m.choices; j0 += kAhead) {
         int at[kAhead];
@@ -436,6 +455,22 @@ scan_status_t check_moves(int dtype, uint64_t tokens, uint64_t rows, uint32_t ch
     return (tokens == 0 || places) && aligned(places, 4) ? SCAN_OK : SCAN_ERR_INVALID;
 }
 
+// Clears rows of `out`, rows of V elements per access, in front of a move; false if they are too many for a grid.
+template <typename T, int V>
+bool clear_rows(const Moves& m, const Clear& c, T* out, int64_t stride, hipStream_t s)
+{
+    const uint32_t chunks = (m.channels + 64 * kClearParts * V - 1) / (64 * kClearParts * V);
+    const uint64_t wgs = ((uint64_t)m.rows + kClearRows - 1) / kClearRows * chunks;
+    if (wgs > kMostInGrid) return false;
+    if (wgs) hipLaunchKernelGGL((clear_kernel<T, V>), grid_of(wgs), dim3(256), 0, s, m, c, chunks, out, stride);
+    return true;
+}
+
+bool valid_clear(const int32_t* used, const int32_t* source, uint64_t source_rows)
+{
+    return aligned(used, 4) && aligned(source, 4) && source_rows < ((uint64_t)1 << 31) && (source || source_rows == 0);
+}
+
 // Calls f with a value of the weights' type.
 template <typename T, class F>
 void with_weights(int weight_dtype, F f)
@@ -495,25 +530,29 @@ scan_status_t expert_dispatch(const expert_dispatch_args_t* args, void* stream)
     if (st != SCAN_OK) return st;
     if (!valid_rows(a.dtype, a.tokens, a.channels, {a.x, a.x_stride}) || !valid_rows(a.dtype, a.rows, a.channels, {a.out, a.out_stride}))
         return SCAN_ERR_INVALID;
-    if (!aligned(a.used, 4)) return SCAN_ERR_INVALID;
+    if (!valid_clear(a.used, a.source, a.source_rows)) return SCAN_ERR_INVALID;
     const size_t es = dtype_size(a.dtype);
     const Range outs[] = {range(a.out, a.rows, a.out_stride, a.channels, es)};
-    const Range ins[] = {range(a.x, a.tokens, a.x_stride, a.channels, es), range(a.places, a.tokens * a.choices * 4), range(a.used, 4)};
+    const Range ins[] = {range(a.x, a.tokens, a.x_stride, a.channels, es), range(a.places, a.tokens * a.choices * 4), range(a.used, 4),
+                         range(a.source, a.source_rows * 4)};
     if (any_overlap(outs, ins)) return SCAN_ERR_INVALID;
     if (a.rows == 0) return SCAN_OK;
-    const Moves m{a.places, (uint32_t)a.tokens, (uint32_t)a.rows, a.choices, a.channels, a.used};
+    const Moves m{a.places, (uint32_t)a.tokens, (uint32_t)a.rows, a.choices, a.channels};
+    const Clear c{a.clear ? nullptr : a.used, a.source, (uint32_t)a.source_rows};
+    const hipStream_t s = static_cast<hipStream_t>(stream);
     return with_dtype(a.dtype, [&](auto e) -> scan_status_t {
         using T = decltype(e);
         scan_status_t launch = SCAN_OK;
         with_pack<T>(a.channels, {{a.x, a.x_stride}, {a.out, a.out_stride}}, [&](auto n) {
             constexpr int V = decltype(n)::value;
             const uint32_t chunks = (a.channels + 64 * V * kCopies - 1) / (64 * V * kCopies);
-            const uint64_t wgs = (a.tokens * chunks + 3) / 4, extra = a.used ? kClearStep : 0;
-            if (wgs + extra > kMostInGrid)
+            const uint64_t wgs = (a.tokens * chunks + 3) / 4;
+            T* out = static_cast<T*>(a.out);
+            if (wgs > kMostInGrid || ((a.clear || a.used) && !clear_rows<T, V>(m, c, out, a.out_stride, s)))
                 launch = SCAN_ERR_INVALID;
-            else if (wgs + extra)
-                hipLaunchKernelGGL((dispatch_kernel<T, V>), grid_of(wgs + extra), dim3(256), 0, static_cast<hipStream_t>(stream), m, chunks,
-                                   wgs, static_cast<const T*>(a.x), a.x_stride, static_cast<T*>(a.out), a.out_stride);
+            else if (wgs)
+                hipLaunchKernelGGL((dispatch_kernel<T, V>), grid_of(wgs), dim3(256), 0, s, m, chunks, static_cast<const T*>(a.x), a.x_stride,
+                                   out, a.out_stride);
         });
         return launch == SCAN_OK ? launched() : launch;
     });
@@ -535,7 +574,7 @@ scan_status_t expert_combine(const expert_combine_args_t* args, void* stream)
                          range(a.weights, a.tokens * a.choices * ws)};
     if (any_overlap(outs, ins)) return SCAN_ERR_INVALID;
     if (a.tokens == 0) return SCAN_OK;
-    const Moves m{a.places, (uint32_t)a.tokens, (uint32_t)a.rows, a.choices, a.channels, nullptr};
+    const Moves m{a.places, (uint32_t)a.tokens, (uint32_t)a.rows, a.choices, a.channels};
     return with_dtype(a.dtype, [&](auto e) -> scan_status_t {
         using T = decltype(e);
         scan_status_t launch = SCAN_OK;
@@ -569,27 +608,37 @@ scan_status_t expert_combine_grad(const expert_combine_grad_args_t* args, void* 
         return SCAN_ERR_INVALID;
     if (a.dweights && !valid_rows(a.dtype, a.rows, a.channels, {a.y, a.y_stride})) return SCAN_ERR_INVALID;
     const size_t es = dtype_size(a.dtype), ws = dtype_size(a.weight_dtype);
-    if (!aligned(a.weights, ws) || !aligned(a.used, 4) || !aligned(a.dweights, 4)) return SCAN_ERR_INVALID;
+    if (!aligned(a.weights, ws) || !valid_clear(a.used, a.source, a.source_rows) || !aligned(a.dweights, 4)) return SCAN_ERR_INVALID;
     const Range outs[] = {range(a.dy, a.rows, a.dy_stride, a.channels, es), range(a.dweights, a.tokens * a.choices * 4)};
     const Range ins[] = {range(a.dout, a.tokens, a.dout_stride, a.channels, es), range(a.dweights ? a.y : nullptr, a.rows, a.y_stride, a.channels, es),
-                         range(a.places, a.tokens * a.choices * 4), range(a.weights, a.tokens * a.choices * ws), range(a.used, 4)};
+                         range(a.places, a.tokens * a.choices * 4), range(a.weights, a.tokens * a.choices * ws), range(a.used, 4),
+                         range(a.source, a.source_rows * 4)};
     if (any_overlap(outs, ins)) return SCAN_ERR_INVALID;
-    const uint64_t wgs = a.tokens + (a.used ? kClearStep : 0);
-    if (wgs == 0) return SCAN_OK;
-    const Moves m{a.places, (uint32_t)a.tokens, (uint32_t)a.rows, a.choices, a.channels, a.used};
+    const bool clears = (a.clear || a.used) && a.rows;
+    if (a.tokens == 0 && !clears) return SCAN_OK;
+    const Moves m{a.places, (uint32_t)a.tokens, (uint32_t)a.rows, a.choices, a.channels};
+    const Clear clear{a.clear ? nullptr : a.used, a.source, (uint32_t)a.source_rows};
+    const hipStream_t s = static_cast<hipStream_t>(stream);
     return with_dtype(a.dtype, [&](auto e) -> scan_status_t {
         using T = decltype(e);
+        scan_status_t launch = SCAN_OK;
         const Array y{a.dweights ? a.y : nullptr, a.y_stride};
         with_pack<T>(a.channels, {{a.dout, a.dout_stride}, y, {a.dy, a.dy_stride}}, [&](auto n) {
             constexpr int V = decltype(n)::value;
+            T* dy = static_cast<T*>(a.dy);
+            if (clears && !clear_rows<T, V>(m, clear, dy, a.dy_stride, s)) {
+                launch = SCAN_ERR_INVALID;
+                return;
+            }
+            if (a.tokens == 0) return;
             with_weights<T>(a.weight_dtype, [&](auto we) {
                 using W = decltype(we);
-                hipLaunchKernelGGL((combine_grad_kernel<T, W, V>), grid_of(wgs), dim3(256), 0, static_cast<hipStream_t>(stream), m,
-                                   static_cast<const W*>(a.weights), static_cast<const T*>(a.dout), a.dout_stride,
-                                   static_cast<const T*>(a.y), a.y_stride, static_cast<T*>(a.dy), a.dy_stride, a.dweights);
+                hipLaunchKernelGGL((combine_grad_kernel<T, W, V>), grid_of(a.tokens), dim3(256), 0, s, m, static_cast<const W*>(a.weights),
+                                   static_cast<const T*>(a.dout), a.dout_stride, static_cast<const T*>(a.y), a.y_stride, dy, a.dy_stride,
+                                   a.dweights);
             });
         });
-        return launched();
+        return launch == SCAN_OK ? launched() : launch;
     });
 }
 

@@ -21,8 +21,9 @@ from .sequence import (_DTYPE, _I, _I64, _P, _U32, _U64, _check, _enqueue, _lib,
 
 
 class _DispatchArgs(ctypes.Structure):
-    _fields_ = [("dtype", _I), ("reserved", _I), ("tokens", _U64), ("rows", _U64), ("choices", _U32), ("channels", _U32),
-                ("places", _P), ("used", _P), ("x", _P), ("x_stride", _I64), ("out", _P), ("out_stride", _I64)]
+    _fields_ = [("dtype", _I), ("clear", _I), ("tokens", _U64), ("rows", _U64), ("choices", _U32), ("channels", _U32),
+                ("places", _P), ("used", _P), ("x", _P), ("x_stride", _I64), ("out", _P), ("out_stride", _I64), ("source", _P),
+                ("source_rows", _U64)]
 
 
 class _CombineArgs(ctypes.Structure):
@@ -33,7 +34,7 @@ class _CombineArgs(ctypes.Structure):
 class _CombineGradArgs(ctypes.Structure):
     _fields_ = [("dtype", _I), ("weight_dtype", _I), ("tokens", _U64), ("rows", _U64), ("choices", _U32), ("channels", _U32),
                 ("places", _P), ("used", _P), ("weights", _P), ("dout", _P), ("dout_stride", _I64), ("y", _P), ("y_stride", _I64),
-                ("dy", _P), ("dy_stride", _I64), ("dweights", _P)]
+                ("dy", _P), ("dy_stride", _I64), ("dweights", _P), ("source", _P), ("source_rows", _U64), ("clear", _I), ("reserved", _I)]
 
 
 _register({
@@ -88,15 +89,24 @@ def expert_split(experts: torch.Tensor, n_experts: int, stream=None) -> ExpertPl
 
 
 def _plan(plan: ExpertPlan, device: int):
-    """(tokens, choices, address of places, address of the number of rows with an expert)"""
+    """(tokens, choices, address of places)"""
     places, offsets = plan.places, plan.offsets
     if places.dim() != 2 or not 1 <= places.shape[1] <= 256:
         raise ValueError("plan.places must be (n, k) with k in 1 .. 256")
     if offsets.dim() != 1 or offsets.shape[0] < 2:
         raise ValueError("plan.offsets must be (E + 1,)")
     at = _plain(places, "plan.places", places.shape, torch.int32, device)
-    ends = _plain(offsets, "plan.offsets", offsets.shape, torch.int32, device)
-    return places.shape[0], places.shape[1], at, ends + 4 * (offsets.shape[0] - 1)
+    _plain(offsets, "plan.offsets", offsets.shape, torch.int32, device)
+    return places.shape[0], places.shape[1], at
+
+
+def _source(plan: ExpertPlan, device: int):
+    """(address, values) of a plan's source, which only says where nothing need be cleared: (None, 0) for one that is not as
+    expert_split makes it."""
+    s = plan.source
+    if not isinstance(s, torch.Tensor) or s.dtype != torch.int32 or s.get_device() != device or not s.is_contiguous():
+        return None, 0
+    return s.data_ptr(), s.numel()
 
 
 def _matrix(t: torch.Tensor, name: str, rows=None):
@@ -117,15 +127,16 @@ def _result(out, shape, like: torch.Tensor, name: str):
 def expert_dispatch(x: torch.Tensor, plan: ExpertPlan, out: Optional[torch.Tensor] = None, stream=None):
     """The tokens' rows in the experts' order: out[plan.places[t, j]] = x[t].
 
-    x: (n, D), any row stride.  A new out is (n k, D), its rows that have no expert zero; in a given one (rows, D) they
-    are left as they were, and places outside it are skipped."""
+    x: (n, D), any row stride.  A new out is (n k, D), its rows that no place leads to zero; in a given one (rows, D) they
+    are left as they were, and places outside it are skipped.  Places may be taken out of a plan (-1) after the split."""
     d = _matrix(x, "x", plan.places.shape[0])
-    n, k, places, used = _plan(plan, x.get_device())
+    n, k, places = _plan(plan, x.get_device())
+    source = _source(plan, x.get_device()) if out is None else (None, 0)
 
     def call(handle):
         y, to, stride = _result(out, (n * k, d), x, "out") if out is None else _result(out, (out.shape[0], d), x, "out")
-        a = _DispatchArgs(_DTYPE[x.dtype], 0, n, y.shape[0], k, d, places, used if out is None else None, x.data_ptr(), _rows(x, "x"),
-                          to, stride)
+        a = _DispatchArgs(_DTYPE[x.dtype], 1 if out is None else 0, n, y.shape[0], k, d, places, None, x.data_ptr(), _rows(x, "x"), to,
+                          stride, *source)
         _check(_lib().expert_dispatch(ctypes.byref(a), handle), "expert_dispatch")
         return y
 
@@ -134,7 +145,7 @@ def expert_dispatch(x: torch.Tensor, plan: ExpertPlan, out: Optional[torch.Tenso
 
 def _combine(y, plan, weights, out, stream, what, name):
     d = _matrix(y, name)
-    n, k, places, _ = _plan(plan, y.get_device())
+    n, k, places = _plan(plan, y.get_device())
     w = _weights(weights, plan, y)
 
     def call(handle):
@@ -175,9 +186,10 @@ def expert_combine_grad(dout: torch.Tensor, y: torch.Tensor, plan: ExpertPlan, w
     """Gradients of ``expert_combine`` (its arguments) for dout (n, D): dy[plan.places[t, j]] = weights[t, j] dout[t], and
     dweights[t, j] = the sum over the channels of dout[t] y[plan.places[t, j]].
 
-    dy may be given to write into; its rows that have no expert are left as they were then, and are zero otherwise."""
+    dy may be given to write into; its rows that no place leads to are left as they were then, and are zero otherwise."""
     d = _matrix(dout, "dout", plan.places.shape[0])
-    n, k, places, used = _plan(plan, dout.get_device())
+    n, k, places = _plan(plan, dout.get_device())
+    source = _source(plan, dout.get_device()) if dy is None else (None, 0)
     _matrix(y, "y")
     y_at, y_stride = _like(y, "y", torch.Size((y.shape[0], d)), dout.dtype, dout.get_device(), d)
     w = _weights(weights, plan, dout)
@@ -186,8 +198,8 @@ def expert_combine_grad(dout: torch.Tensor, y: torch.Tensor, plan: ExpertPlan, w
         o, to, stride = _result(dy, (y.shape[0], d), dout, "dy")
         dw = None if weights is None else torch.empty(plan.places.shape, dtype=torch.float32, device=dout.device)
         a = _CombineGradArgs(_DTYPE[dout.dtype], 0 if weights is None else _DTYPE[weights.dtype], n, y.shape[0], k, d, places,
-                             used if dy is None else None, w, dout.data_ptr(), _rows(dout, "dout"), y_at, y_stride, to, stride,
-                             None if dw is None else dw.data_ptr())
+                             None, w, dout.data_ptr(), _rows(dout, "dout"), y_at, y_stride, to, stride,
+                             None if dw is None else dw.data_ptr(), *source, 1 if dy is None else 0)
         _check(_lib().expert_combine_grad(ctypes.byref(a), handle), "expert_combine_grad")
         return CombineGrads(o, dw)
 

@@ -357,13 +357,15 @@ size_t expert_split_workspace(size_t n, uint32_t n_experts);
 
 /*
  * expert_dispatch: out[places[t][j]] = x[t] for every token t and choice j; places outside 0 .. rows - 1 are
- * skipped (here and below), a row that two choices lead to holds parts of either's.  used (device memory, may be NULL: offsets +
- * n_experts): the rows from *used on are set to zero; other rows that no choice leads to are left as they were.
+ * skipped (here and below), a row that two choices lead to holds parts of either's.  Rows that no choice leads to are
+ * left as they were, but set to zero from *used on (device memory, may be NULL: none) or, with clear != 0, everywhere (used is
+ * not looked at then).  source (source_rows values, may be NULL) is the split's and saves writing: rows r with
+ * places[source[r]] == r need not be cleared; it may hold anything.
  * x: tokens x channels, out: rows x channels; choices <= 256, tokens * choices < 2^31.  The gradient of x is
  * expert_combine without weights.
  */
 typedef struct {
-    int32_t dtype, reserved;
+    int32_t dtype, clear;
     uint64_t tokens, rows;
     uint32_t choices, channels;
     const int32_t* places;
@@ -372,6 +374,8 @@ typedef struct {
     int64_t x_stride;
     void* out;
     int64_t out_stride;
+    const int32_t* source;
+    uint64_t source_rows;
 } expert_dispatch_args_t;
 scan_status_t expert_dispatch(const expert_dispatch_args_t* args, void* stream);
 
@@ -393,7 +397,7 @@ typedef struct {
 scan_status_t expert_combine(const expert_combine_args_t* args, void* stream);
 
 /*
- * Gradients of expert_combine: dy[places[t][j]] = weights[t][j] * dout[t] (used as in expert_dispatch), and
+ * Gradients of expert_combine: dy[places[t][j]] = weights[t][j] * dout[t] (used, clear and source as in expert_dispatch), and
  * dweights[t][j] (tokens x choices float32; may be NULL, y may be NULL then) = the sum over the channels of dout[t] *
  * y[places[t][j]], 0 where there is no place.
  */
@@ -411,6 +415,9 @@ typedef struct {
     void* dy;
     int64_t dy_stride;
     float* dweights;
+    const int32_t* source;
+    uint64_t source_rows;
+    int32_t clear, reserved;
 } expert_combine_grad_args_t;
 scan_status_t expert_combine_grad(const expert_combine_grad_args_t* args, void* stream);
 
