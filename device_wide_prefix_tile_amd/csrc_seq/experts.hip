@@ -259,10 +259,10 @@ struct Clear {
     uint32_t source_rows;
 };
 
-// A workgroup looks at kClearRows rows and sets 64 V kClearParts channels of them to zero, a wavefront every fourth row.  It runs in front of the move, so a
-// row that is cleared although a place leads to it (a source of another origin) is written afterwards.  A map of the rows
-// that are led to would need memory; this needs the launch (2.4 us for 512 rows, 5.3 for 65536), and writes no more than the rows without a choice
-// where source is the split's.
+// A workgroup looks at kClearRows rows and sets 64 V kClearParts channels of them to zero, a wavefront every fourth row.
+// It runs in front of the move, so a row that is cleared although a place leads to it (a source of another origin) is
+// written afterwards.  A map of the rows that are led to would need memory; this needs the launch (2.4 us for 512 rows,
+// 5.3 for 65536), and writes no more than the rows without a choice where source is the split's.
 constexpr int kClearRows = 16;
 constexpr int kClearParts = 8;
 template <typename T, int V>
@@ -451,7 +451,8 @@ scan_status_t check_moves(int dtype, uint64_t tokens, uint64_t rows, uint32_t ch
 {
     if (!valid_dtype(dtype)) return SCAN_ERR_UNSUPPORTED;
     if (choices < 1 || choices > kMaxChoices || channels < 1 || channels > kMaxChannels) return SCAN_ERR_INVALID;
-    if (tokens >= ((uint64_t)1 << 31) / choices || rows >= ((uint64_t)1 << 31)) return SCAN_ERR_INVALID;
+    constexpr uint64_t most = (uint64_t)1 << 31;
+    if (tokens >= most || tokens * choices >= most || rows >= most) return SCAN_ERR_INVALID;
     return (tokens == 0 || places) && aligned(places, 4) ? SCAN_OK : SCAN_ERR_INVALID;
 }
 
