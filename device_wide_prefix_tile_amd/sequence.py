@@ -9,7 +9,8 @@ on the stream that the call runs on, so a call can be captured into a graph.
 
 The gradients are functions of their own: nothing is recorded for autograd.  Where autograd is
 recording, a tensor that requires a gradient is refused rather than detached without a word; call
-under ``torch.no_grad()``, inside an ``autograd.Function``, or with ``tensor.detach()``.
+under ``torch.no_grad()``, inside an ``autograd.Function``, or with ``tensor.detach()``.  A dual
+tensor, whose tangent would be lost, is refused too.
 
 Layout: channels last.  Rows are (B, L, D) for B sequences of one length, or (rows, D) with
 ``seq_offsets`` (int32, S + 1 ascending) for sequences packed one behind the other.  A tensor of
@@ -21,6 +22,7 @@ import ctypes
 from typing import NamedTuple, Optional
 
 import torch
+import torch.autograd.forward_ad as _forward_ad
 
 from .binding import ScanError, _raw_stream, lib
 
@@ -173,11 +175,18 @@ def _on(x: torch.Tensor, name: str, t: torch.Tensor):
 _recording = torch.is_grad_enabled
 
 
+def _dual(t: torch.Tensor):
+    """Whether t has a tangent (asked within a level of forward-mode differentiation)."""
+    return _forward_ad.unpack_dual(t).tangent is not None
+
+
 def _no_graph(t: torch.Tensor, name: str):
-    """Refuses t if autograd would have to record what is done with it."""
+    """Refuses t if autograd would have to record what is done with it, or to carry its tangent on."""
     if t.requires_grad and _recording():
         raise ValueError("%s requires a gradient, which the sequence operators do not record: call them under torch.no_grad(), "
                          "or with %s.detach()" % (name, name))
+    if _forward_ad._current_level >= 0 and _dual(t):
+        raise ValueError("%s has a tangent, which the sequence operators do not carry on: unpack the dual tensor first" % name)
 
 
 def _refuse(t: torch.Tensor, name: str, shape, dtype):
@@ -223,7 +232,8 @@ def _plain(t: torch.Tensor, name: str, shape, dtype, device: int):
     """Address of t, a contiguous tensor of that shape, type and device (its index; -1: the host); None for None."""
     if t is None:
         return None
-    if t.shape != shape or t.dtype != dtype or t.get_device() != device or (t.requires_grad and _recording()):
+    if (t.shape != shape or t.dtype != dtype or t.get_device() != device or (t.requires_grad and _recording())
+            or (_forward_ad._current_level >= 0 and _dual(t))):
         _refuse(t, name, shape, dtype)
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
@@ -234,7 +244,8 @@ def _like(t: torch.Tensor, name: str, shape, dtype, device: int, width: int, inn
     """(address, row stride) of t, rows of `width` values in that shape, type and device; (None, 0) for None."""
     if t is None:
         return None, 0
-    if t.shape != shape or t.dtype != dtype or t.get_device() != device or (t.requires_grad and _recording()):
+    if (t.shape != shape or t.dtype != dtype or t.get_device() != device or (t.requires_grad and _recording())
+            or (_forward_ad._current_level >= 0 and _dual(t))):
         _refuse(t, name, shape, dtype)
     return t.data_ptr(), width if t.is_contiguous() else _rows(t, name, inner)
 
