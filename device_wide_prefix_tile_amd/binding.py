@@ -26,6 +26,7 @@ EXPORTS = ("scan_inclusive", "scan_exclusive", "segmented_scan", "compact", "sca
            "scan_set_spin_limit", "scan_set_multi_tile_mode", "scan_copy_probe", "csr_row_offsets",
            "radix_split", "scan_noalloc",
            # dwpt_seq.h, bound in sequence.py, experts.py and sampling.py
+           "seq_get_device_error", "seq_set_spin_limit",
            "embedding_lookup", "embedding_grad", "embedding_grad_workspace", "causal_conv1d", "causal_conv1d_grad",
            "causal_conv1d_grad_workspace", "causal_conv1d_step", "selective_scan", "selective_scan_workspace",
            "selective_scan_saved", "selective_scan_grad", "selective_scan_grad_workspace", "selective_scan_step",

@@ -23,6 +23,8 @@
 // Packed sequences are segments: a row that begins one starts from the initial state; a tile looks back
 // no further than to the tile in which its first row's sequence begins.  The gradient is the same
 // scan from the other end.
+#include <atomic>
+
 #include "seq_common.hpp"
 
 namespace dwpt_seq {
@@ -40,7 +42,9 @@ constexpr uint32_t kTileRows = kRows * kWaves;
 constexpr uint32_t kGroup = 8;
 constexpr uint32_t kChannelPad = 256;  // channels of a tile in the workspace and the saved states: a multiple of this
 constexpr uint32_t kEmptyStep = 32;    // workgroups per channel block that look for empty sequences
-constexpr uint32_t kMaxPolls = 1u << 22;  // some seconds; a wait that gives up yields NaN
+// Looks of a wait before it gives up, some seconds, yields NaN and sets the device's word.
+std::atomic<uint32_t> g_spin_limit{1u << 22};
+__device__ uint32_t g_gave_up;
 
 // The rows cut into tiles.  Sequences of one length are runs of `run` tiles each, the last of which may have
 // fewer rows; packed sequences are one run.  Tiles are numbered over all runs' first tiles, then all second ones, so
@@ -144,7 +148,8 @@ __global__ __launch_bounds__(256) void unset_kernel(uint32_t* counter, uint64_t*
 // The state (STEP 1; -1: the gradient, from behind) that reaches tile k of the lane's channel.  `first` is the tile in
 // which the sequence begins (ends), whose map needs no state.  maps, starts: the run's of that channel, `pitch` words apart.
 template <int STEP>
-__device__ __forceinline__ float carry(const uint64_t* maps, const uint32_t* starts, uint32_t pitch, uint32_t k, uint32_t first)
+__device__ __forceinline__ float carry(const uint64_t* maps, const uint32_t* starts, uint32_t pitch, uint32_t k, uint32_t first,
+                                       uint32_t spin_limit)
 {
     constexpr int N = kGroup - 1;
     // the tiles of k's group on the way to k: n of them, from `from` on
@@ -155,10 +160,10 @@ __device__ __forceinline__ float carry(const uint64_t* maps, const uint32_t* sta
     // starts[g]: the state before group g's first tile; backwards, the gradient behind its last one
     const uint32_t* start = starts + (uint64_t)g * pitch;
     const auto map = [&](int i) { return maps + (uint64_t)(from + (uint32_t)(i * STEP)) * pitch; };
-    uint64_t v[N];
+    uint64_t v[N] = {};
     uint32_t h0 = 0;
     bool all = false;
-    for (uint32_t polls = 0; !all && polls < kMaxPolls; ++polls) {
+    for (uint32_t polls = 0; !all && polls < spin_limit; ++polls) {
         if (polls) {
             // One load asks for all: lane i for the i-th map of the wavefront's first channel, one more for the start.
             const int lane = threadIdx.x & 63;
@@ -187,7 +192,9 @@ __device__ __forceinline__ float carry(const uint64_t* maps, const uint32_t* sta
             h = inside && i == 0 ? b : fmaf(a, h, b);
         }
     }
-    return all ? h : __builtin_nanf("");
+    if (all) return h;
+    __hip_atomic_store(&g_gave_up, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return __builtin_nanf("");
 }
 
 // ------------------------------------------------------------ the gates
@@ -400,7 +407,7 @@ struct Forward {
     int64_t y_stride;
     float *final_state, *saved;
     Space ws;
-    uint32_t blocks;  // of 64 V channels
+    uint32_t spin_limit, blocks;  // blocks: of 64 V channels
 };
 
 template <int V>
@@ -477,7 +484,7 @@ __device__ __forceinline__ void forward_tile(const Forward& p, ForwardShared<V>&
             uint64_t* maps = p.ws.maps + (uint64_t)t.r * p.cut.run * pitch + c0 + ch;
             uint32_t* starts = p.ws.starts + (uint64_t)t.r * p.cut.groups * pitch + c0 + ch;
             publish_map(maps + (uint64_t)t.k * pitch, am, hm);
-            const float h = PLAIN || t.first >= 0 ? carry<1>(maps, starts, pitch, t.k, (uint32_t)t.first) : 0.0f;
+            const float h = PLAIN || t.first >= 0 ? carry<1>(maps, starts, pitch, t.k, (uint32_t)t.first, p.spin_limit) : 0.0f;
             if ((t.k + 1) % kGroup == 0 && t.k + 1 < p.cut.run)
                 publish_state(starts + (uint64_t)((t.k + 1) / kGroup) * pitch, any ? hm : fmaf(am, h, hm));
             s.in[ch] = h;
@@ -574,7 +581,7 @@ struct Backward {
     int64_t dx_stride, ddecay_stride, dinput_stride;
     float* dinitial;
     Space ws;
-    uint32_t blocks;
+    uint32_t spin_limit, blocks;
 };
 
 // One row: from the state before it the factors of dh, and the state behind it.
@@ -675,7 +682,7 @@ __device__ __forceinline__ void backward_tile(const Backward& p, BackwardShared<
             uint64_t* maps = p.ws.maps + (uint64_t)t.r * p.cut.run * pitch + c0 + ch;
             uint32_t* starts = p.ws.starts + (uint64_t)t.r * p.cut.groups * pitch + c0 + ch;
             publish_map(maps + (uint64_t)t.k * pitch, am, em);
-            const float e = PLAIN || t.last >= 0 ? carry<-1>(maps, starts, pitch, t.k, (uint32_t)t.last) : 0.0f;
+            const float e = PLAIN || t.last >= 0 ? carry<-1>(maps, starts, pitch, t.k, (uint32_t)t.last, p.spin_limit) : 0.0f;
             if (t.k % kGroup == 0 && t.k > 0)
                 publish_state(starts + (uint64_t)(t.k / kGroup - 1) * pitch, any ? em : fmaf(am, e, em));
             s.in[ch] = e;
@@ -1010,7 +1017,7 @@ void with_channels(int v, F f)
 
 scan_status_t forward(const gated_scan_args_t& a, hipStream_t s)
 {
-    Forward p{cut_of(a), inputs_of(a), a.y, a.y_stride, a.final_state, a.saved, {}, 0};
+    Forward p{cut_of(a), inputs_of(a), a.y, a.y_stride, a.final_state, a.saved, {}, g_spin_limit, 0};
     p.ws = lay_out(p.cut, false, a.workspace);
     const Array arrays[] = {{a.x, a.x_stride}, {a.decay_gate, a.decay_stride}, {a.input_gate, a.input_stride}, {a.y, a.y_stride}};
     const int v = channels_per_lane(a.dtype, a.channels, arrays);
@@ -1039,7 +1046,7 @@ scan_status_t gradient(const gated_scan_grad_args_t& g, hipStream_t s)
 {
     const gated_scan_args_t& a = g.args;
     Backward p{cut_of(a), inputs_of(a), g.dy, g.dy_stride, g.dfinal_state, a.saved, g.dx, g.ddecay_gate, g.dinput_gate, g.dx_stride,
-               g.ddecay_stride, g.dinput_stride, g.dinitial_state, {}, 0};
+               g.ddecay_stride, g.dinput_stride, g.dinitial_state, {}, g_spin_limit, 0};
     p.ws = lay_out(p.cut, true, a.workspace);
     const Array arrays[] = {{a.x, a.x_stride}, {a.decay_gate, a.decay_stride}, {a.input_gate, a.input_stride}, {g.dy, g.dy_stride},
                             {g.dx, g.dx_stride}, {g.ddecay_gate, g.ddecay_stride}, {g.dinput_gate, g.dinput_stride}};
@@ -1081,6 +1088,19 @@ scan_status_t gradient(const gated_scan_grad_args_t& g, hipStream_t s)
 using namespace dwpt_seq;
 
 extern "C" {
+
+uint32_t seq_set_spin_limit(uint32_t polls) { return g_spin_limit.exchange(polls); }
+
+scan_status_t seq_get_device_error(void* stream)
+{
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    uint32_t gave_up = 0;
+    const uint32_t zero = 0;
+    if (hipStreamSynchronize(s) != hipSuccess) return SCAN_ERR_HIP;
+    if (hipMemcpyFromSymbol(&gave_up, HIP_SYMBOL(g_gave_up), 4) != hipSuccess) return SCAN_ERR_HIP;
+    if (!gave_up) return SCAN_OK;
+    return hipMemcpyToSymbol(HIP_SYMBOL(g_gave_up), &zero, 4) == hipSuccess ? SCAN_ERR_TIMEOUT : SCAN_ERR_HIP;
+}
 
 size_t gated_scan_workspace(const gated_scan_args_t* args)
 {

@@ -24,7 +24,7 @@ from typing import NamedTuple, Optional
 import torch
 import torch.autograd.forward_ad as _forward_ad
 
-from .binding import ScanError, _raw_stream, lib
+from .binding import ScanError, _raw_stream, _stream, lib
 
 _DTYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _ACT = {None: 0, "silu": 1}
@@ -105,6 +105,8 @@ SIGNATURES = {
     "selective_scan_grad": ([ctypes.POINTER(_ScanGradArgs), _P], _I),
     "selective_scan_grad_workspace": ([ctypes.POINTER(_ScanGradArgs)], _U64),
     "selective_scan_step": ([ctypes.POINTER(_ScanStepArgs), _P], _I),
+    "seq_get_device_error": ([_P], _I),
+    "seq_set_spin_limit": ([_U32], _U32),
     "gated_scan": ([ctypes.POINTER(_GatedArgs), _P], _I),
     "gated_scan_workspace": ([ctypes.POINTER(_GatedArgs)], _U64),
     "gated_scan_saved": ([ctypes.POINTER(_GatedArgs)], _U64),
@@ -294,6 +296,19 @@ def _optional_state(state, name: str, shape, dtype, x: torch.Tensor):
         state = torch.empty(shape, dtype=dtype, device=x.device)
         return state, state.data_ptr()
     return state, _plain(state, name, shape, dtype, x.get_device())
+
+
+# ---------------------------------------------------------------------- waits
+def seq_get_device_error(stream=None) -> int:
+    """Synchronises the stream (a torch stream, a handle, or None: the current one) and reads and clears the current
+    device's word: 5 (SCAN_ERR_TIMEOUT) if a workgroup of a sequence operator gave up waiting for another one since the last
+    check (the results of that call hold NaN then), else 0."""
+    return int(_lib().seq_get_device_error(_stream(stream)))
+
+
+def seq_set_spin_limit(polls: int) -> int:
+    """Looks after which such a wait gives up; returns the old value (2^22 at first, some seconds)."""
+    return int(_lib().seq_set_spin_limit(int(polls)))
 
 
 # ---------------------------------------------------------------------- embedding

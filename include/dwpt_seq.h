@@ -39,6 +39,9 @@
  *     with different workspaces may overlap in time.
  *   - No floating-point atomics: results repeat bit for bit (on one path, see
  *     above).
+ *   - Bounded waits: workgroups of the gated recurrence wait for one another.
+ *     A wait that gives up (after some seconds; see seq_set_spin_limit) yields
+ *     NaN from its row on, and seq_get_device_error reports it.
  *   - Outputs must not overlap inputs or one another (SCAN_ERR_INVALID),
  *     except where a state is updated in place.
  */
@@ -61,6 +64,15 @@ typedef enum {
     SEQ_ACT_NONE = 0,
     SEQ_ACT_SILU = 1 /* u / (1 + exp(-u)) */
 } seq_activation_t;
+
+/*
+ * Synchronises `stream`, then reads and clears the current device's word of the calls of this header:
+ * SCAN_ERR_TIMEOUT if a wait gave up since the last check (the results of that call hold NaN then), else SCAN_OK.
+ */
+scan_status_t seq_get_device_error(void* stream);
+
+/* Looks after which a wait gives up (process-wide, thread-safe; 0: at once).  Returns the old value; default 2^22. */
+uint32_t seq_set_spin_limit(uint32_t polls);
 
 /*
  * out[i] = scale * table[tokens[i]], i < n; a token outside 0 .. n_rows - 1
