@@ -44,28 +44,6 @@ SplitPlan make_plan(size_t n, uint32_t experts)
     return p;
 }
 
-// Exclusive prefix of `v` over the workgroup's first `n` threads (others pass 0); *total: the sum.
-__device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t* s_part, uint32_t& total)
-{
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    uint32_t incl = v;
-    for (int o = 1; o < 64; o <<= 1) {
-        const uint32_t t = __shfl_up(incl, o, 64);
-        if (lane >= o) incl += t;
-    }
-    if (lane == 63) s_part[w] = incl;
-    __syncthreads();
-    uint32_t before = 0, all = 0;
-#pragma unroll
-    for (int q = 0; q < kWaves; ++q) {
-        const uint32_t t = s_part[q];
-        before += q < w ? t : 0u;
-        all += t;
-    }
-    total = all;
-    return before + incl - v;
-}
-
 // Chunk blockIdx.x.  ONE: the only chunk, everything.  Otherwise places receives every choice's rank among its
 // chunk's choices of the same expert, counts[chunk] how many choices each expert has there.
 template <bool ONE>
@@ -116,7 +94,7 @@ __global__ __launch_bounds__(kBlock) void rank_kernel(const int32_t* __restrict_
     }
     if (ONE) {
         uint32_t total;
-        const uint32_t begin = block_prefix(sum, s_part, total);
+        const uint32_t begin = block_prefix<kWaves>(sum, s_part, total);
         if (threadIdx.x < p.experts) {
             for (int q = 0; q < kWaves; ++q) s_cnt[q * p.experts + threadIdx.x] += begin;
             offsets[threadIdx.x] = (int32_t)begin;
@@ -199,7 +177,7 @@ __global__ __launch_bounds__(kBlock) void place_kernel(const int32_t* __restrict
         }
     }
     uint32_t total;
-    const uint32_t begin = block_prefix(sum, s_part, total);
+    const uint32_t begin = block_prefix<kWaves>(sum, s_part, total);
     if (t < p.experts) {
         s_base[t] = begin + before;
         if (blockIdx.x == 0) offsets[t] = (int32_t)begin;
@@ -416,17 +394,6 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(Moves m, const W* __r
 }
 
 // ------------------------------------------------------------ host side
-struct Array {
-    const void* p;
-    int64_t stride;
-};
-
-bool valid_rows(int dtype, uint64_t rows, uint32_t width, const Array& a)
-{
-    if (rows == 0) return true;
-    return a.p && aligned(a.p, dtype_size(dtype)) && a.stride >= (int64_t)width && a.stride <= ((int64_t)1 << 31);
-}
-
 // Calls f with the elements per access as an integral constant: the most of 16 bytes, two elements and one element
 // that every row can be cut into.  Two / one: combine of 1999 x 2 rows of 1002 float32 7.5 / 11.8 us, of 16000 x 4 of 590
 // bfloat16 33 / 55 (with eight rows ahead).

@@ -41,7 +41,7 @@ constexpr uint32_t kTileRows = kRows * kWaves;
 // 16384 x 2048 float16 96 / 80 / 91 / 92 us, of 8 x 2048 x 4096 bfloat16 122 / 123 / 166 / 170.
 constexpr uint32_t kGroup = 8;
 constexpr uint32_t kChannelPad = 256;  // channels of a tile in the workspace and the saved states: a multiple of this
-constexpr uint32_t kEmptyStep = 32;    // workgroups per channel block that look for empty sequences
+constexpr uint32_t kEmptyStep = 32;    // workgroups that look for empty sequences, in all
 // Looks of a wait before it gives up, some seconds, yields NaN and sets the device's word.
 std::atomic<uint32_t> g_spin_limit{1u << 22};
 __device__ uint32_t g_gave_up;
@@ -938,17 +938,6 @@ __global__ __launch_bounds__(256) void step_kernel(Inputs in, uint32_t rows, uin
 }
 
 // ------------------------------------------------------------ host side
-struct Array {
-    const void* p;
-    int64_t stride;
-};
-
-bool valid_rows(int dtype, uint64_t rows, uint32_t width, const Array& a)
-{
-    if (rows == 0) return true;
-    return a.p && aligned(a.p, dtype_size(dtype)) && a.stride >= (int64_t)width && a.stride <= ((int64_t)1 << 31);
-}
-
 // The most channels per lane, of 4, 2 and 1, that every row can be cut into.  Forward with 4 / 2 / 1: 8 x 2048 x 4096 bfloat16
 // 123 / 130 / 214 us, 2048 x 2048 18 / 20 / 25, 16384 x 2048 float16 80 / 78 / 114; float32 rows fill 8 bytes a lane with 2, which
 // are the most there: 8 x 2048 x 4096 191 / 186 / 237, 8 x 2048 x 1024 65 / 62 / 70, 16 x 1024 x 2048 108 / 106 / 126.  The gradient

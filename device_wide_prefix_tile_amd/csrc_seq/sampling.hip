@@ -192,38 +192,17 @@ __device__ __forceinline__ double wave_sum(double v)
     return add_from<0x143, 0xC>(v);  // row_bcast:31 into rows 2 and 3
 }
 
-// Exclusive prefix over the threads, and the sum, in a fixed order.  part: kWaves values in LDS.
-template <typename N>
-__device__ __forceinline__ N block_prefix(N v, N* part, N& total)
-{
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    N incl = v;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const N t = __shfl_up(incl, o, 64);
-        if (lane >= o) incl += t;
-    }
-    const N excl = __shfl_up(incl, 1, 64);
-    __syncthreads();
-    if (lane == 63) part[w] = incl;
-    __syncthreads();
-    N before = 0, all = 0;
-#pragma unroll
-    for (int q = 0; q < kWaves; ++q) {
-        before = q < w ? before + part[q] : before;
-        all += part[q];
-    }
-    total = all;
-    return lane ? before + excl : before;
-}
+// Exclusive prefix over the threads, and the sum, in a fixed order.
 __device__ __forceinline__ uint64_t block_prefix(uint64_t v, Shared& s, uint64_t& total)
 {
-    unsigned long long all;
-    const uint64_t before = block_prefix<unsigned long long>(v, reinterpret_cast<unsigned long long*>(s.part), all);
-    total = all;
-    return before;
+    __syncthreads();
+    return dwpt_seq::block_prefix<kWaves>(v, s.part, total);
 }
-__device__ __forceinline__ double block_prefix(double v, Shared& s, double& total) { return block_prefix<double>(v, s.dpart, total); }
+__device__ __forceinline__ double block_prefix(double v, Shared& s, double& total)
+{
+    __syncthreads();
+    return dwpt_seq::block_prefix<kWaves>(v, s.dpart, total);
+}
 
 // ------------------------------------------------------------ weights
 // 2^t for t <= 0 in 64 bits.  With n the integer next to t and f = t - n (exact), 2^f = 1 + f q(f): q of degree 8 takes the

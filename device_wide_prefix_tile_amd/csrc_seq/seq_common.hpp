@@ -118,6 +118,31 @@ __device__ __forceinline__ void wave_sync()
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// Exclusive prefix of v over the WAVES wavefronts of a workgroup, and the sum, in an order that depends on the threads
+// alone.  part: WAVES values in LDS that nothing else reads or writes until the next barrier behind.
+template <int WAVES, typename N>
+__device__ __forceinline__ N block_prefix(N v, N* part, N& total)
+{
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    N incl = v;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const N t = __shfl_up(incl, o, 64);
+        if (lane >= o) incl += t;
+    }
+    const N excl = __shfl_up(incl, 1, 64);
+    if (lane == 63) part[w] = incl;
+    __syncthreads();
+    N before = 0, all = 0;
+#pragma unroll
+    for (int q = 0; q < WAVES; ++q) {
+        before = q < w ? before + part[q] : before;
+        all += part[q];
+    }
+    total = all;
+    return lane ? before + excl : before;
+}
+
 // A launch's workgroups are numbered over two dimensions of the grid, kGridWidth in a row: HIP takes
 // less than 2^32 work items along one.  The last row may hold numbers behind the last workgroup.
 constexpr uint32_t kGridWidth = 1u << 22;
@@ -167,6 +192,17 @@ bool any_overlap(const Range (&out)[NO], const Range (&in)[NI])
             if (overlap(out[i], out[j])) return true;
     }
     return false;
+}
+
+// Rows at p, `stride` elements apart.
+struct Array {
+    const void* p;
+    int64_t stride;
+};
+inline bool valid_rows(int dtype, uint64_t rows, uint32_t width, const Array& a)
+{
+    if (rows == 0) return true;
+    return a.p && aligned(a.p, dtype_size(dtype)) && a.stride >= (int64_t)width && a.stride <= ((int64_t)1 << 31);
 }
 
 // The grid of `workgroups` (of 256 lanes or fewer) for workgroup(); more of them than kMostInGrid
