@@ -32,13 +32,13 @@ namespace {
 
 constexpr uint32_t kMaxChannels = 1u << 20;
 // Rows of a wavefront (the forward pass saves the state before every such rows for the gradient) and wavefronts of a
-// workgroup.  4 / 8 wavefronts: forward of 8 x 2048 x 4096 bfloat16 136 / 123 us, its gradient 262 / 213, forward of
-// 16384 x 2048 float16 115 / 80.
+// workgroup.  4 / 8 wavefronts: forward of 8 x 2048 x 4096 bfloat16 135 / 125 us, its gradient 266 / 215, forward of
+// 16384 x 2048 float16 116 / 80.
 constexpr int kRows = 8;
 constexpr int kWaves = 8;
 constexpr uint32_t kTileRows = kRows * kWaves;
 // Tiles of a group.  Few make the chain of groups long, many make more maps to read and to wait for: 4 / 8 / 12 / 16 forward of
-// 16384 x 2048 float16 96 / 80 / 91 / 92 us, of 8 x 2048 x 4096 bfloat16 122 / 123 / 166 / 170.
+// 16384 x 2048 float16 96 / 80 / 91 / 91 us, of 8 x 2048 x 4096 bfloat16 124 / 125 / 164 / 170.
 constexpr uint32_t kGroup = 8;
 constexpr uint32_t kChannelPad = 256;  // channels of a tile in the workspace and the saved states: a multiple of this
 constexpr uint32_t kEmptyStep = 32;    // workgroups that look for empty sequences, in all
@@ -301,7 +301,7 @@ struct Walk {
         asm("" : "+s"(row));
     }
     // V columns from `at` bytes behind the row's start on.  Every value is used once, past the caches: forward of 8 x
-    // 2048 x 4096 bfloat16 130 -> 123 us, its gradient 219 -> 213, gradient of 8 x 2048 x 1024 float32 138 -> 120.
+    // 2048 x 4096 bfloat16 130 -> 125 us, its gradient 220 -> 215, gradient of 8 x 2048 x 1024 float32 139 -> 122.
     __device__ Pack<T, V> load(uint32_t at) const
     {
         return __builtin_bit_cast(Pack<T, V>, __builtin_nontemporal_load((const DWPT_GLOBAL R*)(row + at)));
@@ -416,7 +416,7 @@ struct ForwardShared {
     uint32_t head[kWaves], tile;
 };
 
-// 8 x 2048 x 4096 bfloat16: 123 us, 4.4 TB/s (float32 186 us, 5.8 TB/s); vector units busy 66%, 34 vector instructions per
+// 8 x 2048 x 4096 bfloat16: 125 us, 4.3 TB/s (float32 187 us, 5.7 TB/s); vector units busy 69%, 36 vector instructions per
 // element, 6 of them transcendental.  What is left is waiting: a round trip through memory takes some 5 us while the
 // card streams, and a tile makes two between its loads and its results (an earlier version
 // of 129 us took 101 without them, and without their results).  One prompt of 16384 x 2048: 80 us, of which the chain of 32 groups sets most.
@@ -771,7 +771,7 @@ __global__ __launch_bounds__(kWaves * 64) void backward_kernel(Backward p)
 // With enough runs and channels to fill the chip a workgroup walks through its run's tiles one after another, from the
 // last to the first, and nothing passes through memory between tiles: every wavefront composes all wavefronts' maps of
 // a tile from LDS, which takes turns between two halves so that one barrier per tile is enough.  The next tile's rows
-// are on their way while this one's are finished.  (8 x 2048 x 4096 bfloat16: 213 us, 266 with tiles that wait for one another.
+// are on their way while this one's are finished.  (8 x 2048 x 4096 bfloat16: 215 us, 270 with tiles that wait for one another.
 // Forwards the same gained nothing, 125 against 122: its tiles wait less, two workgroups to a compute unit.)
 template <typename T, int V>
 __global__ __launch_bounds__(kWaves * 64) void backward_run_kernel(Backward p)
@@ -939,9 +939,9 @@ __global__ __launch_bounds__(256) void step_kernel(Inputs in, uint32_t rows, uin
 
 // ------------------------------------------------------------ host side
 // The most channels per lane, of 4, 2 and 1, that every row can be cut into.  Forward with 4 / 2 / 1: 8 x 2048 x 4096 bfloat16
-// 123 / 130 / 214 us, 2048 x 2048 18 / 20 / 25, 16384 x 2048 float16 80 / 78 / 114; float32 rows fill 8 bytes a lane with 2, which
-// are the most there: 8 x 2048 x 4096 191 / 186 / 237, 8 x 2048 x 1024 65 / 62 / 70, 16 x 1024 x 2048 108 / 106 / 126.  The gradient
-// takes 2 at most: 4 do not fit the registers.
+// 125 / 133 / 215 us, 2048 x 2048 19 / 20 / 25, 16384 x 2048 float16 80 / 79 / 113; float32 rows fill 8 bytes a lane with 2, which
+// are the most there: 8 x 2048 x 4096 187 / 237, 8 x 2048 x 1024 61 / 70, 16 x 1024 x 2048 105 / 125 (4, in an earlier version: 2 to
+// 5% slower than 2).  The gradient takes 2 at most: 4 do not fit the registers.
 template <size_t N>
 int channels_per_lane(int dtype, uint32_t channels, const Array (&arrays)[N])
 {
@@ -983,8 +983,9 @@ void unset(const Cut& c, const Space& w, hipStream_t s)
 }
 
 // Whether the gradient's workgroups walk through whole runs with this many channels per lane: from one workgroup per
-// compute unit on.  Tiles / runs: 512 workgroups, float32, 16 x 1024 x 2048 210 / 190 us, 8 x 2048 x 4096 398 / 408 to 425; 256 (8 x
-// 2048 x 4096 bfloat16, 2 channels) 266 / 213; 128 (8 x 2048 x 1024 float32) 119 / 134; 16 (one run of 16384 x 2048 float16) 142 / 1358.
+// compute unit on.  Tiles / runs: 512 workgroups, float32, 16 x 1024 x 2048 228 / 188 to 202 us, 8 x 2048 x 4096 402 / 394 to 406; 256
+// (8 x 2048 x 4096 bfloat16, 2 channels) 270 / 215; 128 (8 x 2048 x 1024 float32) 121 / 134; 16 (one run of 16384 x 2048 float16)
+// 146 / 1410.
 constexpr uint64_t kRunWorkgroups = 256;
 bool by_runs(const Cut& c, uint32_t channels, int per_lane)
 {
@@ -1046,7 +1047,7 @@ scan_status_t gradient(const gated_scan_grad_args_t& g, hipStream_t s)
         with_channels<2>(v, [&](auto n) {
             constexpr int V = decltype(n)::value;
             // Whole runs: two channels of float32 rows per lane would spill registers; rows of 16 bits take one where two leave too few
-            // workgroups: 4 x 2048 x 4096 bfloat16 tiles / runs 139 / 119 us, 8 x 2048 x 2048 145 / 121.
+            // workgroups: 4 x 2048 x 4096 bfloat16 tiles / runs 143 / 123 us, 8 x 2048 x 2048 149 / 121 to 126.
             constexpr int RV = std::is_same<T, float>::value ? 1 : V;
             const int run_channels = by_runs(p.cut, a.channels, RV) ? RV : 1;
             const bool chain = p.cut.run > 1, runs = by_runs(p.cut, a.channels, run_channels);

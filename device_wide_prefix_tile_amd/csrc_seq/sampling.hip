@@ -2,7 +2,7 @@
 //
 // One workgroup per row, which it reads once for every pass over it: from the caches but for the first.  (Held in
 // registers, 64 of them for 128000 logits of 16 bits, every pass is unrolled over all pieces, and the instructions
-// come from memory instead: 256 x 128000 top-k 56 us against 36.)  With w[i] = exp((logit[i] - max) / temperature), the
+// come from memory instead: 256 x 128000 top-k 56 us against 36 in an earlier version.)  With w[i] = exp((logit[i] - max) / temperature), the
 // tokens by falling logit (equal ones by ascending index) have a first part that top-k, top-p and min-p leave; the
 // sampled token is the first kept one in the order of the indices up to which the kept weights exceed uniform
 // times their sum: a scan of the row, of which only the path to one element is needed.
@@ -18,10 +18,10 @@
 // top-p leaves out are only added up.
 //
 // Weights and their sums are held in 64 bits: of 2^17 kept tokens each has some 2^-17 of the sum, and an error of e in
-// the running sum moves a row's token with a probability of some 2^17 e.  (32 bits in the weights or in the partial sums, one
-// alone as much as both, gave another token than the definition in 1 of 800 rows of 131072.)  Where LDS atomics add weights
-// up, they are integers, so that the order does not matter: rounded multiples of 2^-63 n, of which n fit 64 bits.  All other
-// sums are of fixed order.
+// the running sum moves a row's token with a probability of some 2^17 e.  (With 32 bits in the weights and a wavefront's
+// sums, 1 of 700 to 800 rows of 131072 had another token than the definition; with the weights in 64 bits and the sums in
+// 32, emulated on the host, 2 of 4096.)  Where LDS atomics add weights up, they are integers, so that the order does not
+// matter: rounded multiples of 2^-63 n, of which n fit 64 bits.  All other sums are of fixed order.
 #include <cfloat>
 #include <cmath>
 
@@ -36,8 +36,8 @@ constexpr int kWaves = kBlock / 64;
 constexpr int kBins = 2 * kBlock;
 constexpr float kPerOctave = 32.0f;  // the last bin holds weights below 2^-64, which are 0 as multiples of 2^-44
 constexpr uint32_t kList = 4096;     // logits of the bin with the border that are kept in LDS; more are looked up in the row
-// Of them, every one is compared with every other one, up to this many.  0 / 64 / 512: 300 rows of 1000 float32 logits 36 / 28 /
-// 28 us, 64 of 50001 64 / 57 / 65, 256 of 128000 bfloat16 with top-p 91 / 91 / 126.
+// Of them, every one is compared with every other one, up to this many.  0 / 64 / 512: 300 rows of 1000 float32 logits 37 / 30 /
+// 31 us, 64 of 50001 80 / 72 / 83, 256 of 128000 bfloat16 with top-p 137 / 138 / 169.
 constexpr uint32_t kRanked = 64;
 constexpr int kMostSums = (kMaxTokens / 4 + 1 + kBlock - 1) / kBlock * kWaves;
 
@@ -50,8 +50,8 @@ struct Settings {
 
 constexpr uint32_t kSorted = 2 * kBlock;  // logits that are sorted in LDS
 // Largest top-k that is sorted: the bound from 1024 threads' largest logits leaves 0.6% of a row for 512 of them, 3% for
-// 1000.  256 rows of 128000 bfloat16 logits, sorted / by counts: top-k 50 38 / 109 us, 400 51 / 122, 700 63 / 128, 1000
-// (more than can be sorted, then counted) 155 / 133.
+// 1000.  256 rows of 128000 bfloat16 logits, sorted / by counts: top-k 50 38 / 112 us, 400 52 / 142, 700 64 / 154, 1000
+// (more than can be sorted, then counted) 184 / 162.
 constexpr int64_t kMostSorted = kBlock / 4 * 3;
 
 struct Shared {
@@ -592,9 +592,10 @@ __device__ __forceinline__ bool sample_sorted(const P& pieces, const Scale& scal
 }
 
 // ------------------------------------------------------------ the kernel
-// 512 rows of 131072 bfloat16 logits without a cut 62 us: HBM is read once (134 MB, 20 us), the second pass comes from the
-// caches; vector units busy 66%.  256 x 128000 with settings of their own 121 us: the longest row's, which takes five
-// passes (counts, their border, weights, their border, sums).
+// 512 rows of 131072 bfloat16 logits without a cut 95 us (68 with weights and partial sums in 32 bits, which gave wrong
+// tokens): HBM is read once (134 MB, 20 us), the second pass comes from the caches; vector units busy 75%, 35 vector
+// instructions per logit, of which a weight in 64 bits and its sum take some 20.  256 x 128000 with settings of their own 154 us:
+// the longest row's, which takes five passes (counts, their border, weights, their border, sums).
 template <typename T>
 __global__ __launch_bounds__(kBlock) void sample_kernel(Settings set, uint32_t rows, uint32_t n, const T* __restrict__ logits,
                                                         int64_t stride, void* __restrict__ tokens, int token_bytes)
